@@ -23,7 +23,7 @@ from .functional import (act_bwd, act_fwd, copy_bytes, swish_bwd, swish_bwd_grou
                          swish_fwd_grouped)
 from .module import ActFn, MemoryEfficientActivation, MemoryEfficientSwish, SwishFn, swish
 from ._lib import MeswishError
-from . import dense
+from . import dense, ffn, norm
 
 __all__ = [
     "swish_fwd", "swish_bwd", "swish_fwd_grouped", "swish_bwd_grouped", "copy_bytes",

@@ -1,5 +1,6 @@
 """ctypes loader for libmeswish.so (the C ABI declared in include/meswish.h,
-include/dense_bn.h and include/fft_conv.h).
+include/dense_bn.h, include/fft_conv.h, include/layer_norm.h and
+include/gated_ffn.h).
 
 Argument marshalling only: every element of every pass is computed by the
 HIP kernels inside the library.  There is no CPU fallback -- if the library
@@ -27,6 +28,9 @@ EXPORTED = ("swish_fwd", "swish_bwd", "swish_fwd_grouped", "swish_bwd_grouped",
             "dense_bn_relu_bwd_noalloc",
             "fftconv_buffer_bytes", "fftconv_fprop", "fftconv_bprop", "fftconv_accgrad",
             "fftconv_r2c", "fftconv_c2r", "fftconv_cmul")
+# The transformer feed-forward operators (include/layer_norm.h, include/gated_ffn.h).
+BLOCK_EXPORTED = ("layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
+                  "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn_workspace_bytes")
 DENSE_MAX_SOURCES = 64
 DENSE_STATIC_WORKSPACE_BYTES = 4 << 20
 
@@ -98,10 +102,25 @@ def _signatures() -> dict:
     return sig
 
 
+def _block_signatures() -> dict:
+    """Argument and result types of the feed-forward operators."""
+    vp, sz, f, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float, ctypes.c_int
+    return {
+        "layer_norm_fwd": ([vp, sz, vp, vp, sz, sz, f, vp, sz, vp, vp, i, i, vp], i),
+        "layer_norm_workspace_bytes": ([sz, sz], sz),
+        "layer_norm_bwd": ([vp, sz, vp, sz, vp, vp, vp, sz, sz, vp, sz, vp, vp, vp, sz, i, i, vp],
+                           i),
+        "gated_ffn_workspace_bytes": ([sz, sz, sz, i, i], sz),
+        "gated_ffn_fwd": ([i, f, vp, sz, vp, sz, vp, sz, sz, sz, sz, vp, sz, vp, sz, i, vp], i),
+        "gated_ffn_bwd": ([i, f, vp, sz, vp, sz, vp, sz, vp, sz, sz, sz, sz, vp, sz, vp, sz, vp,
+                           sz, vp, sz, vp, sz, i, vp], i),
+    }
+
+
 def _declare(lib: ctypes.CDLL, names=None) -> ctypes.CDLL:
     """Set argtypes/restype of ``names`` (every exported function by default);
     a missing symbol raises AttributeError."""
-    sig = _signatures()
+    sig = {**_signatures(), **_block_signatures()}
     for name in (sig if names is None else names):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = sig[name]

@@ -1,0 +1,167 @@
+// block_common.h -- what the layer-norm and gated feed-forward kernels
+// share: element types, 16-byte accesses at element alignment, and host
+// argument checks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "meswish.h"
+
+namespace meblock {
+
+struct bf16_t {
+    uint16_t bits;
+};
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// The same 16 bytes at any element alignment: gfx950's global accesses take
+// them (unaligned access mode), so odd row strides need no element path.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+__device__ __forceinline__ u32x4 load16(const void* p) { return *static_cast<const u32x4_any*>(p); }
+__device__ __forceinline__ void store16(void* p, u32x4 v) { *static_cast<u32x4_any*>(p) = v; }
+
+typedef __bf16 hw_bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two binary32 values rounded to nearest even, as two bf16 (low half first).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    hw_bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+template <typename T> struct Elem;
+
+template <> struct Elem<float> {
+    static constexpr int kPerVec = 4;
+    __device__ static float get(float v) { return v; }
+    __device__ static float put(float v) { return v; }
+    __device__ static void unpack(u32x4 v, float* f)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // A copy: the bit cast of a vector's element itself reads
+            // element 0 whatever i is.
+            const uint32_t bits = v[i];
+            f[i] = __builtin_bit_cast(float, bits);
+        }
+    }
+    __device__ static u32x4 pack(const float* f)
+    {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __builtin_bit_cast(uint32_t, f[i]);
+        return v;
+    }
+};
+
+template <> struct Elem<bf16_t> {
+    static constexpr int kPerVec = 8;
+    __device__ static float get(bf16_t v) { return __builtin_bit_cast(float, (uint32_t)v.bits << 16); }
+    __device__ static bf16_t put(float v)
+    {
+        bf16_t r;
+        r.bits = (uint16_t)(pack_bf16(v, 0.0f) & 0xffffu);
+        return r;
+    }
+    __device__ static void unpack(u32x4 v, float* f)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __builtin_bit_cast(float, v[i] << 16);
+            f[2 * i + 1] = __builtin_bit_cast(float, v[i] & 0xffff0000u);
+        }
+    }
+    __device__ static u32x4 pack(const float* f)
+    {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+        return v;
+    }
+};
+
+// Elements e0 .. e0 + kPerVec - 1 of a row of n, as one packed vector; those
+// past the end are zero and are not read.
+template <typename T>
+__device__ __forceinline__ u32x4 load_chunk(const T* row, int e0, int n)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    if (e0 + E <= n)
+        return load16(row + e0);
+    float f[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        f[j] = e0 + j < n ? Elem<T>::get(row[e0 + j]) : 0.0f;
+    return Elem<T>::pack(f);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* row, int e0, int n, const float* f)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    if (e0 + E <= n) {
+        store16(row + e0, Elem<T>::pack(f));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (e0 + j < n)
+            row[e0 + j] = Elem<T>::put(f[j]);
+}
+
+// ---------------------------------------------------------------------------
+// Host checks.
+// ---------------------------------------------------------------------------
+
+inline size_t elem_size(int dtype) { return dtype == MESWISH_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == MESWISH_F32 || dtype == MESWISH_BF16; }
+inline bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
+
+// A matrix in memory: `rows` rows of `row_bytes` bytes, `ld_bytes` apart.
+struct Span {
+    uintptr_t p;
+    size_t rows, row_bytes, ld_bytes;
+    bool empty() const { return rows == 0 || row_bytes == 0; }
+    uintptr_t end() const { return p + (rows - 1) * ld_bytes + row_bytes; }
+};
+
+inline Span span(const void* p, size_t rows, size_t cols, size_t ld, size_t es)
+{
+    return Span{(uintptr_t)p, rows, cols * es, ld * es};
+}
+
+// Two matrices share a byte.  Two column ranges of one matrix (the same row
+// distance, rows that interleave without touching) do not.
+inline bool overlaps(const Span& a, const Span& b)
+{
+    if (a.empty() || b.empty() || a.end() <= b.p || b.end() <= a.p)
+        return false;
+    if (a.ld_bytes == b.ld_bytes) {
+        const size_t ld = a.ld_bytes;
+        const size_t d = b.p >= a.p ? (b.p - a.p) % ld : (ld - (a.p - b.p) % ld) % ld;
+        if (d >= a.row_bytes && d + b.row_bytes <= ld)
+            return false;
+    }
+    return true;
+}
+
+// An output that coincides exactly with an input, or does not touch it.
+inline bool same_or_apart(const Span& out, const Span& in)
+{
+    return (out.p == in.p && out.row_bytes == in.row_bytes &&
+            (out.ld_bytes == in.ld_bytes || out.rows == 1)) ||
+           !overlaps(out, in);
+}
+
+inline int launch(const void* fn, dim3 grid, int block, void** args, hipStream_t stream)
+{
+    return hipLaunchKernel(fn, grid, dim3(block), args, 0, stream) == hipSuccess ? MESWISH_OK
+                                                                                 : MESWISH_EHIP;
+}
+
+}  // namespace meblock

@@ -1,0 +1,684 @@
+// gated_ffn.hip -- the gated feed-forward unit of libmeswish for gfx950,
+// forward and backward.  Formulas and contracts: include/gated_ffn.h.
+//
+// Every product is written as out[m][n] = sum_k Q(m, k) P(n, k):
+//
+//   kUp  g and u:   P = Wg, Wu (k contiguous), Q = x (k contiguous), k = dim.
+//        A block's columns hold the same hidden units of both projections,
+//        32 of Wg then 32 of Wu, so one wave ends with g and u of the same
+//        elements in its registers and applies the activation there: h, or
+//        dg and du, are all that is written.
+//   kDx  dx:        P = Wg, Wu (n contiguous), Q = dg, du (k contiguous):
+//        one sum over hidden units of both, 2 hidden long.
+//   kDw  dWg, dWu:  P = x (n contiguous), Q = dg, du (m contiguous),
+//        k = tokens.
+//
+// The matrix cores (v_mfma_f32_32x32x16_bf16, v_mfma_f32_32x32x2_f32) take
+// P as the operand whose rows index the four consecutive results a lane
+// holds, so a lane's results are consecutive along n.
+
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "act_math.h"
+#include "block_common.h"
+#include "gated_ffn.h"
+
+namespace meblock {
+
+using meswish::Coef;
+
+enum Mode { kUp = 0, kDx = 1, kDw = 2 };
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+#define MEBLOCK_LDS __attribute__((address_space(3)))
+
+// One operand: two matrices of the same shape (Wg and Wu, dg and du, or x
+// twice), `rows` of them along the dimension that is not summed.
+template <typename T>
+struct Operand {
+    const T* base[2];
+    int64_t ld[2];
+    int rows;
+};
+
+template <typename T>
+struct GemmArgs {
+    Operand<T> p, q;
+    int k;        // length of the sum (of each half, kDx)
+    int tiles_m, tiles_n;
+    T* out[2];    // h, or dg and du; dx; dWg and dWu
+    int64_t ldo[2];
+    int out_cols; // columns of out that are written (kUp: padded, zeros past p.rows)
+    const T* dh;  // kUp, backward
+    int64_t lddh;
+    T* h;         // kUp, backward: the forward's result, or NULL
+    int64_t ldh;
+    int act;
+    Coef coef;
+};
+
+// ---------------------------------------------------------------------------
+// The activation and the product, on binary32 g and u.
+// ---------------------------------------------------------------------------
+template <class Op, bool P>
+__device__ __forceinline__ float act_value(float x, const Coef& k)
+{
+    float key = 0.0f;
+    float y = Op::template fwd<P>(x, k, key);
+    if (Op::kHasRare && Op::template is_rare<false, P>(x, k))
+        y = Op::fwd_rare(x, k);
+    return y;
+}
+
+// dy f'(x).
+template <class Op, bool P>
+__device__ __forceinline__ float act_slope(float x, float dy, const Coef& k)
+{
+    float key = 0.0f;
+    float d = Op::template bwd<P>(x, dy, k, key);
+    if (Op::kHasRare && Op::template is_rare<true, P>(x, k))
+        d = Op::bwd_rare(x, dy, k);
+    return d;
+}
+
+// N elements: forward g <- f(g) u; backward (with d = dh) g <- d u f'(g),
+// u <- d f(g), d <- f(g) u.
+template <class Op, bool P, bool BWD, int N>
+__device__ __forceinline__ void gate(float* g, float* u, float* d, const Coef& k)
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float f = act_value<Op, P>(g[j], k);
+        if constexpr (BWD) {
+            const float dg = act_slope<Op, P>(g[j], d[j] * u[j], k);
+            const float du = d[j] * f;
+            d[j] = f * u[j];
+            g[j] = dg;
+            u[j] = du;
+        } else {
+            g[j] = f * u[j];
+        }
+    }
+}
+
+template <bool P, bool BWD, int N>
+__device__ __forceinline__ void gate_act(int act, float* g, float* u, float* d, const Coef& k)
+{
+    using namespace meswish;
+    switch (act) {
+    case kRelu:
+        gate<ActOp<kRelu>, P, BWD, N>(g, u, d, k);
+        break;
+    case kLeakyRelu:
+        gate<ActOp<kLeakyRelu>, P, BWD, N>(g, u, d, k);
+        break;
+    case kSigmoid:
+        gate<ActOp<kSigmoid>, P, BWD, N>(g, u, d, k);
+        break;
+    case kTanh:
+        gate<ActOp<kTanh>, P, BWD, N>(g, u, d, k);
+        break;
+    case kGeluErf:
+        gate<ActOp<kGeluErf>, P, BWD, N>(g, u, d, k);
+        break;
+    case kGeluTanh:
+        gate<ActOp<kGeluTanh>, P, BWD, N>(g, u, d, k);
+        break;
+    default:
+        gate<ActOp<kSwish>, P, BWD, N>(g, u, d, k);
+        break;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Matrix-core steps.  A step is 16 (bf16) or 8 (binary32) values of k; lane
+// l holds row l % 32 and, of k, 8 (l / 32) + j (bf16, one instruction) or
+// 4 (l / 32) + j (binary32, instruction j).
+// ---------------------------------------------------------------------------
+template <typename T> struct Step;
+
+template <> struct Step<bf16_t> {
+    static constexpr int kK = 16;
+    typedef bf16x8 Frag;
+    __device__ static f32x16 mma(Frag p, Frag q, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(p, q, c, 0, 0, 0);
+    }
+};
+
+template <> struct Step<float> {
+    static constexpr int kK = 8;
+    typedef f32x4 Frag;
+    __device__ static f32x16 mma(Frag p, Frag q, f32x16 c)
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(p[j], q[j], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// Four consecutive k of column `lane % 16` out of 4 rows (k) x 16 columns:
+// lane l of each 16 names the address of row l / 4, columns 4 (l % 4) ...
+__device__ __forceinline__ i16x4 lds_transpose(const char* p)
+{
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEBLOCK_LDS i16x4*)p);
+}
+
+// ---------------------------------------------------------------------------
+// The wave's part of the epilogue: 32 x 64 results (two accumulators side by
+// side along n) through the wave's own LDS rows, so that a lane ends with
+// runs of 16 bytes of a row.
+// ---------------------------------------------------------------------------
+constexpr int kEpiStride = 68;                       // floats a row: 64 and 4 against bank conflicts
+constexpr int kEpiBytes = 32 * kEpiStride * 4;       // a wave's share
+
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ void epi_put(float* lds, int col0, f32x16 c)
+{
+    const int l = threadIdx.x % 64;
+    float* row = lds + (l % 32) * kEpiStride + col0 + 4 * (l / 32);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f32x4 v = {c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
+        *reinterpret_cast<f32x4*>(row + 8 * i) = v;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void epi_get(const float* p, float* f)
+{
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p + j);
+        f[j] = v[0], f[j + 1] = v[1], f[j + 2] = v[2], f[j + 3] = v[3];
+    }
+}
+
+// Rows m0 .. m0 + 31 of the output; kUp: hidden units n0 .. n0 + 31 from
+// both accumulators; otherwise columns n0 .. n0 + 63.
+template <typename T, int MODE, bool BWD>
+__device__ __forceinline__ void epilogue(const GemmArgs<T>& a, float* lds, int64_t m0, int n0,
+                                         int plane, f32x16 c0, f32x16 c1)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    const int l = threadIdx.x % 64;
+    wave_sync();  // the previous rows have been read
+    epi_put(lds, 0, c0);
+    epi_put(lds, 32, c1);
+    wave_sync();
+    if constexpr (MODE == kUp) {
+        constexpr int PER_ROW = 32 / E, ROWS = 64 / PER_ROW;
+#pragma unroll 1
+        for (int r = l / PER_ROW; r < 32; r += ROWS) {
+            const int c = (l % PER_ROW) * E;
+            const int64_t m = m0 + r;
+            const int n = n0 + c;
+            if (m >= a.q.rows || n >= a.out_cols)
+                continue;
+            float g[E], u[E], d[E];
+            epi_get<E>(lds + r * kEpiStride + c, g);
+            epi_get<E>(lds + r * kEpiStride + 32 + c, u);
+            if constexpr (BWD)
+                Elem<T>::unpack(load_chunk(a.dh + m * a.lddh, n, a.p.rows), d);
+            gate_act<sizeof(T) == 4, BWD, E>(a.act, g, u, d, a.coef);
+            if constexpr (BWD) {
+                // The workspace rows are padded: zeros past the last unit.
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    g[j] = n + j < a.p.rows ? g[j] : 0.0f;
+                    u[j] = n + j < a.p.rows ? u[j] : 0.0f;
+                }
+                store_chunk(a.out[0] + m * a.ldo[0], n, a.out_cols, g);
+                store_chunk(a.out[1] + m * a.ldo[1], n, a.out_cols, u);
+                if (a.h)
+                    store_chunk(a.h + m * a.ldh, n, a.p.rows, d);
+            } else {
+                store_chunk(a.out[0] + m * a.ldo[0], n, a.out_cols, g);
+            }
+        }
+    } else {
+        constexpr int PER_ROW = 64 / E, ROWS = 64 / PER_ROW;
+#pragma unroll 1
+        for (int r = l / PER_ROW; r < 32; r += ROWS) {
+            const int c = (l % PER_ROW) * E;
+            const int64_t m = m0 + r;
+            const int n = n0 + c;
+            if (m >= a.q.rows || n >= a.out_cols)
+                continue;
+            float f[E];
+            epi_get<E>(lds + r * kEpiStride + c, f);
+            store_chunk(a.out[plane] + m * a.ldo[plane], n, a.out_cols, f);
+        }
+    }
+}
+
+// Tiles in an order that keeps the blocks of one XCD (every eighth block) on
+// neighbouring tiles, whose operands they then share in that XCD's L2:
+// columns of 8 tiles along m, then along n.
+__device__ __forceinline__ void tile_of_block(int tiles_m, int tiles_n, int& tm, int& tn)
+{
+    const int total = tiles_m * tiles_n;
+    int id = blockIdx.x;
+    const int per = total / 8, rest = total % 8;
+    const int xcd = id % 8, at = id / 8;
+    id = xcd * per + (xcd < rest ? xcd : rest) + at;
+    constexpr int kGroup = 8;
+    const int width = kGroup * tiles_n;
+    const int first = id / width * kGroup;
+    const int rows = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+    tm = first + id % width % rows;
+    tn = id % width / rows;
+}
+
+// ---------------------------------------------------------------------------
+// Products for any alignment and size: 128 x 128 tiles, four waves of 64 x 64,
+// k in steps of 64 bytes; the next step's operands are loaded into registers
+// (16 bytes at element alignment, zeros past every edge) while the current
+// one is multiplied.
+// ---------------------------------------------------------------------------
+constexpr int kAnyTile = 128;
+
+// A tile of 128 rows (k contiguous: 64 bytes of k a row, 80 apart in LDS) or
+// of 64 bytes' worth of k rows (n contiguous: 128 values a row, padded by 32
+// bytes): both strides spread a wave's reads over all banks.
+template <typename T, bool KC>
+struct AnyTile {
+    static constexpr int E = Elem<T>::kPerVec;
+    static constexpr int kK = 64 / sizeof(T);
+    static constexpr int kStride = KC ? 80 : kAnyTile * (int)sizeof(T) + 32;
+    static constexpr int kBytes = KC ? kAnyTile * kStride : kK * kStride;
+    static constexpr int kChunks = kAnyTile * 64 / 16 / 256;  // a thread's
+
+    // Chunk i of this thread: its row of the tile and its first element in it.
+    __device__ static int row(int i)
+    {
+        const int c = threadIdx.x + i * 256;
+        return KC ? c / 4 : c / (kAnyTile / E);
+    }
+    __device__ static int col(int i)
+    {
+        const int c = threadIdx.x + i * 256;
+        return KC ? c % 4 * E : c % (kAnyTile / E) * E;
+    }
+    __device__ static typename Step<T>::Frag frag(const char* lds, int step, int row0)
+    {
+        const int l = threadIdx.x % 64;
+        if constexpr (KC) {
+            return *reinterpret_cast<const typename Step<T>::Frag*>(
+                lds + (row0 + l % 32) * kStride + step * 32 + l / 32 * 16);
+        } else if constexpr (sizeof(T) == 2) {
+            const int g = l / 16;
+            const char* p = lds + (step * 16 + 8 * (g >> 1) + l % 16 / 4) * kStride +
+                            (row0 + 16 * (g & 1) + 4 * (l % 4)) * 2;
+            const i16x4 lo = lds_transpose(p), hi = lds_transpose(p + 4 * kStride);
+            typedef short i16x8 __attribute__((ext_vector_type(8)));
+            const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(bf16x8, v);
+        } else {
+            const char* p = lds + (step * 8 + 4 * (l / 32)) * kStride + (row0 + l % 32) * 4;
+            f32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = *reinterpret_cast<const float*>(p + j * kStride);
+            return v;
+        }
+    }
+};
+
+template <typename T, int MODE, bool BWD>
+__global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
+{
+    constexpr bool PK = MODE == kUp, QK = MODE != kDw;
+    using PT = AnyTile<T, PK>;
+    using QT = AnyTile<T, QK>;
+    constexpr int kK = PT::kK;
+    constexpr int kBytes = PT::kBytes + QT::kBytes;
+    __shared__ __attribute__((aligned(16))) char lds[kBytes > 4 * kEpiBytes ? kBytes : 4 * kEpiBytes];
+    char* const lp = lds;
+    char* const lq = lds + PT::kBytes;
+
+    int tm, tn, plane = 0;
+    if constexpr (MODE == kDw) {
+        // The tiles of dWg, then those of dWu.
+        tile_of_block(2 * a.tiles_m, a.tiles_n, tm, tn);
+        plane = tm >= a.tiles_m;
+        tm -= plane * a.tiles_m;
+    } else {
+        tile_of_block(a.tiles_m, a.tiles_n, tm, tn);
+    }
+    const int64_t m0 = (int64_t)tm * kAnyTile;
+    const int n0 = tn * (MODE == kUp ? kAnyTile / 2 : kAnyTile);
+    const int steps = (a.k + kK - 1) / kK;
+    const int total = MODE == kDx ? 2 * steps : steps;
+
+    u32x4 rp[PT::kChunks], rq[QT::kChunks];
+    const u32x4 zero = {0, 0, 0, 0};
+    auto load = [&](int s) {
+        const int seg = MODE == kDx && s >= steps;
+        const int k0 = (s - seg * steps) * kK;
+#pragma unroll
+        for (int i = 0; i < PT::kChunks; ++i) {
+            const int r = PT::row(i), c = PT::col(i);
+            if constexpr (MODE == kUp) {
+                const int which = r / 32 % 2, n = n0 + r / 64 * 32 + r % 32;
+                rp[i] = n < a.p.rows
+                            ? load_chunk(a.p.base[which] + (int64_t)n * a.p.ld[which], k0 + c, a.k)
+                            : zero;
+            } else {
+                rp[i] = k0 + r < a.k ? load_chunk(a.p.base[seg] + (int64_t)(k0 + r) * a.p.ld[seg],
+                                                  n0 + c, a.p.rows)
+                                     : zero;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < QT::kChunks; ++i) {
+            const int r = QT::row(i), c = QT::col(i);
+            if constexpr (QK)
+                rq[i] = m0 + r < a.q.rows
+                            ? load_chunk(a.q.base[seg] + (m0 + r) * a.q.ld[seg], k0 + c, a.k)
+                            : zero;
+            else
+                rq[i] = k0 + r < a.k
+                            ? load_chunk(a.q.base[plane] + (int64_t)(k0 + r) * a.q.ld[plane],
+                                         (int)m0 + c, a.q.rows)
+                            : zero;
+        }
+    };
+
+    const int wave = threadIdx.x / 64, wm = wave / 2 * 64, wn = wave % 2 * 64;
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            acc[i][j] = f32x16{};
+    if (total > 0)
+        load(0);
+    for (int s = 0; s < total; ++s) {
+        __syncthreads();  // the previous step has been read
+#pragma unroll
+        for (int i = 0; i < PT::kChunks; ++i)
+            *reinterpret_cast<u32x4*>(lp + PT::row(i) * PT::kStride + PT::col(i) * sizeof(T)) = rp[i];
+#pragma unroll
+        for (int i = 0; i < QT::kChunks; ++i)
+            *reinterpret_cast<u32x4*>(lq + QT::row(i) * QT::kStride + QT::col(i) * sizeof(T)) = rq[i];
+        __syncthreads();
+        if (s + 1 < total)
+            load(s + 1);
+#pragma unroll
+        for (int t = 0; t < kK / Step<T>::kK; ++t) {
+            typename Step<T>::Frag fp[2], fq[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fp[i] = PT::frag(lp, t, wn + 32 * i);
+                fq[i] = QT::frag(lq, t, wm + 32 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = Step<T>::mma(fp[j], fq[i], acc[i][j]);
+        }
+    }
+    __syncthreads();
+    float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        epilogue<T, MODE, BWD>(a, epi, m0 + wm + 32 * i, n0 + (MODE == kUp ? wn / 2 : wn), plane,
+                               acc[i][0], acc[i][1]);
+}
+
+// ---------------------------------------------------------------------------
+// Host.
+// ---------------------------------------------------------------------------
+
+// Coefficients of the activation, in binary64 and split (see Coef).
+static Coef make_coef(int act, float p)
+{
+    const double log2e = 1.44269504088896340735992468100189214;
+    const double sqrt_2_over_pi = 0.797884560802865355879892119868763737;
+    double c = 0.0;
+    switch (act) {
+    case MESWISH_ACT_SWISH:
+        c = -(double)p * log2e;
+        break;
+    case MESWISH_ACT_SIGMOID:
+        c = -log2e;
+        break;
+    case MESWISH_ACT_TANH:
+        c = -2.0 * log2e;
+        break;
+    case MESWISH_ACT_GELU_ERF:
+        c = -0.5 * log2e;
+        break;
+    case MESWISH_ACT_GELU_TANH:
+        c = -2.0 * sqrt_2_over_pi * log2e;
+        break;
+    default:
+        break;
+    }
+    const double cubic = 0.044715;
+    Coef k;
+    k.p = p;
+    k.c_hi = (float)c;
+    k.c_lo = (float)(c - (double)k.c_hi);
+    k.aux_hi = (float)cubic;
+    k.aux_lo = (float)(cubic - (double)k.aux_hi);
+    return k;
+}
+
+static bool act_ok(int act, float param)
+{
+    if (act < MESWISH_ACT_SWISH || act > MESWISH_ACT_GELU_TANH || !isfinite(param))
+        return false;
+    // Swish's exponent coefficient must be a finite binary32 value.
+    return act != MESWISH_ACT_SWISH || isfinite(make_coef(act, param).c_hi);
+}
+
+constexpr size_t kMaxTokens = (size_t)1 << 30;
+
+static bool sizes_ok(size_t tokens, size_t dim, size_t hidden)
+{
+    return tokens < kMaxTokens && dim <= GATED_FFN_MAX_LD && hidden <= GATED_FFN_MAX_LD;
+}
+
+static bool matrix_ok(const void* p, size_t rows, size_t cols, size_t ld, size_t es)
+{
+    if (ld < cols || ld > GATED_FFN_MAX_LD)
+        return false;
+    return rows == 0 || cols == 0 || (p && aligned(p, es));
+}
+
+static size_t padded(size_t hidden) { return (hidden + 63) / 64 * 64; }
+
+template <typename T, int MODE, bool BWD>
+static int gemm_run(GemmArgs<T>& a, hipStream_t stream)
+{
+    const int cols = MODE == kUp ? kAnyTile / 2 : kAnyTile;
+    a.tiles_m = (a.q.rows + kAnyTile - 1) / kAnyTile;
+    a.tiles_n = (a.out_cols + cols - 1) / cols;
+    const int64_t grid = (int64_t)a.tiles_m * a.tiles_n * (MODE == kDw ? 2 : 1);
+    if (grid == 0)
+        return MESWISH_OK;
+    if (grid >= ((int64_t)1 << 24))
+        return MESWISH_EINVAL;
+    void* args[] = {&a};
+    return launch(reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD>),
+                  dim3((unsigned)grid), 256, args, stream);
+}
+
+template <typename T>
+static Operand<T> operand(const void* a, size_t lda, const void* b, size_t ldb, size_t rows)
+{
+    return Operand<T>{{static_cast<const T*>(a), static_cast<const T*>(b)},
+                      {(int64_t)lda, (int64_t)ldb},
+                      (int)rows};
+}
+
+template <typename T>
+static int fwd(int act, float param, const void* x, size_t ldx, const void* wg, size_t ldwg,
+               const void* wu, size_t ldwu, size_t tokens, size_t dim, size_t hidden, void* h,
+               size_t ldh, hipStream_t stream)
+{
+    GemmArgs<T> a{};
+    a.p = operand<T>(wg, ldwg, wu, ldwu, hidden);
+    a.q = operand<T>(x, ldx, x, ldx, tokens);
+    a.k = (int)dim;
+    a.out[0] = static_cast<T*>(h);
+    a.ldo[0] = (int64_t)ldh;
+    a.out_cols = (int)hidden;
+    a.act = act;
+    a.coef = make_coef(act, param);
+    return gemm_run<T, kUp, false>(a, stream);
+}
+
+template <typename T>
+static int bwd(int act, float param, const void* x, size_t ldx, const void* wg, size_t ldwg,
+               const void* wu, size_t ldwu, const void* dh, size_t lddh, size_t tokens, size_t dim,
+               size_t hidden, void* dx, size_t lddx, void* dwg, size_t lddwg, void* dwu,
+               size_t lddwu, void* h, size_t ldh, void* workspace, hipStream_t stream)
+{
+    const size_t fp = padded(hidden);
+    T* dg = static_cast<T*>(workspace);
+    T* du = dg + tokens * fp;
+    GemmArgs<T> a{};
+    a.p = operand<T>(wg, ldwg, wu, ldwu, hidden);
+    a.q = operand<T>(x, ldx, x, ldx, tokens);
+    a.k = (int)dim;
+    a.out[0] = dg;
+    a.out[1] = du;
+    a.ldo[0] = a.ldo[1] = (int64_t)fp;
+    a.out_cols = (int)fp;
+    a.dh = static_cast<const T*>(dh);
+    a.lddh = (int64_t)lddh;
+    a.h = static_cast<T*>(h);
+    a.ldh = (int64_t)ldh;
+    a.act = act;
+    a.coef = make_coef(act, param);
+    int rc = gemm_run<T, kUp, true>(a, stream);
+    if (rc == MESWISH_OK && dx) {
+        GemmArgs<T> b{};
+        b.p = operand<T>(wg, ldwg, wu, ldwu, dim);
+        b.q = operand<T>(dg, fp, du, fp, tokens);
+        b.k = (int)hidden;
+        b.out[0] = static_cast<T*>(dx);
+        b.ldo[0] = (int64_t)lddx;
+        b.out_cols = (int)dim;
+        rc = gemm_run<T, kDx, false>(b, stream);
+    }
+    if (rc == MESWISH_OK && dwg) {
+        GemmArgs<T> b{};
+        b.p = operand<T>(x, ldx, x, ldx, dim);
+        b.q = operand<T>(dg, fp, du, fp, hidden);
+        b.k = (int)tokens;
+        b.out[0] = static_cast<T*>(dwg);
+        b.out[1] = static_cast<T*>(dwu);
+        b.ldo[0] = (int64_t)lddwg;
+        b.ldo[1] = (int64_t)lddwu;
+        b.out_cols = (int)dim;
+        rc = gemm_run<T, kDw, false>(b, stream);
+    }
+    return rc;
+}
+
+// No output touches an input or another output.
+static int apart(const Span* out, int nout, const Span* in, int nin)
+{
+    for (int o = 0; o < nout; ++o) {
+        for (int i = 0; i < nin; ++i)
+            if (overlaps(out[o], in[i]))
+                return MESWISH_EALIAS;
+        for (int i = 0; i < o; ++i)
+            if (overlaps(out[o], out[i]))
+                return MESWISH_EALIAS;
+    }
+    return MESWISH_OK;
+}
+
+}  // namespace meblock
+
+using namespace meblock;
+
+extern "C" size_t gated_ffn_workspace_bytes(size_t tokens, size_t dim, size_t hidden, int dtype,
+                                            int backward)
+{
+    if (!dtype_ok(dtype) || !sizes_ok(tokens, dim, hidden) || !backward)
+        return 0;
+    return 2 * tokens * padded(hidden) * elem_size(dtype);
+}
+
+extern "C" int gated_ffn_fwd(int act, float param, const void* x, size_t ldx, const void* wg,
+                             size_t ldwg, const void* wu, size_t ldwu, size_t tokens, size_t dim,
+                             size_t hidden, void* h, size_t ldh, void* workspace,
+                             size_t workspace_bytes, int dtype, void* stream)
+{
+    if (!dtype_ok(dtype) || !act_ok(act, param) || !sizes_ok(tokens, dim, hidden))
+        return MESWISH_EINVAL;
+    const size_t es = elem_size(dtype);
+    if (!matrix_ok(x, tokens, dim, ldx, es) || !matrix_ok(wg, hidden, dim, ldwg, es) ||
+        !matrix_ok(wu, hidden, dim, ldwu, es) || !matrix_ok(h, tokens, hidden, ldh, es))
+        return MESWISH_EINVAL;
+    const size_t need = gated_ffn_workspace_bytes(tokens, dim, hidden, dtype, 0);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return MESWISH_EINVAL;
+    const Span in[] = {span(x, tokens, dim, ldx, es), span(wg, hidden, dim, ldwg, es),
+                       span(wu, hidden, dim, ldwu, es)};
+    const Span out[] = {span(h, tokens, hidden, ldh, es), span(workspace, need ? 1 : 0, need, need, 1)};
+    int rc = apart(out, 2, in, 3);
+    if (rc != MESWISH_OK)
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return dtype == MESWISH_F32
+               ? fwd<float>(act, param, x, ldx, wg, ldwg, wu, ldwu, tokens, dim, hidden, h, ldh, s)
+               : fwd<bf16_t>(act, param, x, ldx, wg, ldwg, wu, ldwu, tokens, dim, hidden, h, ldh, s);
+}
+
+extern "C" int gated_ffn_bwd(int act, float param, const void* x, size_t ldx, const void* wg,
+                             size_t ldwg, const void* wu, size_t ldwu, const void* dh, size_t lddh,
+                             size_t tokens, size_t dim, size_t hidden, void* dx, size_t lddx,
+                             void* dwg, size_t lddwg, void* dwu, size_t lddwu, void* h, size_t ldh,
+                             void* workspace, size_t workspace_bytes, int dtype, void* stream)
+{
+    if (!dtype_ok(dtype) || !act_ok(act, param) || !sizes_ok(tokens, dim, hidden) ||
+        (dwg == nullptr) != (dwu == nullptr))
+        return MESWISH_EINVAL;
+    const size_t es = elem_size(dtype);
+    if (!matrix_ok(x, tokens, dim, ldx, es) || !matrix_ok(wg, hidden, dim, ldwg, es) ||
+        !matrix_ok(wu, hidden, dim, ldwu, es) || !matrix_ok(dh, tokens, hidden, lddh, es) ||
+        (dx && !matrix_ok(dx, tokens, dim, lddx, es)) ||
+        (dwg && (!matrix_ok(dwg, hidden, dim, lddwg, es) || !matrix_ok(dwu, hidden, dim, lddwu, es))) ||
+        (h && !matrix_ok(h, tokens, hidden, ldh, es)))
+        return MESWISH_EINVAL;
+    const size_t need = gated_ffn_workspace_bytes(tokens, dim, hidden, dtype, 1);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return MESWISH_EINVAL;
+    const Span in[] = {span(x, tokens, dim, ldx, es), span(wg, hidden, dim, ldwg, es),
+                       span(wu, hidden, dim, ldwu, es), span(dh, tokens, hidden, lddh, es)};
+    const Span out[] = {span(dx, dx ? tokens : 0, dim, lddx, es),
+                        span(dwg, dwg ? hidden : 0, dim, lddwg, es),
+                        span(dwu, dwu ? hidden : 0, dim, lddwu, es),
+                        span(h, h ? tokens : 0, hidden, ldh, es),
+                        span(workspace, need ? 1 : 0, need, need, 1)};
+    int rc = apart(out, 5, in, 4);
+    if (rc != MESWISH_OK)
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return dtype == MESWISH_F32
+               ? bwd<float>(act, param, x, ldx, wg, ldwg, wu, ldwu, dh, lddh, tokens, dim, hidden,
+                            dx, lddx, dwg, lddwg, dwu, lddwu, h, ldh, workspace, s)
+               : bwd<bf16_t>(act, param, x, ldx, wg, ldwg, wu, ldwu, dh, lddh, tokens, dim, hidden,
+                             dx, lddx, dwg, lddwg, dwu, lddwu, h, ldh, workspace, s);
+}

@@ -1,0 +1,715 @@
+// layer_norm.hip -- layer normalization of libmeswish for gfx950, forward
+// and backward.  Formulas and contracts: include/layer_norm.h.
+//
+// Bound: HBM bandwidth (8 flops an element forward, 15 backward).  Both
+// directions read each row once and keep it in registers, packed as loaded:
+//   * A group of G threads owns a row, thread g holding the 16-byte vectors
+//     g, G + g, ... (V of them).  G is 4 or 16 lanes of a wave, a wave, or a
+//     block of 256 or 1024 threads, so the two sums of a row cost lane
+//     exchanges only, or one exchange through LDS a batch of rows.
+//   * The variance is the mean of squared differences from the mean, from
+//     the registers: no cancellation of E[x^2] - mean^2.
+//   * Backward: a thread owns the same columns in every row its block takes,
+//     so the sums for dweight and dbias stay in registers over the block's
+//     rows.  Each block writes one binary32 partial per column; a second
+//     kernel adds them in a fixed order (no atomics, deterministic).
+//   * Rows longer than 1024 threads hold are read again for each pass (the
+//     caches serve most of it), one block per row.
+
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "block_common.h"
+#include "layer_norm.h"
+
+namespace meblock {
+
+// Most blocks of the backward, each with its own partial sums.
+constexpr int kMaxParts = 512;
+constexpr int64_t kMaxGrid = 1 << 23;
+
+template <int G>
+struct Group {
+    static constexpr int kThreads = G > 256 ? G : 256;
+    static constexpr int kGroups = kThreads / G;  // rows a block takes at once
+    static constexpr int kWaves = G / 64;         // waves of a group, where it is whole waves
+};
+
+// Sum of K values over each group of G threads, the result in every thread.
+// Waves combine through `lds` (K * kWaves floats); two barriers.
+template <int G, int K>
+__device__ __forceinline__ void group_sum(float (&v)[K], float* lds)
+{
+#pragma unroll
+    for (int m = 1; m < (G < 64 ? G : 64); m <<= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            v[k] += __shfl_xor(v[k], m);
+    if constexpr (G > 64) {
+        constexpr int W = Group<G>::kWaves;
+        const int wave = threadIdx.x / 64;
+        __syncthreads();
+        if (threadIdx.x % 64 == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                lds[k * W + wave] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                s += lds[k * W + w];
+            v[k] = s;
+        }
+    }
+}
+
+// E whole parameters from e0, or `none` where there are no parameters.
+template <int E, typename P>
+__device__ __forceinline__ void load_params(const P* p, int e0, float none, float* f)
+{
+    constexpr int K = Elem<P>::kPerVec;
+    if (!p) {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            f[j] = none;
+    } else if constexpr (E >= K) {
+#pragma unroll
+        for (int j = 0; j < E; j += K)
+            Elem<P>::unpack(load16(p + e0 + j), f + j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            f[j] = Elem<P>::get(p[e0 + j]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Forward.
+// ---------------------------------------------------------------------------
+template <typename T, typename P, int G, int V>
+__global__ __launch_bounds__(Group<G>::kThreads) void ln_fwd_kernel(
+    const T* __restrict__ x, int64_t ldx, const P* __restrict__ w, const P* __restrict__ b,
+    int64_t rows, int n, float eps, T* y, int64_t ldy, float* __restrict__ mean,
+    float* __restrict__ rstd)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    constexpr int NG = Group<G>::kGroups;
+    __shared__ float lds[G > 64 ? Group<G>::kWaves : 1];
+    const int g = threadIdx.x % G;
+    const float inv_n = 1.0f / (float)n;
+    // Threads of one group agree on the row; a group of whole blocks meets
+    // every barrier together.
+    for (int64_t row = (int64_t)blockIdx.x * NG + threadIdx.x / G; row < rows;
+         row += (int64_t)gridDim.x * NG) {
+        const T* xr = x + row * ldx;
+        u32x4 raw[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            raw[v] = load_chunk(xr, (v * G + g) * E, n);
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float f[E];
+            Elem<T>::unpack(raw[v], f);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                s[0] += f[j];
+        }
+        group_sum<G>(s, lds);
+        const float mu = s[0] * inv_n;
+        float q[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e0 = (v * G + g) * E;
+            float f[E];
+            Elem<T>::unpack(raw[v], f);
+            if (e0 + E <= n) {
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    q[0] = fmaf(f[j] - mu, f[j] - mu, q[0]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    q[0] += e0 + j < n ? (f[j] - mu) * (f[j] - mu) : 0.0f;
+            }
+        }
+        group_sum<G>(q, lds);
+        const float r = 1.0f / sqrtf(fmaf(q[0], inv_n, eps));
+        if (g == 0) {
+            if (mean)
+                mean[row] = mu;
+            if (rstd)
+                rstd[row] = r;
+        }
+        T* yr = y + row * ldy;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e0 = (v * G + g) * E;
+            if (e0 >= n)
+                continue;
+            float f[E];
+            Elem<T>::unpack(raw[v], f);
+            if (e0 + E <= n) {
+                float wf[E], bf[E];
+                load_params<E>(w, e0, 1.0f, wf);
+                load_params<E>(b, e0, 0.0f, bf);
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    f[j] = fmaf((f[j] - mu) * r, wf[j], bf[j]);
+                store16(yr + e0, Elem<T>::pack(f));
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if (e0 + j < n)
+                        yr[e0 + j] = Elem<T>::put(fmaf((f[j] - mu) * r,
+                                                       w ? Elem<P>::get(w[e0 + j]) : 1.0f,
+                                                       b ? Elem<P>::get(b[e0 + j]) : 0.0f));
+            }
+        }
+    }
+}
+
+// Rows of any length: three passes over the row, one block of 1024 threads.
+template <typename T, typename P>
+__global__ __launch_bounds__(1024) void ln_fwd_long_kernel(
+    const T* x, int64_t ldx, const P* __restrict__ w, const P* __restrict__ b, int64_t rows, int n,
+    float eps, T* y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    __shared__ float lds[16];
+    const float inv_n = 1.0f / (float)n;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const T* xr = x + row * ldx;
+        T* yr = y + row * ldy;
+        float s[1] = {0.0f};
+        for (int64_t e0 = (int64_t)threadIdx.x * E; e0 < n; e0 += 1024 * E) {
+            float f[E];
+            Elem<T>::unpack(load_chunk(xr, (int)e0, n), f);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                s[0] += f[j];
+        }
+        group_sum<1024>(s, lds);
+        const float mu = s[0] * inv_n;
+        float q[1] = {0.0f};
+        for (int64_t e0 = (int64_t)threadIdx.x * E; e0 < n; e0 += 1024 * E) {
+            float f[E];
+            Elem<T>::unpack(load_chunk(xr, (int)e0, n), f);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                q[0] += e0 + j < n ? (f[j] - mu) * (f[j] - mu) : 0.0f;
+        }
+        group_sum<1024>(q, lds);
+        const float r = 1.0f / sqrtf(fmaf(q[0], inv_n, eps));
+        if (threadIdx.x == 0) {
+            if (mean)
+                mean[row] = mu;
+            if (rstd)
+                rstd[row] = r;
+        }
+        for (int64_t e0 = (int64_t)threadIdx.x * E; e0 < n; e0 += 1024 * E) {
+            float f[E];
+            Elem<T>::unpack(load_chunk(xr, (int)e0, n), f);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                f[j] = e0 + j < n ? fmaf((f[j] - mu) * r, w ? Elem<P>::get(w[e0 + j]) : 1.0f,
+                                         b ? Elem<P>::get(b[e0 + j]) : 0.0f)
+                                  : 0.0f;
+            store_chunk(yr, (int)e0, n, f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Backward.
+// ---------------------------------------------------------------------------
+
+// R rows a group and batch: their loads are in flight together and their
+// sums share one exchange.
+template <typename T, typename P, int G, int V, int R>
+__global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
+    const T* x, int64_t ldx, const T* dy, int64_t lddy, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const P* __restrict__ w, int64_t rows, int n, T* dx,
+    int64_t lddx, float* __restrict__ part)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    constexpr int NG = Group<G>::kGroups;
+    __shared__ float lds[G > 64 ? 2 * R * Group<G>::kWaves : 1];
+    const int g = threadIdx.x % G, grp = threadIdx.x / G;
+    const float inv_n = 1.0f / (float)n;
+    float wf[V][E], aw[V][E], ab[V][E];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const int e = (v * G + g) * E + j;
+            wf[v][j] = w && e < n ? Elem<P>::get(w[e]) : 1.0f;
+            aw[v][j] = ab[v][j] = 0.0f;
+        }
+    for (int64_t base = (int64_t)blockIdx.x * (NG * R); base < rows;
+         base += (int64_t)gridDim.x * (NG * R)) {
+        u32x4 rx[R][V], rd[R][V];
+        float mu[R], rs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = base + r * NG + grp;
+            const bool in = row < rows;
+            mu[r] = in ? mean[row] : 0.0f;
+            rs[r] = in ? rstd[row] : 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                // A row past the end counts as an empty one (zeros).
+                rx[r][v] = load_chunk(x + row * ldx, (v * G + g) * E, in ? n : 0);
+                rd[r][v] = load_chunk(dy + row * lddy, (v * G + g) * E, in ? n : 0);
+            }
+        }
+        float s[2 * R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float fx[E], fd[E];
+                Elem<T>::unpack(rx[r][v], fx);
+                Elem<T>::unpack(rd[r][v], fd);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float xh = (fx[j] - mu[r]) * rs[r];
+                    const float gg = fd[j] * wf[v][j];
+                    s1 += gg;
+                    s2 = fmaf(gg, xh, s2);
+                    aw[v][j] = fmaf(fd[j], xh, aw[v][j]);
+                    ab[v][j] += fd[j];
+                }
+            }
+            s[2 * r] = s1;
+            s[2 * r + 1] = s2;
+        }
+        group_sum<G>(s, lds);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = base + r * NG + grp;
+            if (row >= rows)
+                continue;
+            const float m1 = s[2 * r] * inv_n, m2 = s[2 * r + 1] * inv_n;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e0 = (v * G + g) * E;
+                if (e0 >= n)
+                    continue;
+                float fx[E], fd[E];
+                Elem<T>::unpack(rx[r][v], fx);
+                Elem<T>::unpack(rd[r][v], fd);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float xh = (fx[j] - mu[r]) * rs[r];
+                    fd[j] = rs[r] * (fmaf(fd[j], wf[v][j], -m1) - xh * m2);
+                }
+                store_chunk(dx + row * lddx, e0, n, fd);
+            }
+        }
+    }
+    if (!part)
+        return;
+    float* pw = part + (int64_t)blockIdx.x * 2 * n;
+    if constexpr (NG > 1) {
+        // Columns of the block's groups, added in order of the group.
+        __shared__ float sums[2][256 * V * E];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int e = (v * G + g) * E + j;
+                sums[0][grp * (G * V * E) + e] = aw[v][j];
+                sums[1][grp * (G * V * E) + e] = ab[v][j];
+            }
+        __syncthreads();
+        for (int e = threadIdx.x; e < 2 * n; e += Group<G>::kThreads) {
+            const int which = e >= n, col = e - which * n;
+            float s = 0.0f;
+            for (int k = 0; k < NG; ++k)
+                s += sums[which][k * (G * V * E) + col];
+            pw[e] = s;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int e = (v * G + g) * E + j;
+                if (e < n) {
+                    pw[e] = aw[v][j];
+                    pw[n + e] = ab[v][j];
+                }
+            }
+    }
+}
+
+// dweight and dbias from the blocks' partial sums: 32 columns a block, 32
+// threads a column.
+template <typename P>
+__global__ __launch_bounds__(1024) void ln_params_kernel(const float* __restrict__ part, int parts,
+                                                         int n, P* dweight, P* dbias)
+{
+    __shared__ float lds[32][33];
+    const int c = threadIdx.x % 32, k = threadIdx.x / 32;
+    const int64_t col = (int64_t)blockIdx.x * 32 + c;  // of 2 n: dweight's, then dbias's
+    float s = 0.0f;
+    if (col < 2 * (int64_t)n)
+        for (int p = k; p < parts; p += 32)
+            s += part[(int64_t)p * 2 * n + col];
+    lds[k][c] = s;
+    __syncthreads();
+    // Thread (c', k') takes column k', part c': a half wave a column.
+    float t = lds[c][k];
+#pragma unroll
+    for (int m = 16; m; m >>= 1)
+        t += __shfl_xor(t, m);
+    const int64_t out = (int64_t)blockIdx.x * 32 + k;
+    if (c == 0 && out < 2 * (int64_t)n) {
+        P* dst = out < n ? dweight : dbias;
+        if (dst)
+            dst[out < n ? out : out - n] = Elem<P>::put(t);
+    }
+}
+
+// Long rows: dx in two passes over the row.
+template <typename T, typename P>
+__global__ __launch_bounds__(1024) void ln_bwd_long_kernel(
+    const T* x, int64_t ldx, const T* dy, int64_t lddy, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const P* __restrict__ w, int64_t rows, int n, T* dx,
+    int64_t lddx)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    __shared__ float lds[32];
+    const float inv_n = 1.0f / (float)n;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const T* xr = x + row * ldx;
+        const T* dr = dy + row * lddy;
+        const float mu = mean[row], rs = rstd[row];
+        float s[2] = {0.0f, 0.0f};
+        for (int64_t e0 = (int64_t)threadIdx.x * E; e0 < n; e0 += 1024 * E) {
+            float fx[E], fd[E];
+            Elem<T>::unpack(load_chunk(xr, (int)e0, n), fx);
+            Elem<T>::unpack(load_chunk(dr, (int)e0, n), fd);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                if (e0 + j >= n)
+                    continue;
+                const float gg = fd[j] * (w ? Elem<P>::get(w[e0 + j]) : 1.0f);
+                s[0] += gg;
+                s[1] = fmaf(gg, (fx[j] - mu) * rs, s[1]);
+            }
+        }
+        group_sum<1024>(s, lds);
+        const float m1 = s[0] * inv_n, m2 = s[1] * inv_n;
+        for (int64_t e0 = (int64_t)threadIdx.x * E; e0 < n; e0 += 1024 * E) {
+            float fx[E], fd[E];
+            Elem<T>::unpack(load_chunk(xr, (int)e0, n), fx);
+            Elem<T>::unpack(load_chunk(dr, (int)e0, n), fd);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const float wj = w && e0 + j < n ? Elem<P>::get(w[e0 + j]) : 1.0f;
+                fd[j] = rs * (fmaf(fd[j], wj, -m1) - (fx[j] - mu) * rs * m2);
+            }
+            store_chunk(dx + row * lddx, (int)e0, n, fd);
+        }
+    }
+}
+
+// Long rows: the blocks' partial column sums, 256 E columns by a share of
+// the rows.
+template <typename T>
+__global__ __launch_bounds__(256) void ln_cols_kernel(const T* __restrict__ x, int64_t ldx,
+                                                      const T* __restrict__ dy, int64_t lddy,
+                                                      const float* __restrict__ mean,
+                                                      const float* __restrict__ rstd, int64_t rows,
+                                                      int n, float* __restrict__ part)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    const int64_t first = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E;
+    if (first >= n)
+        return;
+    const int e0 = (int)first;
+    float aw[E], ab[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        aw[j] = ab[j] = 0.0f;
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        float fx[E], fd[E];
+        Elem<T>::unpack(load_chunk(x + row * ldx, e0, n), fx);
+        Elem<T>::unpack(load_chunk(dy + row * lddy, e0, n), fd);
+        const float mu = mean[row], rs = rstd[row];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            aw[j] = fmaf(fd[j], (fx[j] - mu) * rs, aw[j]);
+            ab[j] += fd[j];
+        }
+    }
+    float* pw = part + (int64_t)blockIdx.y * 2 * n;
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (e0 + j < n) {
+            pw[e0 + j] = aw[j];
+            pw[n + e0 + j] = ab[j];
+        }
+}
+
+// ---------------------------------------------------------------------------
+// Host.
+// ---------------------------------------------------------------------------
+
+template <typename T, typename P>
+struct LnArgs {
+    const T *x, *dy;
+    const P *w, *b;
+    int64_t ldx, lddy, ldo, rows;
+    int n;
+    float eps;
+    T* out;  // y or dx
+    float *mean, *rstd, *part;
+    P *dweight, *dbias;
+    hipStream_t stream;
+};
+
+template <typename T, typename P, int G, int V>
+static int fwd_launch(LnArgs<T, P>& a)
+{
+    constexpr int NG = Group<G>::kGroups;
+    int64_t grid = (a.rows + NG - 1) / NG;
+    if (grid > kMaxGrid)
+        grid = kMaxGrid;
+    void* args[] = {&a.x, &a.ldx, &a.w, &a.b, &a.rows, &a.n, &a.eps, &a.out, &a.ldo, &a.mean,
+                    &a.rstd};
+    return launch(reinterpret_cast<const void*>(&ln_fwd_kernel<T, P, G, V>), dim3((unsigned)grid),
+                  Group<G>::kThreads, args, a.stream);
+}
+
+// 16-byte vectors a row.
+template <typename T>
+static int64_t chunks(int n)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    return ((int64_t)n + E - 1) / E;
+}
+
+template <typename T, typename P>
+static int fwd_run(LnArgs<T, P>& a)
+{
+    const int64_t c = chunks<T>(a.n);
+    if (c <= 4)
+        return fwd_launch<T, P, 4, 1>(a);
+    if (c <= 16)
+        return fwd_launch<T, P, 16, 1>(a);
+    if (c <= 64)
+        return fwd_launch<T, P, 64, 1>(a);
+    if (c <= 128)
+        return fwd_launch<T, P, 64, 2>(a);
+    if (c <= 256)
+        return fwd_launch<T, P, 256, 1>(a);
+    if (c <= 512)
+        return fwd_launch<T, P, 256, 2>(a);
+    if (c <= 1024)
+        return fwd_launch<T, P, 256, 4>(a);
+    if (c <= 2048)
+        return fwd_launch<T, P, 256, 8>(a);
+    if (c <= 4096)
+        return fwd_launch<T, P, 1024, 4>(a);
+    int64_t grid = a.rows < kMaxGrid ? a.rows : kMaxGrid;
+    void* args[] = {&a.x, &a.ldx, &a.w, &a.b, &a.rows, &a.n, &a.eps, &a.out, &a.ldo, &a.mean,
+                    &a.rstd};
+    return launch(reinterpret_cast<const void*>(&ln_fwd_long_kernel<T, P>), dim3((unsigned)grid),
+                  1024, args, a.stream);
+}
+
+template <typename P>
+static int params_launch(const float* part, int parts, int n, P* dweight, P* dbias,
+                         hipStream_t stream)
+{
+    void* args[] = {&part, &parts, &n, &dweight, &dbias};
+    const int64_t grid = (2 * (int64_t)n + 31) / 32;
+    return launch(reinterpret_cast<const void*>(&ln_params_kernel<P>), dim3((unsigned)grid), 1024,
+                  args, stream);
+}
+
+template <typename T, typename P, int G, int V, int R>
+static int bwd_launch(LnArgs<T, P>& a)
+{
+    constexpr int NG = Group<G>::kGroups;
+    int64_t grid = (a.rows + NG * R - 1) / (NG * R);
+    if (grid > kMaxParts)
+        grid = kMaxParts;
+    void* args[] = {&a.x, &a.ldx, &a.dy, &a.lddy, &a.mean, &a.rstd, &a.w, &a.rows, &a.n, &a.out,
+                    &a.ldo, &a.part};
+    int rc = launch(reinterpret_cast<const void*>(&ln_bwd_kernel<T, P, G, V, R>),
+                    dim3((unsigned)grid), Group<G>::kThreads, args, a.stream);
+    if (rc != MESWISH_OK || !a.part)
+        return rc;
+    return params_launch<P>(a.part, (int)grid, a.n, a.dweight, a.dbias, a.stream);
+}
+
+template <typename T, typename P>
+static int bwd_run(LnArgs<T, P>& a)
+{
+    if (a.rows == 0)
+        return a.part ? params_launch<P>(a.part, 0, a.n, a.dweight, a.dbias, a.stream) : MESWISH_OK;
+    const int64_t c = chunks<T>(a.n);
+    if (c <= 4)
+        return bwd_launch<T, P, 4, 1, 1>(a);
+    if (c <= 16)
+        return bwd_launch<T, P, 16, 1, 2>(a);
+    if (c <= 64)
+        return bwd_launch<T, P, 64, 1, 2>(a);
+    if (c <= 256)
+        return bwd_launch<T, P, 256, 1, 4>(a);
+    if (c <= 512)
+        return bwd_launch<T, P, 256, 2, 2>(a);
+    if (c <= 1024)
+        return bwd_launch<T, P, 256, 4, 1>(a);
+    if (c <= 2048)
+        return bwd_launch<T, P, 1024, 2, 1>(a);
+    if (a.part) {
+        int64_t rowsplit = a.rows < kMaxParts ? a.rows : kMaxParts;
+        void* args[] = {&a.x, &a.ldx, &a.dy, &a.lddy, &a.mean, &a.rstd, &a.rows, &a.n, &a.part};
+        int rc = launch(reinterpret_cast<const void*>(&ln_cols_kernel<T>),
+                        dim3((unsigned)((c + 255) / 256), (unsigned)rowsplit), 256, args, a.stream);
+        if (rc == MESWISH_OK)
+            rc = params_launch<P>(a.part, (int)rowsplit, a.n, a.dweight, a.dbias, a.stream);
+        if (rc != MESWISH_OK)
+            return rc;
+    }
+    int64_t grid = a.rows < kMaxGrid ? a.rows : kMaxGrid;
+    void* args[] = {&a.x, &a.ldx, &a.dy, &a.lddy, &a.mean, &a.rstd, &a.w, &a.rows, &a.n, &a.out,
+                    &a.ldo};
+    return launch(reinterpret_cast<const void*>(&ln_bwd_long_kernel<T, P>), dim3((unsigned)grid),
+                  1024, args, a.stream);
+}
+
+static bool matrix_ok(const void* p, size_t rows, size_t n, size_t ld, size_t es)
+{
+    if (!p || !aligned(p, es) || n >= ((size_t)1 << 31) || ld < n)
+        return false;
+    const size_t most = (size_t)1 << 59;
+    return rows == 0 || (rows < most && n < most && (ld == 0 || (rows - 1) < (most - n) / ld));
+}
+
+}  // namespace meblock
+
+using namespace meblock;
+
+extern "C" size_t layer_norm_workspace_bytes(size_t rows, size_t n)
+{
+    if (n >= ((size_t)1 << 31))
+        return 0;
+    // At most one part a row.
+    const size_t parts = rows < (size_t)kMaxParts ? (rows ? rows : 1) : (size_t)kMaxParts;
+    return parts * 2 * (n ? n : 1) * sizeof(float);
+}
+
+extern "C" int layer_norm_fwd(const void* x, size_t ldx, const void* weight, const void* bias,
+                              size_t rows, size_t n, float eps, void* y, size_t ldy, float* mean,
+                              float* rstd, int dtype, int param_dtype, void* stream)
+{
+    if (!dtype_ok(dtype) || !dtype_ok(param_dtype) || !isfinite(eps) || eps < 0.0f)
+        return MESWISH_EINVAL;
+    if (rows == 0 || n == 0)
+        return MESWISH_OK;
+    const size_t es = elem_size(dtype), ps = elem_size(param_dtype);
+    if (!matrix_ok(x, rows, n, ldx, es) || !matrix_ok(y, rows, n, ldy, es) ||
+        !aligned(weight, ps) || !aligned(bias, ps) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return MESWISH_EINVAL;
+    const Span sx = span(x, rows, n, ldx, es), sy = span(y, rows, n, ldy, es);
+    const Span sw = span(weight, weight ? 1 : 0, n, n, ps), sb = span(bias, bias ? 1 : 0, n, n, ps);
+    const Span sm = span(mean, mean ? 1 : 0, rows, rows, 4), sr = span(rstd, rstd ? 1 : 0, rows, rows, 4);
+    if (!same_or_apart(sy, sx) || overlaps(sy, sw) || overlaps(sy, sb) || overlaps(sy, sm) ||
+        overlaps(sy, sr) || overlaps(sm, sx) || overlaps(sr, sx) || overlaps(sm, sr) ||
+        overlaps(sm, sw) || overlaps(sm, sb) || overlaps(sr, sw) || overlaps(sr, sb))
+        return MESWISH_EALIAS;
+    auto run = [&](auto t, auto p) {
+        using T = decltype(t);
+        using P = decltype(p);
+        LnArgs<T, P> a{};
+        a.x = static_cast<const T*>(x);
+        a.w = static_cast<const P*>(weight);
+        a.b = static_cast<const P*>(bias);
+        a.ldx = (int64_t)ldx;
+        a.ldo = (int64_t)ldy;
+        a.rows = (int64_t)rows;
+        a.n = (int)n;
+        a.eps = eps;
+        a.out = static_cast<T*>(y);
+        a.mean = mean;
+        a.rstd = rstd;
+        a.stream = static_cast<hipStream_t>(stream);
+        return fwd_run<T, P>(a);
+    };
+    if (dtype == MESWISH_F32)
+        return param_dtype == MESWISH_F32 ? run(float(), float()) : run(float(), bf16_t());
+    return param_dtype == MESWISH_F32 ? run(bf16_t(), float()) : run(bf16_t(), bf16_t());
+}
+
+extern "C" int layer_norm_bwd(const void* x, size_t ldx, const void* dy, size_t lddy,
+                              const float* mean, const float* rstd, const void* weight, size_t rows,
+                              size_t n, void* dx, size_t lddx, void* dweight, void* dbias,
+                              void* workspace, size_t workspace_bytes, int dtype, int param_dtype,
+                              void* stream)
+{
+    if (!dtype_ok(dtype) || !dtype_ok(param_dtype) || n >= ((size_t)1 << 31))
+        return MESWISH_EINVAL;
+    if (n == 0)
+        return MESWISH_OK;
+    const size_t es = elem_size(dtype), ps = elem_size(param_dtype);
+    const bool sums = dweight || dbias;
+    const size_t need = sums ? layer_norm_workspace_bytes(rows, n) : 0;
+    if (sums && (!workspace || workspace_bytes < need || !aligned(workspace, 4)))
+        return MESWISH_EINVAL;
+    if (!aligned(dweight, ps) || !aligned(dbias, ps) || !aligned(weight, ps))
+        return MESWISH_EINVAL;
+    if (rows > 0 && (!matrix_ok(x, rows, n, ldx, es) || !matrix_ok(dy, rows, n, lddy, es) ||
+                     !matrix_ok(dx, rows, n, lddx, es) || !mean || !rstd || !aligned(mean, 4) ||
+                     !aligned(rstd, 4)))
+        return MESWISH_EINVAL;
+    // With no rows every pointer below but the sums' is empty.
+    const Span in[] = {span(x, rows, n, ldx, es), span(dy, rows, n, lddy, es),
+                       span(mean, rows ? 1 : 0, rows, rows, 4),
+                       span(rstd, rows ? 1 : 0, rows, rows, 4),
+                       span(weight, weight ? 1 : 0, n, n, ps)};
+    const Span out[] = {span(dx, rows, n, lddx, es), span(dweight, dweight ? 1 : 0, n, n, ps),
+                        span(dbias, dbias ? 1 : 0, n, n, ps), span(workspace, sums ? 1 : 0, need, need, 1)};
+    for (int o = 0; o < 4; ++o) {
+        for (int i = 0; i < 5; ++i)
+            if (o == 0 && i < 2 ? !same_or_apart(out[o], in[i]) : overlaps(out[o], in[i]))
+                return MESWISH_EALIAS;
+        for (int i = 0; i < o; ++i)
+            if (overlaps(out[o], out[i]))
+                return MESWISH_EALIAS;
+    }
+    auto run = [&](auto t, auto p) {
+        using T = decltype(t);
+        using P = decltype(p);
+        LnArgs<T, P> a{};
+        a.x = static_cast<const T*>(x);
+        a.dy = static_cast<const T*>(dy);
+        a.w = static_cast<const P*>(weight);
+        a.ldx = (int64_t)ldx;
+        a.lddy = (int64_t)lddy;
+        a.ldo = (int64_t)lddx;
+        a.rows = (int64_t)rows;
+        a.n = (int)n;
+        a.out = static_cast<T*>(dx);
+        a.mean = const_cast<float*>(mean);
+        a.rstd = const_cast<float*>(rstd);
+        a.part = sums ? static_cast<float*>(workspace) : nullptr;
+        a.dweight = static_cast<P*>(dweight);
+        a.dbias = static_cast<P*>(dbias);
+        a.stream = static_cast<hipStream_t>(stream);
+        return bwd_run<T, P>(a);
+    };
+    if (dtype == MESWISH_F32)
+        return param_dtype == MESWISH_F32 ? run(float(), float()) : run(float(), bf16_t());
+    return param_dtype == MESWISH_F32 ? run(bf16_t(), float()) : run(bf16_t(), bf16_t());
+}

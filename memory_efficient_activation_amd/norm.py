@@ -1,0 +1,178 @@
+"""Layer normalization on libmeswish (include/layer_norm.h).
+
+y = (x - mean) rstd weight + bias over the last dimension, with
+mean = sum x / n and rstd = 1 / sqrt(sum (x - mean)^2 / n + eps).  In the
+manner of the memory-efficient activations the backward keeps the input and
+recomputes the normalized map, from two binary32 values a row.
+
+* ``layer_norm_fwd(x, weight, bias, eps)`` -> (y, mean, rstd);
+* ``layer_norm_bwd(x, dy, mean, rstd, weight)`` -> (dx, dweight, dbias);
+* ``LayerNormFn`` / ``LayerNorm`` -- an autograd function and module that
+  keep x and the rows' statistics.
+
+x is float32 or bfloat16 and may have any leading shape; rows at a constant
+distance (a column range of a wider matrix) are read in place.  weight and
+bias are float32 or bfloat16, independent of x.  Tensor-level functions only
+check and marshal arguments; there is no CPU path.
+"""
+
+from __future__ import annotations
+
+import torch
+import torch.nn as nn
+
+from . import _lib
+from .dense import EPS, SharedBuffer, _current
+from .functional import _dtype_code, _require_device, _same, _stream
+
+
+def as_rows(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int, int, int]:
+    """(t, rows, n, ld): t as rows of n contiguous elements, ld elements
+    apart; copied only if its strides allow no such reading."""
+    _require_device(t, name)
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    n = t.shape[-1]
+    if t.is_contiguous():
+        return t, (t.numel() // n if n else 0), n, n
+    if t.stride(-1) == 1 or n == 1:
+        # Every leading dimension steps over whole blocks of the next.
+        ld, ok, span = None, t.numel() > 0, 1
+        for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if size == 1:
+                continue
+            if ld is None:
+                ld, span = stride, size
+            elif stride == ld * span:
+                span *= size
+            else:
+                ok = False
+        if ok and (ld is None or ld >= n):
+            return t, t.numel() // n, n, (n if ld is None else ld)
+    t = t.contiguous()
+    return t, (t.numel() // n if n else 0), n, n
+
+
+def _param(p: torch.Tensor | None, n: int, like: torch.Tensor, name: str) -> int | None:
+    if p is None:
+        return None
+    if p.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {p.dtype}")
+    if p.shape != (n,) or not p.is_contiguous() or p.device != like.device:
+        raise ValueError(f"{name} must be a contiguous tensor of {n} values on {like.device}")
+    return p.data_ptr()
+
+
+def _out_rows(out: torch.Tensor | None, x: torch.Tensor, name: str):
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        return out, x.shape[-1]
+    _same(x, out, "x", name)
+    view, _, _, ld = as_rows(out, name)
+    if view is not out:
+        raise ValueError(f"{name} must have contiguous rows at a constant distance")
+    return out, ld
+
+
+def _param_code(weight, bias, x) -> int:
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError(f"weight and bias have different dtypes ({weight.dtype}, {bias.dtype})")
+    p = weight if weight is not None else bias
+    return _dtype_code(x if p is None else p)
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None,
+                   bias: torch.Tensor | None = None, eps: float = EPS,
+                   out: torch.Tensor | None = None
+                   ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(y, mean, rstd): y like x, mean and rstd float32, one value a row."""
+    code = _dtype_code(x)
+    x, rows, n, ldx = as_rows(x, "x")
+    wp, bp = _param(weight, n, x, "weight"), _param(bias, n, x, "bias")
+    pcode = _param_code(weight, bias, x)
+    y, ldy = _out_rows(out, x, "out")
+    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
+    mean, rstd = stats[0], stats[1]
+    with _current(x.device):
+        st = _lib.library().layer_norm_fwd(x.data_ptr(), ldx, wp, bp, rows, n, float(eps),
+                                           y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(),
+                                           code, pcode, _stream(x.device))
+    _lib.check(st, "layer_norm_fwd")
+    return y, mean, rstd
+
+
+def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   weight: torch.Tensor | None = None, need_params: bool = True,
+                   out: torch.Tensor | None = None, shared: SharedBuffer | None = None
+                   ) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor | None]:
+    """(dx, dweight, dbias) from the input, the upstream gradient and the
+    statistics the forward returned.  dweight and dbias have weight's dtype
+    (x's without a weight); None if ``need_params`` is False.  ``shared``
+    lends its workspace."""
+    _require_device(x, "x")
+    _require_device(dy, "dy")
+    _same(x, dy, "x", "dy")
+    code = _dtype_code(x)
+    x, rows, n, ldx = as_rows(x, "x")
+    dy, _, _, lddy = as_rows(dy, "dy")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or t.device != x.device or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape "
+                             f"{tuple(x.shape[:-1])} on {x.device}")
+    wp = _param(weight, n, x, "weight")
+    pcode = _param_code(weight, None, x)
+    dx, lddx = _out_rows(out, x, "out")
+    dw = db = ws = None
+    if need_params:
+        params = torch.empty((2, n), dtype=x.dtype if weight is None else weight.dtype,
+                             device=x.device)
+        dw, db = params[0], params[1]
+        nbytes = _lib.library().layer_norm_workspace_bytes(rows, n)
+        ws = (shared or SharedBuffer()).workspace(nbytes, x.device)
+    with _current(x.device):
+        st = _lib.library().layer_norm_bwd(
+            x.data_ptr(), ldx, dy.data_ptr(), lddy, mean.data_ptr(), rstd.data_ptr(), wp, rows, n,
+            dx.data_ptr(), lddx, dw.data_ptr() if need_params else None,
+            db.data_ptr() if need_params else None, ws.data_ptr() if need_params else None,
+            ws.numel() if need_params else 0, code, pcode, _stream(x.device))
+    _lib.check(st, "layer_norm_bwd")
+    return dx, dw, db
+
+
+class LayerNormFn(torch.autograd.Function):
+    """Layer normalization keeping x and two values a row."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, shared):
+        y, mean, rstd = layer_norm_fwd(x, weight, bias, eps)
+        ctx.save_for_backward(x, mean, rstd, weight)
+        ctx.shared = shared
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, mean, rstd, weight = ctx.saved_tensors
+        need_w, need_b = ctx.needs_input_grad[1:3]
+        dx, dw, db = layer_norm_bwd(x, dy, mean, rstd, weight, need_w or need_b,
+                                    shared=ctx.shared)
+        return (dx, dw if need_w else None, db.to(ctx.bias_dtype) if need_b else None, None, None)
+
+
+class LayerNorm(nn.Module):
+    """Layer normalization over the last dimension (n values), with weight
+    and, unless ``bias`` is False, bias."""
+
+    def __init__(self, n: int, eps: float = EPS, bias: bool = True,
+                 shared: SharedBuffer | None = None, dtype: torch.dtype = torch.float32):
+        super().__init__()
+        self.weight = nn.Parameter(torch.ones(n, dtype=dtype))
+        self.bias = nn.Parameter(torch.zeros(n, dtype=dtype)) if bias else None
+        self.eps, self.shared = float(eps), shared
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return LayerNormFn.apply(x, self.weight, self.bias, self.eps, self.shared)
+
+    def extra_repr(self) -> str:
+        return f"{self.weight.numel()}, eps={self.eps}, bias={self.bias is not None}"
