@@ -51,6 +51,7 @@ template <typename T>
 struct GemmArgs {
     Operand<T> p, q;
     int k;        // length of the sum (of each half, kDx)
+    int q_cols;   // kDw: columns of q that may be read (padded)
     int tiles_m, tiles_n;
     T* out[2];    // h, or dg and du; dx; dWg and dWu
     int64_t ldo[2];
@@ -207,18 +208,14 @@ __device__ __forceinline__ void epi_get(const float* p, float* f)
     }
 }
 
-// Rows m0 .. m0 + 31 of the output; kUp: hidden units n0 .. n0 + 31 from
-// both accumulators; otherwise columns n0 .. n0 + 63.
+// Rows m0 .. m0 + 31 of the output, from the wave's LDS rows; kUp: hidden
+// units n0 .. n0 + 31 of g and u; otherwise columns n0 .. n0 + 63.
 template <typename T, int MODE, bool BWD>
-__device__ __forceinline__ void epilogue(const GemmArgs<T>& a, float* lds, int64_t m0, int n0,
-                                         int plane, f32x16 c0, f32x16 c1)
+__device__ __forceinline__ void epi_rows(const GemmArgs<T>& a, const float* lds, int64_t m0, int n0,
+                                         int plane)
 {
     constexpr int E = Elem<T>::kPerVec;
     const int l = threadIdx.x % 64;
-    wave_sync();  // the previous rows have been read
-    epi_put(lds, 0, c0);
-    epi_put(lds, 32, c1);
-    wave_sync();
     if constexpr (MODE == kUp) {
         constexpr int PER_ROW = 32 / E, ROWS = 64 / PER_ROW;
 #pragma unroll 1
@@ -262,6 +259,26 @@ __device__ __forceinline__ void epilogue(const GemmArgs<T>& a, float* lds, int64
             epi_get<E>(lds + r * kEpiStride + c, f);
             store_chunk(a.out[plane] + m * a.ldo[plane], n, a.out_cols, f);
         }
+    }
+}
+
+// The whole wave's results, 32 rows at a time.  The loop stays a loop (the
+// activations' code once); which accumulators it takes is a uniform branch.
+template <typename T, int MODE, bool BWD, int MT>
+__device__ __forceinline__ void epilogue(const GemmArgs<T>& a, float* lds, int64_t m0, int n0,
+                                         int plane, const f32x16 (&acc)[MT][2])
+{
+#pragma unroll 1
+    for (int i = 0; i < MT; ++i) {
+        wave_sync();  // the previous rows have been read
+#pragma unroll
+        for (int k = 0; k < MT; ++k)
+            if (k == i) {
+                epi_put(lds, 0, acc[k][0]);
+                epi_put(lds, 32, acc[k][1]);
+            }
+        wave_sync();
+        epi_rows<T, MODE, BWD>(a, lds, m0 + 32 * i, n0, plane);
     }
 }
 
@@ -435,10 +452,252 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
     }
     __syncthreads();
     float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
+    epilogue<T, MODE, BWD, 2>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
+}
+
+// ---------------------------------------------------------------------------
+// Products of matrices whose rows start on 16-byte boundaries.  WM x WN waves
+// of (32 MT) x 64 results each; k in steps of 128 bytes.  Operands go from
+// memory to LDS directly (buffer loads with the LDS bit, 16 bytes a lane),
+// two tiles of each operand in LDS: while one is multiplied the next one
+// arrives.
+//
+// A load writes 1 KiB of LDS in lane order, so the layouts that avoid bank
+// conflicts are made by choosing which 16 bytes each lane fetches:
+//   k contiguous: rows of 128 bytes; 16-byte slot s of row r holds chunk
+//     s ^ (r / 2 % 8).  A wave's 16-byte reads take one chunk of 32 rows; any
+//     16 consecutive rows then cover all 64 banks once.
+//   n contiguous: a k row holds the tile's columns; 64-byte unit c of row k
+//     holds unit c ^ (k % 4) (bf16; ^ 2 (k / 4 % 2) for binary32).  A
+//     transposing read takes 64 bytes of 4 consecutive rows: again all banks.
+// Chunks past the end of the sum lie outside the buffer descriptor's range
+// (or are pointed there), which reads as zero.  Rows and columns past an
+// edge repeat the last one: their results are not stored.
+// ---------------------------------------------------------------------------
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+constexpr uint32_t kBufferBytes = 0xc0000000u;  // no tile reaches this far
+constexpr uint32_t kOutside = 0xf0000000u;
+
+__device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t offset, i32x4 rsrc)
+{
+    // The wait for it is explicit (wait_loads) and ends before a barrier.
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(rsrc)
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+__device__ __forceinline__ i32x4 buffer(const void* p, uint32_t bytes)
+{
+    const uint64_t a = (uint64_t)p;
+    i32x4 r = {(int)(uint32_t)a, (int)(uint32_t)((a >> 32) & 0xffff), (int)bytes, 0x00020000};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        epilogue<T, MODE, BWD>(a, epi, m0 + wm + 32 * i, n0 + (MODE == kUp ? wn / 2 : wn), plane,
-                               acc[i][0], acc[i][1]);
+    for (int i = 0; i < 4; ++i)
+        r[i] = __builtin_amdgcn_readfirstlane(r[i]);
+    return r;
+}
+
+// A tile of ROWS values of m or n and 128 bytes of k, filled by WAVES waves.
+template <typename T, bool KC, int ROWS, int WAVES>
+struct FastTile {
+    static constexpr int E = Elem<T>::kPerVec;
+    static constexpr int kK = 128 / sizeof(T);
+    static constexpr int kBytes = ROWS * 128;
+    static constexpr int kRowBytes = KC ? 128 : ROWS * (int)sizeof(T);
+    static constexpr int kLoads = kBytes / 1024 / WAVES;  // of a wave
+    static_assert(kLoads * WAVES * 1024 == kBytes, "whole loads");
+
+    __device__ static int swizzle(int r)  // of 16-byte slots
+    {
+        return KC ? r / 2 % 8 : sizeof(T) == 2 ? r % 4 * 4 : r / 4 % 2 * 8;
+    }
+    // This lane's part of load i: the tile row it falls in and the chunk of it.
+    __device__ static int row(int wave, int i)
+    {
+        return ((wave * kLoads + i) * 1024 + (int)(threadIdx.x % 64) * 16) / kRowBytes;
+    }
+    __device__ static int chunk(int wave, int i)
+    {
+        static_assert(kRowBytes <= 1024, "a load covers whole rows");
+        return (int)(threadIdx.x % 64) * 16 % kRowBytes / 16 ^ swizzle(row(wave, i));
+    }
+    __device__ static typename Step<T>::Frag frag(const char* lds, int step, int row0)
+    {
+        const int l = threadIdx.x % 64;
+        if constexpr (KC) {
+            const int r = row0 + l % 32;
+            return *reinterpret_cast<const typename Step<T>::Frag*>(
+                lds + r * 128 + ((step * 2 + l / 32) ^ swizzle(l % 32)) * 16);
+        } else if constexpr (sizeof(T) == 2) {
+            const int g = l / 16;
+            const int k = step * 16 + 8 * (g >> 1) + l % 16 / 4;
+            const char* p = lds + k * kRowBytes + ((row0 / 8) ^ swizzle(l % 16 / 4)) * 16 +
+                            (16 * (g & 1) + 4 * (l % 4)) * 2;
+            const i16x4 lo = lds_transpose(p), hi = lds_transpose(p + 4 * kRowBytes);
+            typedef short i16x8 __attribute__((ext_vector_type(8)));
+            const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(bf16x8, v);
+        } else {
+            const int k = step * 8 + 4 * (l / 32);
+            const char* p = lds + k * kRowBytes + ((row0 / 4) ^ swizzle(4 * (l / 32))) * 16 +
+                            l % 32 * 4;
+            f32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = *reinterpret_cast<const float*>(p + j * kRowBytes);
+            return v;
+        }
+    }
+};
+
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT>
+__global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<T> a)
+{
+    constexpr bool PK = MODE == kUp, QK = MODE != kDw;
+    constexpr int BM = WM * MT * 32, BN = WN * 64, WAVES = WM * WN;
+    using PT = FastTile<T, PK, BN, WAVES>;
+    using QT = FastTile<T, QK, BM, WAVES>;
+    constexpr int kK = PT::kK, E = Elem<T>::kPerVec, STEPS = kK / Step<T>::kK;
+    constexpr int kStage = PT::kBytes + QT::kBytes;
+    constexpr int kLds = 2 * kStage > WAVES * kEpiBytes ? 2 * kStage : WAVES * kEpiBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[kLds];
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(MEBLOCK_LDS char*)lds;
+
+    int tm, tn, plane = 0;
+    if constexpr (MODE == kDw) {
+        tile_of_block(2 * a.tiles_m, a.tiles_n, tm, tn);
+        plane = tm >= a.tiles_m;
+        tm -= plane * a.tiles_m;
+    } else {
+        tile_of_block(a.tiles_m, a.tiles_n, tm, tn);
+    }
+    const int64_t m0 = (int64_t)tm * BM;
+    const int n0 = tn * (MODE == kUp ? BN / 2 : BN);
+    const int steps = (a.k + kK - 1) / kK;
+    const int total = MODE == kDx ? 2 * steps : steps;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+
+    // Offsets of this lane's 16 bytes in each load, from the tile's first
+    // element; (kUp) Wu's from Wu's own first row.
+    uint32_t offp[PT::kLoads], offq[QT::kLoads];
+#pragma unroll
+    for (int i = 0; i < PT::kLoads; ++i) {
+        const int r = PT::row(wave, i), c = PT::chunk(wave, i) * E;
+        if constexpr (MODE == kUp) {
+            // Rows of the tile: 32 of Wg, 32 of Wu, in turn.
+            int n = r / 64 * 32 + r % 32;
+            n = n0 + n < a.p.rows ? n : a.p.rows - 1 - n0;
+            offp[i] = (uint32_t)((int64_t)n * a.p.ld[r / 32 % 2] + c) * (uint32_t)sizeof(T);
+        } else {
+            const int n = n0 + c < a.p.rows ? c : a.p.rows - E - n0;
+            offp[i] = (uint32_t)((int64_t)r * a.p.ld[0] + n) * (uint32_t)sizeof(T);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < QT::kLoads; ++i) {
+        const int r = QT::row(wave, i), c = QT::chunk(wave, i) * E;
+        if constexpr (QK) {
+            const int m = m0 + r < a.q.rows ? r : (int)(a.q.rows - 1 - m0);
+            offq[i] = (uint32_t)((int64_t)m * a.q.ld[0] + c) * (uint32_t)sizeof(T);
+        } else {
+            const int m = m0 + c < a.q_cols ? c : (int)(a.q_cols - E - m0);
+            offq[i] = (uint32_t)((int64_t)r * a.q.ld[0] + m) * (uint32_t)sizeof(T);
+        }
+    }
+
+    // Loads of step s into half `stage` of the LDS.
+    auto issue = [&](int s, int stage) {
+        const int seg = MODE == kDx && s >= steps;
+        const int k0 = (s - seg * steps) * kK;
+        const uint32_t lp = lds0 + stage * kStage + wave * (PT::kLoads * 1024);
+        const uint32_t lq = lds0 + stage * kStage + PT::kBytes + wave * (QT::kLoads * 1024);
+        // What is left of the sum, in bytes from the tile's first k row.
+        auto left = [&](int64_t ld, int64_t cols) {
+            const int64_t b = ((int64_t)(a.k - k0 - 1) * ld + cols) * (int64_t)sizeof(T);
+            return (uint32_t)(b < (int64_t)kBufferBytes ? b : (int64_t)kBufferBytes);
+        };
+        if constexpr (MODE == kUp) {
+            const i32x4 bg = buffer(a.p.base[0] + (int64_t)n0 * a.p.ld[0] + k0, kBufferBytes);
+            const i32x4 bu = buffer(a.p.base[1] + (int64_t)n0 * a.p.ld[1] + k0, kBufferBytes);
+#pragma unroll
+            for (int i = 0; i < PT::kLoads; ++i) {
+                // A load covers 8 rows: of one of the two weights.
+                const int which = (wave * PT::kLoads + i) * 8 / 32 % 2;
+                const uint32_t o = k0 + PT::chunk(wave, i) * E < a.k ? offp[i] : kOutside;
+                load_lds16(lp + i * 1024, o, which ? bu : bg);
+            }
+        } else {
+            const int64_t ld = a.p.ld[seg];
+            const i32x4 b = buffer(a.p.base[seg] + (int64_t)k0 * ld + n0, left(ld, a.p.rows - n0));
+#pragma unroll
+            for (int i = 0; i < PT::kLoads; ++i)
+                load_lds16(lp + i * 1024, offp[i], b);
+        }
+        if constexpr (QK) {
+            const i32x4 b = buffer(a.q.base[seg] + m0 * a.q.ld[seg] + k0, kBufferBytes);
+#pragma unroll
+            for (int i = 0; i < QT::kLoads; ++i) {
+                // kDx: the rows of dg and du are padded to whole steps.
+                const uint32_t o =
+                    MODE == kDx || k0 + QT::chunk(wave, i) * E < a.k ? offq[i] : kOutside;
+                load_lds16(lq + i * 1024, o, b);
+            }
+        } else {
+            const int64_t ld = a.q.ld[plane];
+            const i32x4 b =
+                buffer(a.q.base[plane] + (int64_t)k0 * ld + m0, left(ld, a.q_cols - m0));
+#pragma unroll
+            for (int i = 0; i < QT::kLoads; ++i)
+                load_lds16(lq + i * 1024, offq[i], b);
+        }
+    };
+
+    const int wm = wave / WN * (MT * 32), wn = wave % WN * 64;
+    f32x16 acc[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            acc[i][j] = f32x16{};
+    if (total > 0)
+        issue(0, 0);
+    for (int s = 0; s < total; ++s) {
+        if (s + 1 < total) {
+            issue(s + 1, (s + 1) & 1);
+            wait_loads<PT::kLoads + QT::kLoads>();
+        } else {
+            wait_loads<0>();
+        }
+        __builtin_amdgcn_s_barrier();  // every wave's part of this step is there
+        const char* lp = lds + (s & 1) * kStage;
+        const char* lq = lp + PT::kBytes;
+#pragma unroll
+        for (int t = 0; t < STEPS; ++t) {
+            typename Step<T>::Frag fp[2], fq[MT];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                fp[j] = PT::frag(lp, t, wn + 32 * j);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                fq[i] = QT::frag(lq, t, wm + 32 * i);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = Step<T>::mma(fp[j], fq[i], acc[i][j]);
+        }
+        // Reads have arrived before another wave may load over them.
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        __builtin_amdgcn_s_barrier();
+    }
+    float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
+    epilogue<T, MODE, BWD, MT>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -504,20 +763,60 @@ static bool matrix_ok(const void* p, size_t rows, size_t cols, size_t ld, size_t
 
 static size_t padded(size_t hidden) { return (hidden + 63) / 64 * 64; }
 
-template <typename T, int MODE, bool BWD>
-static int gemm_run(GemmArgs<T>& a, hipStream_t stream)
+template <typename T, int MODE>
+static int gemm_launch(GemmArgs<T>& a, const void* fn, int bm, int bn, int block,
+                       hipStream_t stream)
 {
-    const int cols = MODE == kUp ? kAnyTile / 2 : kAnyTile;
-    a.tiles_m = (a.q.rows + kAnyTile - 1) / kAnyTile;
+    const int cols = MODE == kUp ? bn / 2 : bn;
+    a.tiles_m = (a.q.rows + bm - 1) / bm;
     a.tiles_n = (a.out_cols + cols - 1) / cols;
     const int64_t grid = (int64_t)a.tiles_m * a.tiles_n * (MODE == kDw ? 2 : 1);
     if (grid == 0)
         return MESWISH_OK;
-    if (grid >= ((int64_t)1 << 24))
+    if (grid >= ((int64_t)1 << 23))
         return MESWISH_EINVAL;
     void* args[] = {&a};
-    return launch(reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD>),
-                  dim3((unsigned)grid), 256, args, stream);
+    return launch(fn, dim3((unsigned)grid), block, args, stream);
+}
+
+// Every row of the operands starts on a 16-byte boundary and the loads' 16
+// bytes lie whole in or out of it.
+template <typename T, int MODE>
+static bool aligned_rows(const GemmArgs<T>& a)
+{
+    constexpr int64_t E = Elem<T>::kPerVec;
+    if ((MODE == kUp ? a.k : a.p.rows) % E)
+        return false;
+    for (int i = 0; i < 2; ++i)
+        if (!aligned(a.p.base[i], 16) || !aligned(a.q.base[i], 16) || a.p.ld[i] % E ||
+            a.q.ld[i] % E)
+            return false;
+    // One offset serves both matrices of a sum.
+    return MODE != kDx || (a.p.ld[0] == a.p.ld[1] && a.q.ld[0] == a.q.ld[1]);
+}
+
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT>
+static int gemm_fast(GemmArgs<T>& a, hipStream_t stream)
+{
+    return gemm_launch<T, MODE>(
+        a, reinterpret_cast<const void*>(&gemm_fast_kernel<T, MODE, BWD, WM, WN, MT>), WM * MT * 32,
+        WN * 64, WM * WN * 64, stream);
+}
+
+template <typename T, int MODE, bool BWD>
+static int gemm_run(GemmArgs<T>& a, hipStream_t stream)
+{
+    if (aligned_rows<T, MODE>(a)) {
+        const int cols = MODE == kUp ? 128 : 256;
+        const int64_t big = (int64_t)((a.q.rows + 255) / 256) * ((a.out_cols + cols - 1) / cols) *
+                            (MODE == kDw ? 2 : 1);
+        if (big >= 256)
+            return gemm_fast<T, MODE, BWD, 2, 4, 4>(a, stream);
+        return gemm_fast<T, MODE, BWD, 2, 2, 2>(a, stream);
+    }
+    return gemm_launch<T, MODE>(
+        a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD>), kAnyTile, kAnyTile, 256,
+        stream);
 }
 
 template <typename T>
@@ -584,6 +883,7 @@ static int bwd(int act, float param, const void* x, size_t ldx, const void* wg, 
         b.p = operand<T>(x, ldx, x, ldx, dim);
         b.q = operand<T>(dg, fp, du, fp, hidden);
         b.k = (int)tokens;
+        b.q_cols = (int)fp;
         b.out[0] = static_cast<T*>(dwg);
         b.out[1] = static_cast<T*>(dwu);
         b.ldo[0] = (int64_t)lddwg;
