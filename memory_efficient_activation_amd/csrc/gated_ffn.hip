@@ -611,52 +611,58 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
         }
     }
 
-    // Loads of step s into half `stage` of the LDS.
-    auto issue = [&](int s, int stage) {
+    // The loads of a step into half `stage` of the LDS, one at a time: what
+    // they share is in scalar registers.
+    struct Loads {
+        i32x4 p, q;
+        uint32_t lp, lq;
+        int k0;
+    };
+    auto prepare = [&](int s, int stage) {
+        Loads d;
         const int seg = MODE == kDx && s >= steps;
-        const int k0 = (s - seg * steps) * kK;
-        const uint32_t lp = lds0 + stage * kStage + wave * (PT::kLoads * 1024);
-        const uint32_t lq = lds0 + stage * kStage + PT::kBytes + wave * (QT::kLoads * 1024);
+        d.k0 = (s - seg * steps) * kK;
+        d.lp = lds0 + stage * kStage + wave * (PT::kLoads * 1024);
+        d.lq = lds0 + stage * kStage + PT::kBytes + wave * (QT::kLoads * 1024);
         // What is left of the sum, in bytes from the tile's first k row.
         auto left = [&](int64_t ld, int64_t cols) {
-            const int64_t b = ((int64_t)(a.k - k0 - 1) * ld + cols) * (int64_t)sizeof(T);
+            const int64_t b = ((int64_t)(a.k - d.k0 - 1) * ld + cols) * (int64_t)sizeof(T);
             return (uint32_t)(b < (int64_t)kBufferBytes ? b : (int64_t)kBufferBytes);
         };
         if constexpr (MODE == kUp) {
-            const i32x4 bg = buffer(a.p.base[0] + (int64_t)n0 * a.p.ld[0] + k0, kBufferBytes);
-            const i32x4 bu = buffer(a.p.base[1] + (int64_t)n0 * a.p.ld[1] + k0, kBufferBytes);
-#pragma unroll
-            for (int i = 0; i < PT::kLoads; ++i) {
-                // A load covers 8 rows: of one of the two weights.
-                const int which = (wave * PT::kLoads + i) * 8 / 32 % 2;
-                const uint32_t o = k0 + PT::chunk(wave, i) * E < a.k ? offp[i] : kOutside;
-                load_lds16(lp + i * 1024, o, which ? bu : bg);
-            }
+            // A load covers 8 rows, a wave at most 32: of one of the weights.
+            static_assert(PT::kLoads <= 4, "a wave loads one weight");
+            const bool up = wave * PT::kLoads / 4 % 2;
+            const T* w = up ? a.p.base[1] : a.p.base[0];
+            d.p = buffer(w + (int64_t)n0 * (up ? a.p.ld[1] : a.p.ld[0]) + d.k0, kBufferBytes);
         } else {
             const int64_t ld = a.p.ld[seg];
-            const i32x4 b = buffer(a.p.base[seg] + (int64_t)k0 * ld + n0, left(ld, a.p.rows - n0));
-#pragma unroll
-            for (int i = 0; i < PT::kLoads; ++i)
-                load_lds16(lp + i * 1024, offp[i], b);
+            d.p = buffer(a.p.base[seg] + (int64_t)d.k0 * ld + n0, left(ld, a.p.rows - n0));
         }
         if constexpr (QK) {
-            const i32x4 b = buffer(a.q.base[seg] + m0 * a.q.ld[seg] + k0, kBufferBytes);
-#pragma unroll
-            for (int i = 0; i < QT::kLoads; ++i) {
-                // kDx: the rows of dg and du are padded to whole steps.
-                const uint32_t o =
-                    MODE == kDx || k0 + QT::chunk(wave, i) * E < a.k ? offq[i] : kOutside;
-                load_lds16(lq + i * 1024, o, b);
-            }
+            d.q = buffer(a.q.base[seg] + m0 * a.q.ld[seg] + d.k0, kBufferBytes);
         } else {
             const int64_t ld = a.q.ld[plane];
-            const i32x4 b =
-                buffer(a.q.base[plane] + (int64_t)k0 * ld + m0, left(ld, a.q_cols - m0));
-#pragma unroll
-            for (int i = 0; i < QT::kLoads; ++i)
-                load_lds16(lq + i * 1024, offq[i], b);
+            d.q = buffer(a.q.base[plane] + (int64_t)d.k0 * ld + m0, left(ld, a.q_cols - m0));
+        }
+        return d;
+    };
+    auto issue = [&](const Loads& d, int i) {
+        if (i < PT::kLoads) {
+            uint32_t o = offp[i];
+            if constexpr (MODE == kUp)
+                o = d.k0 + PT::chunk(wave, i) * E < a.k ? o : kOutside;
+            load_lds16(d.lp + i * 1024, o, d.p);
+        } else {
+            i -= PT::kLoads;
+            uint32_t o = offq[i];
+            // kDx: the rows of dg and du are padded to whole steps.
+            if constexpr (MODE == kUp)
+                o = d.k0 + QT::chunk(wave, i) * E < a.k ? o : kOutside;
+            load_lds16(d.lq + i * 1024, o, d.q);
         }
     };
+    constexpr int kLoads = PT::kLoads + QT::kLoads;
 
     const int wm = wave / WN * (MT * 32), wn = wave % WN * 64;
     f32x16 acc[MT][2];
@@ -665,37 +671,75 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             acc[i][j] = f32x16{};
-    if (total > 0)
-        issue(0, 0);
-    for (int s = 0; s < total; ++s) {
-        if (s + 1 < total) {
-            issue(s + 1, (s + 1) & 1);
-            wait_loads<PT::kLoads + QT::kLoads>();
+
+    // Two sets of fragments: one is multiplied while the next is read.
+    typename Step<T>::Frag fp[2][2], fq[2][MT];
+    auto read = [&](int set, int stage, int t) {
+        const char* lp = lds + stage * kStage;
+        const char* lq = lp + PT::kBytes;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            fp[set][j] = PT::frag(lp, t, wn + 32 * j);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            fq[set][i] = QT::frag(lq, t, wm + 32 * i);
+    };
+    static_assert(STEPS % 2 == 0, "fragment sets alternate across steps");
+
+    if (total > 0) {
+        const Loads d = prepare(0, 0);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            issue(d, i);
+        if (total > 1) {
+            const Loads e = prepare(1, 1);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                issue(e, i);
+            wait_loads<kLoads>();
         } else {
             wait_loads<0>();
         }
-        __builtin_amdgcn_s_barrier();  // every wave's part of this step is there
-        const char* lp = lds + (s & 1) * kStage;
-        const char* lq = lp + PT::kBytes;
+        __builtin_amdgcn_s_barrier();
+        read(0, 0, 0);
+    }
+    // Step s: its first fragments are in registers; its last are multiplied
+    // after the barrier behind which step s + 1 is in LDS and the half of
+    // step s is free for step s + 2.
+    for (int s = 0; s < total; ++s) {
+        const int stage = s & 1;
 #pragma unroll
-        for (int t = 0; t < STEPS; ++t) {
-            typename Step<T>::Frag fp[2], fq[MT];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                fp[j] = PT::frag(lp, t, wn + 32 * j);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                fq[i] = QT::frag(lq, t, wm + 32 * i);
+        for (int t = 0; t < STEPS - 1; ++t) {
+            read((t + 1) & 1, stage, t + 1);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    acc[i][j] = Step<T>::mma(fp[j], fq[i], acc[i][j]);
+                    acc[i][j] = Step<T>::mma(fp[t & 1][j], fq[t & 1][i], acc[i][j]);
         }
-        // Reads have arrived before another wave may load over them.
-        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
         __builtin_amdgcn_s_barrier();
+        const bool more = s + 2 < total;
+        Loads d;
+        if (more)
+            d = prepare(s + 2, stage);
+        if (s + 1 < total)
+            read(0, stage ^ 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[i][j] = Step<T>::mma(fp[1][j], fq[1][i], acc[i][j]);
+            if (more) {
+#pragma unroll
+                for (int k = i * kLoads / MT; k < (i + 1) * kLoads / MT; ++k)
+                    issue(d, k);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
+    __syncthreads();
     float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
     epilogue<T, MODE, BWD, MT>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
 }
