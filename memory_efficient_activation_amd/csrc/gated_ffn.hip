@@ -474,6 +474,14 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
 // (or are pointed there), which reads as zero.  Rows and columns past an
 // edge repeat the last one: their results are not stored.
 // ---------------------------------------------------------------------------
+#ifndef BIG_KB
+#define BIG_KB 128
+#define BIG_NS 2
+#endif
+#ifndef SMALL_KB
+#define SMALL_KB 128
+#define SMALL_NS 2
+#endif
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr uint32_t kBufferBytes = 0xc0000000u;  // no tile reaches this far
 constexpr uint32_t kOutside = 0xf0000000u;
@@ -503,19 +511,19 @@ __device__ __forceinline__ i32x4 buffer(const void* p, uint32_t bytes)
     return r;
 }
 
-// A tile of ROWS values of m or n and 128 bytes of k, filled by WAVES waves.
-template <typename T, bool KC, int ROWS, int WAVES>
+// A tile of ROWS values of m or n and KB bytes of k, filled by WAVES waves.
+template <typename T, bool KC, int ROWS, int WAVES, int KB>
 struct FastTile {
     static constexpr int E = Elem<T>::kPerVec;
-    static constexpr int kK = 128 / sizeof(T);
-    static constexpr int kBytes = ROWS * 128;
-    static constexpr int kRowBytes = KC ? 128 : ROWS * (int)sizeof(T);
+    static constexpr int kK = KB / sizeof(T);
+    static constexpr int kBytes = ROWS * KB;
+    static constexpr int kRowBytes = KC ? KB : ROWS * (int)sizeof(T);
     static constexpr int kLoads = kBytes / 1024 / WAVES;  // of a wave
     static_assert(kLoads * WAVES * 1024 == kBytes, "whole loads");
 
     __device__ static int swizzle(int r)  // of 16-byte slots
     {
-        return KC ? r / 2 % 8 : sizeof(T) == 2 ? r % 4 * 4 : r / 4 % 2 * 8;
+        return KC ? (KB == 128 ? r / 2 % 8 : r / 4 % 4) : sizeof(T) == 2 ? r % 4 * 4 : r / 4 % 2 * 8;
     }
     // This lane's part of load i: the tile row it falls in and the chunk of it.
     __device__ static int row(int wave, int i)
@@ -533,7 +541,7 @@ struct FastTile {
         if constexpr (KC) {
             const int r = row0 + l % 32;
             return *reinterpret_cast<const typename Step<T>::Frag*>(
-                lds + r * 128 + ((step * 2 + l / 32) ^ swizzle(l % 32)) * 16);
+                lds + r * KB + ((step * 2 + l / 32) ^ swizzle(l % 32)) * 16);
         } else if constexpr (sizeof(T) == 2) {
             const int g = l / 16;
             const int k = step * 16 + 8 * (g >> 1) + l % 16 / 4;
@@ -556,16 +564,16 @@ struct FastTile {
     }
 };
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT>
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int KB, int NS>
 __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<T> a)
 {
     constexpr bool PK = MODE == kUp, QK = MODE != kDw;
     constexpr int BM = WM * MT * 32, BN = WN * 64, WAVES = WM * WN;
-    using PT = FastTile<T, PK, BN, WAVES>;
-    using QT = FastTile<T, QK, BM, WAVES>;
+    using PT = FastTile<T, PK, BN, WAVES, KB>;
+    using QT = FastTile<T, QK, BM, WAVES, KB>;
     constexpr int kK = PT::kK, E = Elem<T>::kPerVec, STEPS = kK / Step<T>::kK;
     constexpr int kStage = PT::kBytes + QT::kBytes;
-    constexpr int kLds = 2 * kStage > WAVES * kEpiBytes ? 2 * kStage : WAVES * kEpiBytes;
+    constexpr int kLds = NS * kStage > WAVES * kEpiBytes ? NS * kStage : WAVES * kEpiBytes;
     __shared__ __attribute__((aligned(1024))) char lds[kLds];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(MEBLOCK_LDS char*)lds;
 
@@ -611,58 +619,82 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
         }
     }
 
-    // The loads of a step into half `stage` of the LDS, one at a time: what
-    // they share is in scalar registers.
-    struct Loads {
-        i32x4 p, q;
-        uint32_t lp, lq;
-        int k0;
-    };
-    auto prepare = [&](int s, int stage) {
-        Loads d;
-        const int seg = MODE == kDx && s >= steps;
-        d.k0 = (s - seg * steps) * kK;
-        d.lp = lds0 + stage * kStage + wave * (PT::kLoads * 1024);
-        d.lq = lds0 + stage * kStage + PT::kBytes + wave * (QT::kLoads * 1024);
-        // What is left of the sum, in bytes from the tile's first k row.
-        auto left = [&](int64_t ld, int64_t cols) {
-            const int64_t b = ((int64_t)(a.k - d.k0 - 1) * ld + cols) * (int64_t)sizeof(T);
-            return (uint32_t)(b < (int64_t)kBufferBytes ? b : (int64_t)kBufferBytes);
-        };
+    // Where the next step's loads start, in scalar registers: address, bytes
+    // left of the sum from there (what lies past them reads as zero).
+    constexpr int kStepK = kK;
+    const char *curp, *curq;
+    int64_t incp, incq, leftp, leftq;
+    auto start = [&](int seg) {
         if constexpr (MODE == kUp) {
-            // A load covers 8 rows, a wave at most 32: of one of the weights.
-            static_assert(PT::kLoads <= 4, "a wave loads one weight");
-            const bool up = wave * PT::kLoads / 4 % 2;
+            // A wave's loads of P are of one of the weights.
+            constexpr int kTurn = 32 * KB / 1024;  // loads of one weight's 32 rows
+            static_assert(kTurn % PT::kLoads == 0, "a wave loads one weight");
+            const bool up = wave * PT::kLoads / kTurn % 2;
             const T* w = up ? a.p.base[1] : a.p.base[0];
-            d.p = buffer(w + (int64_t)n0 * (up ? a.p.ld[1] : a.p.ld[0]) + d.k0, kBufferBytes);
+            const int64_t ld = up ? a.p.ld[1] : a.p.ld[0];
+            curp = reinterpret_cast<const char*>(w + (int64_t)n0 * ld);
+            incp = kStepK * (int64_t)sizeof(T);
+            leftp = kBufferBytes;
         } else {
-            const int64_t ld = a.p.ld[seg];
-            d.p = buffer(a.p.base[seg] + (int64_t)d.k0 * ld + n0, left(ld, a.p.rows - n0));
+            const int64_t ld = a.p.ld[0];
+            curp = reinterpret_cast<const char*>((seg ? a.p.base[1] : a.p.base[0]) + n0);
+            incp = kStepK * ld * (int64_t)sizeof(T);
+            leftp = ((int64_t)(a.k - 1) * ld + a.p.rows - n0) * (int64_t)sizeof(T);
         }
         if constexpr (QK) {
-            d.q = buffer(a.q.base[seg] + m0 * a.q.ld[seg] + d.k0, kBufferBytes);
+            curq = reinterpret_cast<const char*>((seg ? a.q.base[1] : a.q.base[0]) +
+                                                 m0 * a.q.ld[0]);
+            incq = kStepK * (int64_t)sizeof(T);
+            leftq = kBufferBytes;
         } else {
-            const int64_t ld = a.q.ld[plane];
-            d.q = buffer(a.q.base[plane] + (int64_t)d.k0 * ld + m0, left(ld, a.q_cols - m0));
-        }
-        return d;
-    };
-    auto issue = [&](const Loads& d, int i) {
-        if (i < PT::kLoads) {
-            uint32_t o = offp[i];
-            if constexpr (MODE == kUp)
-                o = d.k0 + PT::chunk(wave, i) * E < a.k ? o : kOutside;
-            load_lds16(d.lp + i * 1024, o, d.p);
-        } else {
-            i -= PT::kLoads;
-            uint32_t o = offq[i];
-            // kDx: the rows of dg and du are padded to whole steps.
-            if constexpr (MODE == kUp)
-                o = d.k0 + QT::chunk(wave, i) * E < a.k ? o : kOutside;
-            load_lds16(d.lq + i * 1024, o, d.q);
+            const int64_t ld = a.q.ld[0];
+            curq = reinterpret_cast<const char*>((plane ? a.q.base[1] : a.q.base[0]) + m0);
+            incq = kStepK * ld * (int64_t)sizeof(T);
+            leftq = ((int64_t)(a.k - 1) * ld + a.q_cols - m0) * (int64_t)sizeof(T);
         }
     };
+    i32x4 rp, rq;
+    int ahead = 0;  // the step whose loads come next
+    auto next_step = [&]() {
+        if (MODE == kDx ? ahead == 0 || ahead == steps : ahead == 0)
+            start(ahead != 0);
+        // Past the last step nothing is read (zeros are written).
+        const bool any = ahead < total;
+        auto bytes = [&](int64_t left) {
+            return any ? (uint32_t)(left < (int64_t)kBufferBytes ? left : (int64_t)kBufferBytes) : 0u;
+        };
+        rp = buffer(curp, bytes(leftp));
+        rq = buffer(curq, bytes(leftq));
+        curp += incp;
+        curq += incq;
+        if constexpr (!PK)
+            leftp -= incp;
+        if constexpr (!QK)
+            leftq -= incq;
+        if constexpr (MODE == kUp) {
+            // A last step that is cut short: chunks past the end are pointed
+            // outside, for good (no step follows).
+            if (ahead == total - 1 && a.k % kK) {
+                const int k0 = ahead * kK;
+#pragma unroll
+                for (int i = 0; i < PT::kLoads; ++i)
+                    offp[i] = k0 + PT::chunk(wave, i) * E < a.k ? offp[i] : kOutside;
+#pragma unroll
+                for (int i = 0; i < QT::kLoads; ++i)
+                    offq[i] = k0 + QT::chunk(wave, i) * E < a.k ? offq[i] : kOutside;
+            }
+        }
+        ++ahead;
+    };
+    const uint32_t ldsp = lds0 + wave * (PT::kLoads * 1024);
+    const uint32_t ldsq = lds0 + PT::kBytes + wave * (QT::kLoads * 1024);
     constexpr int kLoads = PT::kLoads + QT::kLoads;
+    auto issue = [&](uint32_t place, int i) {
+        if (i < PT::kLoads)
+            load_lds16(ldsp + place + i * 1024, offp[i], rp);
+        else
+            load_lds16(ldsq + place + (i - PT::kLoads) * 1024, offq[i - PT::kLoads], rq);
+    };
 
     const int wm = wave / WN * (MT * 32), wn = wave % WN * 64;
     f32x16 acc[MT][2];
@@ -674,71 +706,66 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
 
     // Two sets of fragments: one is multiplied while the next is read.
     typename Step<T>::Frag fp[2][2], fq[2][MT];
-    auto read = [&](int set, int stage, int t) {
-        const char* lp = lds + stage * kStage;
-        const char* lq = lp + PT::kBytes;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            fp[set][j] = PT::frag(lp, t, wn + 32 * j);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-            fq[set][i] = QT::frag(lq, t, wm + 32 * i);
+    constexpr int kFrags = 2 + MT;
+    auto read = [&](int set, uint32_t place, int t, int i) {
+        if (i < 2)
+            fp[set][i] = PT::frag(lds + place, t, wn + 32 * i);
+        else
+            fq[set][i - 2] = QT::frag(lds + place + PT::kBytes, t, wm + 32 * (i - 2));
     };
     static_assert(STEPS % 2 == 0, "fragment sets alternate across steps");
 
     if (total > 0) {
-        const Loads d = prepare(0, 0);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            issue(d, i);
-        if (total > 1) {
-            const Loads e = prepare(1, 1);
+        for (int s = 0; s < NS; ++s) {
+            next_step();
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                issue(e, i);
-            wait_loads<kLoads>();
-        } else {
-            wait_loads<0>();
+                issue(s * kStage, i);
         }
+        wait_loads<(NS - 1) * kLoads>();
         __builtin_amdgcn_s_barrier();
-        read(0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kFrags; ++i)
+            read(0, 0, 0, i);
     }
     // Step s: its first fragments are in registers; its last are multiplied
-    // after the barrier behind which step s + 1 is in LDS and the half of
-    // step s is free for step s + 2.
+    // after the barrier behind which step s + 1 is in LDS and the place of
+    // step s is free for step s + NS.  Reads and loads are spread between
+    // the products; the order is kept as written.
+    uint32_t place = 0;
+#pragma unroll 1
     for (int s = 0; s < total; ++s) {
-        const int stage = s & 1;
+        const uint32_t next = place + kStage == NS * kStage ? 0 : place + kStage;
 #pragma unroll
-        for (int t = 0; t < STEPS - 1; ++t) {
-            read((t + 1) & 1, stage, t + 1);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = Step<T>::mma(fp[t & 1][j], fq[t & 1][i], acc[i][j]);
-        }
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
-        __builtin_amdgcn_s_barrier();
-        const bool more = s + 2 < total;
-        Loads d;
-        if (more)
-            d = prepare(s + 2, stage);
-        if (s + 1 < total)
-            read(0, stage ^ 1, 0);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                acc[i][j] = Step<T>::mma(fp[1][j], fq[1][i], acc[i][j]);
-            if (more) {
-#pragma unroll
-                for (int k = i * kLoads / MT; k < (i + 1) * kLoads / MT; ++k)
-                    issue(d, k);
+        for (int t = 0; t < STEPS; ++t) {
+            const bool last = t == STEPS - 1;
+            if (last) {
+                next_step();
+                // Loads of steps s + 2 .. s + NS - 1 may stay in flight.
+                wait_loads<(NS - 2) * kLoads>();
+                asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+                __builtin_amdgcn_s_barrier();
             }
             __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                acc[i / 2][i % 2] = Step<T>::mma(fp[t & 1][i % 2], fq[t & 1][i / 2],
+                                                 acc[i / 2][i % 2]);
+#pragma unroll
+                for (int k = i * kFrags / (2 * MT); k < (i + 1) * kFrags / (2 * MT); ++k)
+                    read(~t & 1, last ? next : place, last ? 0 : t + 1, k);
+                if (last) {
+#pragma unroll
+                    for (int k = i * kLoads / (2 * MT); k < (i + 1) * kLoads / (2 * MT); ++k)
+                        issue(place, k);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
+        place = next;
     }
+    wait_loads<0>();
     __syncthreads();
     float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
     epilogue<T, MODE, BWD, MT>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
@@ -839,11 +866,11 @@ static bool aligned_rows(const GemmArgs<T>& a)
     return MODE != kDx || (a.p.ld[0] == a.p.ld[1] && a.q.ld[0] == a.q.ld[1]);
 }
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT>
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int KB, int NS>
 static int gemm_fast(GemmArgs<T>& a, hipStream_t stream)
 {
     return gemm_launch<T, MODE>(
-        a, reinterpret_cast<const void*>(&gemm_fast_kernel<T, MODE, BWD, WM, WN, MT>), WM * MT * 32,
+        a, reinterpret_cast<const void*>(&gemm_fast_kernel<T, MODE, BWD, WM, WN, MT, KB, NS>), WM * MT * 32,
         WN * 64, WM * WN * 64, stream);
 }
 
@@ -855,8 +882,8 @@ static int gemm_run(GemmArgs<T>& a, hipStream_t stream)
         const int64_t big = (int64_t)((a.q.rows + 255) / 256) * ((a.out_cols + cols - 1) / cols) *
                             (MODE == kDw ? 2 : 1);
         if (big >= 256)
-            return gemm_fast<T, MODE, BWD, 2, 4, 4>(a, stream);
-        return gemm_fast<T, MODE, BWD, 2, 2, 2>(a, stream);
+            return gemm_fast<T, MODE, BWD, 2, 4, 4, BIG_KB, BIG_NS>(a, stream);
+        return gemm_fast<T, MODE, BWD, 2, 2, 2, SMALL_KB, SMALL_NS>(a, stream);
     }
     return gemm_launch<T, MODE>(
         a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD>), kAnyTile, kAnyTile, 256,
