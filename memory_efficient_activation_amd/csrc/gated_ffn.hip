@@ -13,7 +13,7 @@
 //   kDw  dWg, dWu:  P = x (n contiguous), Q = dg, du (m contiguous),
 //        k = tokens.
 //
-// The matrix cores (v_mfma_f32_32x32x16_bf16, v_mfma_f32_32x32x2_f32) take
+// The matrix cores (v_mfma_f32_16x16x32_bf16, v_mfma_f32_16x16x4_f32) take
 // P as the operand whose rows index the four consecutive results a lane
 // holds, so a lane's results are consecutive along n.
 
@@ -34,7 +34,6 @@ enum Mode { kUp = 0, kDx = 1, kDw = 2 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 #define MEBLOCK_LDS __attribute__((address_space(3)))
 
@@ -138,29 +137,28 @@ __device__ __forceinline__ void gate_act(int act, float* g, float* u, float* d, 
 }
 
 // ---------------------------------------------------------------------------
-// Matrix-core steps.  A step is 16 (bf16) or 8 (binary32) values of k; lane
-// l holds row l % 32 and, of k, 8 (l / 32) + j (bf16, one instruction) or
-// 4 (l / 32) + j (binary32, instruction j).
+// Matrix-core steps of 16 x 16 results.  A step is 64 bytes of k: 32 (bf16)
+// or 16 (binary32) values; lane l holds row l % 16 and, of k, values
+// 8 (l / 16) + j (bf16, one instruction) or 4 (l / 16) + j (binary32,
+// instruction j): 16 consecutive bytes.
 // ---------------------------------------------------------------------------
 template <typename T> struct Step;
 
 template <> struct Step<bf16_t> {
-    static constexpr int kK = 16;
     typedef bf16x8 Frag;
-    __device__ static f32x16 mma(Frag p, Frag q, f32x16 c)
+    __device__ static f32x4 mma(Frag p, Frag q, f32x4 c)
     {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(p, q, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q, c, 0, 0, 0);
     }
 };
 
 template <> struct Step<float> {
-    static constexpr int kK = 8;
     typedef f32x4 Frag;
-    __device__ static f32x16 mma(Frag p, Frag q, f32x16 c)
+    __device__ static f32x4 mma(Frag p, Frag q, f32x4 c)
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            c = __builtin_amdgcn_mfma_f32_32x32x2f32(p[j], q[j], c, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[j], q[j], c, 0, 0, 0);
         return c;
     }
 };
@@ -172,9 +170,15 @@ __device__ __forceinline__ i16x4 lds_transpose(const char* p)
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEBLOCK_LDS i16x4*)p);
 }
 
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ bf16x8 join(i16x4 lo, i16x4 hi)
+{
+    const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, v);
+}
+
 // ---------------------------------------------------------------------------
-// The wave's part of the epilogue: 32 x 64 results (two accumulators side by
-// side along n) through the wave's own LDS rows, so that a lane ends with
+// The wave's part of the epilogue: 32 x 64 results through the wave's own LDS rows, so that a lane ends with
 // runs of 16 bytes of a row.
 // ---------------------------------------------------------------------------
 constexpr int kEpiStride = 68;                       // floats a row: 64 and 4 against bank conflicts
@@ -187,15 +191,11 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ void epi_put(float* lds, int col0, f32x16 c)
+// 16 x 16 results: lane l holds row l % 16 (of m), columns 4 (l / 16) ...
+__device__ __forceinline__ void epi_put(float* lds, int row0, int col0, f32x4 c)
 {
     const int l = threadIdx.x % 64;
-    float* row = lds + (l % 32) * kEpiStride + col0 + 4 * (l / 32);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f32x4 v = {c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
-        *reinterpret_cast<f32x4*>(row + 8 * i) = v;
-    }
+    *reinterpret_cast<f32x4*>(lds + (row0 + l % 16) * kEpiStride + col0 + 4 * (l / 16)) = c;
 }
 
 template <int N>
@@ -262,23 +262,26 @@ __device__ __forceinline__ void epi_rows(const GemmArgs<T>& a, const float* lds,
     }
 }
 
-// The whole wave's results, 32 rows at a time.  The loop stays a loop (the
+// The whole wave's results, 32 x 64 at a time.  The loop stays a loop (the
 // activations' code once); which accumulators it takes is a uniform branch.
-template <typename T, int MODE, bool BWD, int MT>
+template <typename T, int MODE, bool BWD, int MT, int NT>
 __device__ __forceinline__ void epilogue(const GemmArgs<T>& a, float* lds, int64_t m0, int n0,
-                                         int plane, const f32x16 (&acc)[MT][2])
+                                         int plane, const f32x4 (&acc)[MT][NT])
 {
+    constexpr int MB = MT / 2, NB = NT / 4;
 #pragma unroll 1
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < MB * NB; ++i) {
         wave_sync();  // the previous rows have been read
 #pragma unroll
-        for (int k = 0; k < MT; ++k)
-            if (k == i) {
-                epi_put(lds, 0, acc[k][0]);
-                epi_put(lds, 32, acc[k][1]);
-            }
+        for (int k = 0; k < MB * NB; ++k)
+            if (k == i)
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    epi_put(lds, t / 4 * 16, t % 4 * 16,
+                            acc[k / NB * 2 + t / 4][k % NB * 4 + t % 4]);
         wave_sync();
-        epi_rows<T, MODE, BWD>(a, lds, m0 + 32 * i, n0, plane);
+        epi_rows<T, MODE, BWD>(a, lds, m0 + 32 * (i / NB),
+                               n0 + (MODE == kUp ? 32 : 64) * (i % NB), plane);
     }
 }
 
@@ -330,22 +333,17 @@ struct AnyTile {
         const int c = threadIdx.x + i * 256;
         return KC ? c % 4 * E : c % (kAnyTile / E) * E;
     }
-    __device__ static typename Step<T>::Frag frag(const char* lds, int step, int row0)
+    __device__ static typename Step<T>::Frag frag(const char* lds, int row0)
     {
         const int l = threadIdx.x % 64;
         if constexpr (KC) {
             return *reinterpret_cast<const typename Step<T>::Frag*>(
-                lds + (row0 + l % 32) * kStride + step * 32 + l / 32 * 16);
+                lds + (row0 + l % 16) * kStride + l / 16 * 16);
         } else if constexpr (sizeof(T) == 2) {
-            const int g = l / 16;
-            const char* p = lds + (step * 16 + 8 * (g >> 1) + l % 16 / 4) * kStride +
-                            (row0 + 16 * (g & 1) + 4 * (l % 4)) * 2;
-            const i16x4 lo = lds_transpose(p), hi = lds_transpose(p + 4 * kStride);
-            typedef short i16x8 __attribute__((ext_vector_type(8)));
-            const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            return __builtin_bit_cast(bf16x8, v);
+            const char* p = lds + (8 * (l / 16) + l % 16 / 4) * kStride + (row0 + 4 * (l % 4)) * 2;
+            return join(lds_transpose(p), lds_transpose(p + 4 * kStride));
         } else {
-            const char* p = lds + (step * 8 + 4 * (l / 32)) * kStride + (row0 + l % 32) * 4;
+            const char* p = lds + 4 * (l / 16) * kStride + (row0 + l % 16) * 4;
             f32x4 v;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -416,12 +414,12 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
     };
 
     const int wave = threadIdx.x / 64, wm = wave / 2 * 64, wn = wave % 2 * 64;
-    f32x16 acc[2][2];
+    f32x4 acc[4][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            acc[i][j] = f32x16{};
+        for (int j = 0; j < 4; ++j)
+            acc[i][j] = f32x4{};
     if (total > 0)
         load(0);
     for (int s = 0; s < total; ++s) {
@@ -435,24 +433,21 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
         __syncthreads();
         if (s + 1 < total)
             load(s + 1);
+        typename Step<T>::Frag fp[4], fq[4];
 #pragma unroll
-        for (int t = 0; t < kK / Step<T>::kK; ++t) {
-            typename Step<T>::Frag fp[2], fq[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fp[i] = PT::frag(lp, t, wn + 32 * i);
-                fq[i] = QT::frag(lq, t, wm + 32 * i);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = Step<T>::mma(fp[j], fq[i], acc[i][j]);
+        for (int i = 0; i < 4; ++i) {
+            fp[i] = PT::frag(lp, wn + 16 * i);
+            fq[i] = QT::frag(lq, wm + 16 * i);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = Step<T>::mma(fp[j], fq[i], acc[i][j]);
     }
     __syncthreads();
     float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
-    epilogue<T, MODE, BWD, 2>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
+    epilogue<T, MODE, BWD, 4, 4>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -465,15 +460,37 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
 // A load writes 1 KiB of LDS in lane order, so the layouts that avoid bank
 // conflicts are made by choosing which 16 bytes each lane fetches:
 //   k contiguous: rows of 128 bytes; 16-byte slot s of row r holds chunk
-//     s ^ (r / 2 % 8).  A wave's 16-byte reads take one chunk of 32 rows; any
-//     16 consecutive rows then cover all 64 banks once.
-//   n contiguous: a k row holds the tile's columns; 64-byte unit c of row k
-//     holds unit c ^ (k % 4) (bf16; ^ 2 (k / 4 % 2) for binary32).  A
-//     transposing read takes 64 bytes of 4 consecutive rows: again all banks.
+//     s ^ (r / 2 % 8).  Sixteen lanes read one chunk of 16 consecutive rows,
+//     which then covers all 64 banks once.
+//   n contiguous: a k row holds the tile's columns.  bf16: 32-byte unit c of
+//     row k holds unit c ^ (k % 4 + 4 (k / 8 % 2)); 32 lanes of a transposing
+//     read take one unit of rows k .. k + 3 and k + 8 .. k + 11, again all
+//     banks.  binary32: 64-byte unit c holds unit c ^ (k / 4 % 4).
 // Chunks past the end of the sum lie outside the buffer descriptor's range
 // (or are pointed there), which reads as zero.  Rows and columns past an
 // edge repeat the last one: their results are not stored.
 // ---------------------------------------------------------------------------
+#ifndef RPM
+#define RPM 2
+#endif
+#ifndef PRIO
+#define PRIO 0
+#endif
+#ifndef BIG_SHAPE
+#define BIG_SHAPE 2, 4, 8, 4
+#endif
+#ifndef BIG_PF
+#define BIG_PF 0
+#endif
+#ifndef SMALL_PF
+#define SMALL_PF 0
+#endif
+#ifndef BIG_SP
+#define BIG_SP 1
+#endif
+#ifndef SMALL_SP
+#define SMALL_SP 1
+#endif
 #ifndef BIG_KB
 #define BIG_KB 128
 #define BIG_NS 2
@@ -490,6 +507,14 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t offset, i32x4 
 {
     // The wait for it is explicit (wait_loads) and ends before a barrier.
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(rsrc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t offset, i32x4 rsrc)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(offset), "s"(rsrc)
                  : "memory");
@@ -523,7 +548,9 @@ struct FastTile {
 
     __device__ static int swizzle(int r)  // of 16-byte slots
     {
-        return KC ? (KB == 128 ? r / 2 % 8 : r / 4 % 4) : sizeof(T) == 2 ? r % 4 * 4 : r / 4 % 2 * 8;
+        if (KC)
+            return KB == 128 ? r / 2 % 8 : r / 4 % 4;
+        return sizeof(T) == 2 ? (r % 4 + r / 8 % 2 * 4) * 2 : r / 4 % 4 * 4;
     }
     // This lane's part of load i: the tile row it falls in and the chunk of it.
     __device__ static int row(int wave, int i)
@@ -539,22 +566,17 @@ struct FastTile {
     {
         const int l = threadIdx.x % 64;
         if constexpr (KC) {
-            const int r = row0 + l % 32;
             return *reinterpret_cast<const typename Step<T>::Frag*>(
-                lds + r * KB + ((step * 2 + l / 32) ^ swizzle(l % 32)) * 16);
+                lds + (row0 + l % 16) * KB + ((step * 4 + l / 16) ^ swizzle(l % 16)) * 16);
         } else if constexpr (sizeof(T) == 2) {
-            const int g = l / 16;
-            const int k = step * 16 + 8 * (g >> 1) + l % 16 / 4;
-            const char* p = lds + k * kRowBytes + ((row0 / 8) ^ swizzle(l % 16 / 4)) * 16 +
-                            (16 * (g & 1) + 4 * (l % 4)) * 2;
-            const i16x4 lo = lds_transpose(p), hi = lds_transpose(p + 4 * kRowBytes);
-            typedef short i16x8 __attribute__((ext_vector_type(8)));
-            const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            return __builtin_bit_cast(bf16x8, v);
+            const int k = 8 * (l / 16) + l % 16 / 4;
+            const char* p = lds + (step * 32 + k) * kRowBytes +
+                            ((row0 / 8 + l % 4 / 2) ^ swizzle(k)) * 16 + l % 2 * 8;
+            return join(lds_transpose(p), lds_transpose(p + 4 * kRowBytes));
         } else {
-            const int k = step * 8 + 4 * (l / 32);
-            const char* p = lds + k * kRowBytes + ((row0 / 4) ^ swizzle(4 * (l / 32))) * 16 +
-                            l % 32 * 4;
+            const int k = 4 * (l / 16);
+            const char* p = lds + (step * 16 + k) * kRowBytes +
+                            ((row0 / 4 + l % 16 / 4) ^ swizzle(k)) * 16 + l % 4 * 4;
             f32x4 v;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -564,17 +586,17 @@ struct FastTile {
     }
 };
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int KB, int NS>
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP, int PF>
 __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<T> a)
 {
     constexpr bool PK = MODE == kUp, QK = MODE != kDw;
-    constexpr int BM = WM * MT * 32, BN = WN * 64, WAVES = WM * WN;
+    constexpr int BM = WM * MT * 16, BN = WN * NT * 16, WAVES = WM * WN;
     using PT = FastTile<T, PK, BN, WAVES, KB>;
     using QT = FastTile<T, QK, BM, WAVES, KB>;
-    constexpr int kK = PT::kK, E = Elem<T>::kPerVec, STEPS = kK / Step<T>::kK;
+    constexpr int kK = PT::kK, E = Elem<T>::kPerVec, STEPS = KB / 64;
     constexpr int kStage = PT::kBytes + QT::kBytes;
     constexpr int kLds = NS * kStage > WAVES * kEpiBytes ? NS * kStage : WAVES * kEpiBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[kLds];
+    __shared__ __attribute__((aligned(1024))) char lds[kLds + (PF ? WAVES * 256 : 0)];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(MEBLOCK_LDS char*)lds;
 
     int tm, tn, plane = 0;
@@ -622,17 +644,20 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
     // Where the next step's loads start, in scalar registers: address, bytes
     // left of the sum from there (what lies past them reads as zero).
     constexpr int kStepK = kK;
-    const char *curp, *curq;
+    const char *curp, *curu, *curq;  // curu (kUp): Wu's, curp Wg's
     int64_t incp, incq, leftp, leftq;
+    // Loads of one weight's 32 rows; a wave loads of one weight, or of both.
+    constexpr int kTurn = 32 * KB / 1024;
+    constexpr bool kBoth = MODE == kUp && PT::kLoads > kTurn;
+    static_assert(kBoth ? PT::kLoads % (2 * kTurn) == 0 : kTurn % PT::kLoads == 0 || MODE != kUp,
+                  "which weight a load is of depends on its number, or on the wave");
     auto start = [&](int seg) {
         if constexpr (MODE == kUp) {
-            // A wave's loads of P are of one of the weights.
-            constexpr int kTurn = 32 * KB / 1024;  // loads of one weight's 32 rows
-            static_assert(kTurn % PT::kLoads == 0, "a wave loads one weight");
-            const bool up = wave * PT::kLoads / kTurn % 2;
+            const bool up = !kBoth && wave * PT::kLoads / kTurn % 2;
             const T* w = up ? a.p.base[1] : a.p.base[0];
             const int64_t ld = up ? a.p.ld[1] : a.p.ld[0];
             curp = reinterpret_cast<const char*>(w + (int64_t)n0 * ld);
+            curu = reinterpret_cast<const char*>(a.p.base[1] + (int64_t)n0 * a.p.ld[1]);
             incp = kStepK * (int64_t)sizeof(T);
             leftp = kBufferBytes;
         } else {
@@ -653,7 +678,9 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
             leftq = ((int64_t)(a.k - 1) * ld + a.q_cols - m0) * (int64_t)sizeof(T);
         }
     };
-    i32x4 rp, rq;
+    i32x4 rp, ru, rq;
+    const char* curt = reinterpret_cast<const char*>(
+        wave % 2 ? a.p.base[1] + (int64_t)n0 * a.p.ld[1] : a.p.base[0] + (int64_t)n0 * a.p.ld[0]);
     int ahead = 0;  // the step whose loads come next
     auto next_step = [&]() {
         if (MODE == kDx ? ahead == 0 || ahead == steps : ahead == 0)
@@ -664,6 +691,10 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
             return any ? (uint32_t)(left < (int64_t)kBufferBytes ? left : (int64_t)kBufferBytes) : 0u;
         };
         rp = buffer(curp, bytes(leftp));
+        if constexpr (kBoth) {
+            ru = buffer(curu, bytes(leftp));
+            curu += incp;
+        }
         rq = buffer(curq, bytes(leftq));
         curp += incp;
         curq += incq;
@@ -686,89 +717,172 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
         }
         ++ahead;
     };
+    // Touching the lines of a later step brings them into the XCD's L2.
+    uint32_t offt = kOutside;
+    bool touch_p = false;
+    if constexpr (PF > 0) {
+        static_assert(BM + BN == WAVES * 64 && KB == 128, "one line a lane");
+        touch_p = wave < BN / 64;
+        const int line = (touch_p ? wave : wave - BN / 64) * 64 + (int)(threadIdx.x % 64);
+        if (touch_p) {
+            if (line % 8 == tm % 8) {
+                if constexpr (MODE == kUp) {
+                    // Waves in turn take rows of Wg and of Wu.
+                    int n = line / 128 * 64 + line % 64;
+                    n = n0 + n < a.p.rows ? n : a.p.rows - 1 - n0;
+                    offt = (uint32_t)((int64_t)n * (wave % 2 ? a.p.ld[1] : a.p.ld[0])) *
+                           (uint32_t)sizeof(T);
+                } else {
+                    constexpr int kLines = BN * (int)sizeof(T) / 128;
+                    const int c = line % kLines * (128 / (int)sizeof(T));
+                    const int n = n0 + c < a.p.rows ? c : a.p.rows - E - n0;
+                    offt = (uint32_t)((int64_t)(line / kLines) * a.p.ld[0] + n) * (uint32_t)sizeof(T);
+                }
+            }
+        } else if (line % 4 == tn % 4) {
+            if constexpr (QK) {
+                const int m = m0 + line < a.q.rows ? line : (int)(a.q.rows - 1 - m0);
+                offt = (uint32_t)((int64_t)m * a.q.ld[0]) * (uint32_t)sizeof(T);
+            } else {
+                constexpr int kLines = BM * (int)sizeof(T) / 128;
+                const int c = line % kLines * (128 / (int)sizeof(T));
+                const int m = m0 + c < a.q_cols ? c : (int)(a.q_cols - E - m0);
+                offt = (uint32_t)((int64_t)(line / kLines) * a.q.ld[0] + m) * (uint32_t)sizeof(T);
+            }
+        }
+    }
+    auto touch = [&]() {
+        const int at = ahead - 1 + PF;
+        const bool any = at < total && !(MODE == kDx && ahead - 1 < steps && at >= steps);
+        const char* p = (touch_p ? curp : curq) + (PF - 1) * (touch_p ? incp : incq);
+        int64_t left = kBufferBytes;
+        if constexpr (MODE == kUp) {
+            if (touch_p)
+                p = curt + (int64_t)at * 128;
+        }
+        if (!PK && touch_p)
+            left = leftp - (PF - 1) * incp;
+        if (!QK && !touch_p)
+            left = leftq - (PF - 1) * incq;
+        const uint32_t bytes = any && left > 0 ? (uint32_t)(left < (int64_t)kBufferBytes ? left : (int64_t)kBufferBytes) : 0u;
+        load_lds4(lds0 + kLds + wave * 256, offt, buffer(p, bytes));
+    };
     const uint32_t ldsp = lds0 + wave * (PT::kLoads * 1024);
     const uint32_t ldsq = lds0 + PT::kBytes + wave * (QT::kLoads * 1024);
     constexpr int kLoads = PT::kLoads + QT::kLoads;
     auto issue = [&](uint32_t place, int i) {
         if (i < PT::kLoads)
-            load_lds16(ldsp + place + i * 1024, offp[i], rp);
+            load_lds16(ldsp + place + i * 1024, offp[i], kBoth && i / kTurn % 2 ? ru : rp);
         else
             load_lds16(ldsq + place + (i - PT::kLoads) * 1024, offq[i - PT::kLoads], rq);
     };
 
-    const int wm = wave / WN * (MT * 32), wn = wave % WN * 64;
-    f32x16 acc[MT][2];
+    const int wm = wave / WN * (MT * 16), wn = wave % WN * (NT * 16);
+    f32x4 acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            acc[i][j] = f32x16{};
+        for (int j = 0; j < NT; ++j)
+            acc[i][j] = f32x4{};
 
-    // Two sets of fragments: one is multiplied while the next is read.
-    typename Step<T>::Frag fp[2][2], fq[2][MT];
-    constexpr int kFrags = 2 + MT;
-    auto read = [&](int set, uint32_t place, int t, int i) {
-        if (i < 2)
-            fp[set][i] = PT::frag(lds + place, t, wn + 32 * i);
-        else
-            fq[set][i - 2] = QT::frag(lds + place + PT::kBytes, t, wm + 32 * (i - 2));
+    // A step's loads are spread over SP parts of a step from its last part on.
+    constexpr int kSlot = kLoads / SP;
+    static_assert(kLoads % SP == 0 && SP <= STEPS, "equal slots");
+
+    // Fragments: P's twice, one set multiplied while the next is read; Q's
+    // once, each read again as soon as its products have been issued.
+    typename Step<T>::Frag fp[2][NT], fq[MT];
+    auto read_p = [&](int set, uint32_t place, int t, int j) {
+        fp[set][j] = PT::frag(lds + place, t, wn + 16 * j);
     };
-    static_assert(STEPS % 2 == 0, "fragment sets alternate across steps");
+    auto read_q = [&](uint32_t place, int t, int i) {
+        fq[i] = QT::frag(lds + place + PT::kBytes, t, wm + 16 * i);
+    };
+    static_assert(STEPS % 2 == 0, "P's sets alternate across steps");
 
     if (total > 0) {
+        // As if steps before the first had issued them.
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             next_step();
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
+            for (int i = 0; i < (s == NS - 1 ? kSlot : kLoads); ++i)
                 issue(s * kStage, i);
+            if (PF && (s < NS - 1 || SP == 1))
+                touch();
         }
-        wait_loads<(NS - 1) * kLoads>();
+        wait_loads<(NS - 2) * kLoads + kSlot + (PF ? NS - (SP > 1) : 0)>();
         __builtin_amdgcn_s_barrier();
 #pragma unroll
-        for (int i = 0; i < kFrags; ++i)
-            read(0, 0, 0, i);
+        for (int j = 0; j < NT; ++j)
+            read_p(0, 0, 0, j);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            read_q(0, 0, i);
     }
-    // Step s: its first fragments are in registers; its last are multiplied
-    // after the barrier behind which step s + 1 is in LDS and the place of
-    // step s is free for step s + NS.  Reads and loads are spread between
-    // the products; the order is kept as written.
-    uint32_t place = 0;
+    // Step s: its first fragments are in registers.  Its last reads are issued
+    // before its last part; a row of products into that part (BG), the barrier
+    // behind which step s + 1 is in LDS and the place of step s is free for
+    // step s + NS.  Reads and loads are spread between the products; the
+    // order is kept as written.
+    constexpr int BG = 1;
+    uint32_t place = 0, before = (NS - 1) * kStage;
 #pragma unroll 1
     for (int s = 0; s < total; ++s) {
         const uint32_t next = place + kStage == NS * kStage ? 0 : place + kStage;
 #pragma unroll
         for (int t = 0; t < STEPS; ++t) {
             const bool last = t == STEPS - 1;
-            if (last) {
+            if (last)
                 next_step();
-                // Loads of steps s + 2 .. s + NS - 1 may stay in flight.
-                wait_loads<(NS - 2) * kLoads>();
-                asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-                __builtin_amdgcn_s_barrier();
-            }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
-                acc[i / 2][i % 2] = Step<T>::mma(fp[t & 1][i % 2], fq[t & 1][i / 2],
-                                                 acc[i / 2][i % 2]);
+            for (int i = 0; i < MT; ++i) {
 #pragma unroll
-                for (int k = i * kFrags / (2 * MT); k < (i + 1) * kFrags / (2 * MT); ++k)
-                    read(~t & 1, last ? next : place, last ? 0 : t + 1, k);
-                if (last) {
+                for (int j = 0; j < NT; ++j)
+                    acc[i][j] = Step<T>::mma(fp[t & 1][j], fq[i], acc[i][j]);
+                if (last && i == BG) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    // Loads of steps s + 2 .. s + NS - 1 may stay in flight
+                    // (and the touch that came after the loads).
+                    wait_loads<(NS - 2) * kLoads + (PF ? NS - 1 : 0)>();
+                    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+                    __builtin_amdgcn_s_barrier();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                const uint32_t from = last ? next : place;
+                const int tt = last ? 0 : t + 1;
+                const int first = last ? BG : 0;  // row of products whose reads come first
+                if (i >= first) {
+                    if (i == first)
 #pragma unroll
-                    for (int k = i * kLoads / (2 * MT); k < (i + 1) * kLoads / (2 * MT); ++k)
-                        issue(place, k);
+                        for (int k = 0; k < first; ++k)
+                            read_q(from, tt, k);
+                    read_q(from, tt, i);
+                    const int jn = NT / (MT / 2 - 1 > 0 ? (MT / 2 < NT ? MT / 2 : NT) : 1);
+#pragma unroll
+                    for (int j = (i - first) * jn; j < (i - first + 1) * jn && j < NT; ++j)
+                        read_p(~t & 1, from, tt, j);
+                }
+                const int slot = last ? 0 : t + 1;
+                if (slot < SP && i >= first) {
+                    const int rows = MT - first, r = i - first;
+#pragma unroll
+                    for (int k = r * kSlot / rows; k < (r + 1) * kSlot / rows; ++k)
+                        issue(last ? place : before, slot * kSlot + k);
+                    if (PF && slot == SP - 1 && i == MT - 1)
+                        touch();
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+        before = place;
         place = next;
     }
     wait_loads<0>();
     __syncthreads();
     float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
-    epilogue<T, MODE, BWD, MT>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
+    epilogue<T, MODE, BWD, MT, NT>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -866,12 +980,12 @@ static bool aligned_rows(const GemmArgs<T>& a)
     return MODE != kDx || (a.p.ld[0] == a.p.ld[1] && a.q.ld[0] == a.q.ld[1]);
 }
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int KB, int NS>
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP, int PF>
 static int gemm_fast(GemmArgs<T>& a, hipStream_t stream)
 {
     return gemm_launch<T, MODE>(
-        a, reinterpret_cast<const void*>(&gemm_fast_kernel<T, MODE, BWD, WM, WN, MT, KB, NS>), WM * MT * 32,
-        WN * 64, WM * WN * 64, stream);
+        a, reinterpret_cast<const void*>(&gemm_fast_kernel<T, MODE, BWD, WM, WN, MT, NT, KB, NS, SP, PF>),
+        WM * MT * 16, WN * NT * 16, WM * WN * 64, stream);
 }
 
 template <typename T, int MODE, bool BWD>
@@ -882,8 +996,8 @@ static int gemm_run(GemmArgs<T>& a, hipStream_t stream)
         const int64_t big = (int64_t)((a.q.rows + 255) / 256) * ((a.out_cols + cols - 1) / cols) *
                             (MODE == kDw ? 2 : 1);
         if (big >= 256)
-            return gemm_fast<T, MODE, BWD, 2, 4, 4, BIG_KB, BIG_NS>(a, stream);
-        return gemm_fast<T, MODE, BWD, 2, 2, 2, SMALL_KB, SMALL_NS>(a, stream);
+            return gemm_fast<T, MODE, BWD, BIG_SHAPE, BIG_KB, BIG_NS, BIG_SP, BIG_PF>(a, stream);
+        return gemm_fast<T, MODE, BWD, 2, 2, 4, 4, SMALL_KB, SMALL_NS, SMALL_SP, SMALL_PF>(a, stream);
     }
     return gemm_launch<T, MODE>(
         a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD>), kAnyTile, kAnyTile, 256,
