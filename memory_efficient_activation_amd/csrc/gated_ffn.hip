@@ -87,55 +87,6 @@ __device__ __forceinline__ float act_slope(float x, float dy, const Coef& k)
     return d;
 }
 
-// N elements: forward g <- f(g) u; backward (with d = dh) g <- d u f'(g),
-// u <- d f(g), d <- f(g) u.
-template <class Op, bool P, bool BWD, int N>
-__device__ __forceinline__ void gate(float* g, float* u, float* d, const Coef& k)
-{
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const float f = act_value<Op, P>(g[j], k);
-        if constexpr (BWD) {
-            const float dg = act_slope<Op, P>(g[j], d[j] * u[j], k);
-            const float du = d[j] * f;
-            d[j] = f * u[j];
-            g[j] = dg;
-            u[j] = du;
-        } else {
-            g[j] = f * u[j];
-        }
-    }
-}
-
-template <bool P, bool BWD, int N>
-__device__ __forceinline__ void gate_act(int act, float* g, float* u, float* d, const Coef& k)
-{
-    using namespace meswish;
-    switch (act) {
-    case kRelu:
-        gate<ActOp<kRelu>, P, BWD, N>(g, u, d, k);
-        break;
-    case kLeakyRelu:
-        gate<ActOp<kLeakyRelu>, P, BWD, N>(g, u, d, k);
-        break;
-    case kSigmoid:
-        gate<ActOp<kSigmoid>, P, BWD, N>(g, u, d, k);
-        break;
-    case kTanh:
-        gate<ActOp<kTanh>, P, BWD, N>(g, u, d, k);
-        break;
-    case kGeluErf:
-        gate<ActOp<kGeluErf>, P, BWD, N>(g, u, d, k);
-        break;
-    case kGeluTanh:
-        gate<ActOp<kGeluTanh>, P, BWD, N>(g, u, d, k);
-        break;
-    default:
-        gate<ActOp<kSwish>, P, BWD, N>(g, u, d, k);
-        break;
-    }
-}
-
 // ---------------------------------------------------------------------------
 // Matrix-core steps of 16 x 16 results.  A step is 64 bytes of k: 32 (bf16)
 // or 16 (binary32) values; lane l holds row l % 16 and, of k, values
@@ -170,6 +121,16 @@ __device__ __forceinline__ i16x4 lds_transpose(const char* p)
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEBLOCK_LDS i16x4*)p);
 }
 
+// The row that lane l's row l % 16 of the 16 rows from `row0` (a multiple of
+// 16) is: itself, or (PAIR, P of kUp) interleaved by fours with the other 16
+// of its 32.
+template <bool PAIR>
+__device__ __forceinline__ int frag_row(int row0)
+{
+    const int l = threadIdx.x % 64;
+    return PAIR ? row0 / 32 * 32 + row0 / 16 % 2 * 4 + l % 16 / 4 * 8 + l % 4 : row0 + l % 16;
+}
+
 typedef short i16x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ bf16x8 join(i16x4 lo, i16x4 hi)
 {
@@ -178,120 +139,253 @@ __device__ __forceinline__ bf16x8 join(i16x4 lo, i16x4 hi)
 }
 
 // ---------------------------------------------------------------------------
-// The wave's part of the epilogue: 32 x 64 results through the wave's own LDS rows, so that a lane ends with
-// runs of 16 bytes of a row.
+// Epilogues, from the accumulators: lane l holds, of each 16 x 16 results,
+// row l % 16 (of m) and the four columns 4 (l / 16) ...  kUp: a wave's
+// columns are 32 hidden units of g and the same 32 of u in turn, and the
+// fragments are read so that the first and second 16 of them give a lane
+// units 8 (l / 16) ... and 8 (l / 16) + 4 ...: eight consecutive ones.
 // ---------------------------------------------------------------------------
-constexpr int kEpiStride = 68;                       // floats a row: 64 and 4 against bank conflicts
-constexpr int kEpiBytes = 32 * kEpiStride * 4;       // a wave's share
-
-__device__ __forceinline__ void wave_sync()
+// The lane, as a value the compiler computes where it is used: what follows
+// from it does not occupy registers through the products.
+__device__ __forceinline__ int late_lane()
 {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    int l = threadIdx.x % 64;
+    asm volatile("" : "+v"(l));
+    return l;
 }
 
-// 16 x 16 results: lane l holds row l % 16 (of m), columns 4 (l / 16) ...
-__device__ __forceinline__ void epi_put(float* lds, int row0, int col0, f32x4 c)
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
+__device__ __forceinline__ void store4(bf16_t* p, f32x4 f)
 {
-    const int l = threadIdx.x % 64;
-    *reinterpret_cast<f32x4*>(lds + (row0 + l % 16) * kEpiStride + col0 + 4 * (l / 16)) = c;
+    const u32x2 v = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+    *reinterpret_cast<u32x2_any*>(p) = v;
+}
+__device__ __forceinline__ void store4(float* p, f32x4 f)
+{
+    store16(p, Elem<float>::pack(reinterpret_cast<const float*>(&f)));
 }
 
-template <int N>
-__device__ __forceinline__ void epi_get(const float* p, float* f)
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, f32x4 f, int n)  // the first n of four
 {
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(p + j);
-        f[j] = v[0], f[j + 1] = v[1], f[j + 2] = v[2], f[j + 3] = v[3];
+    for (int j = 0; j < 4; ++j)
+        if (j < n)
+            p[j] = Elem<T>::put(f[j]);
+}
+
+// dx, dWg, dWu.
+template <typename T, int MT, int NT>
+__device__ __forceinline__ void store_results(const GemmArgs<T>& a, int64_t m0, int n0, int plane,
+                                              const f32x4 (&acc)[MT][NT])
+{
+    const int l = late_lane();
+    const int64_t m = m0 + l % 16;
+    const int n = n0 + 4 * (l / 16);
+    const int64_t ld = plane ? a.ldo[1] : a.ldo[0];
+    T* out = (plane ? a.out[1] : a.out[0]) + m * ld + n;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        if (m + 16 * i < a.q.rows)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int left = a.out_cols - (n + 16 * j);
+                if (left >= 4)
+                    store4(out + 16 * j, acc[i][j]);
+                else if (left > 0)
+                    store_some(out + 16 * j, acc[i][j], left);
+            }
+        out += 16 * ld;
     }
 }
 
-// Rows m0 .. m0 + 31 of the output, from the wave's LDS rows; kUp: hidden
-// units n0 .. n0 + 31 of g and u; otherwise columns n0 .. n0 + 63.
-template <typename T, int MODE, bool BWD>
-__device__ __forceinline__ void epi_rows(const GemmArgs<T>& a, const float* lds, int64_t m0, int n0,
-                                         int plane)
-{
-    constexpr int E = Elem<T>::kPerVec;
-    const int l = threadIdx.x % 64;
-    if constexpr (MODE == kUp) {
-        constexpr int PER_ROW = 32 / E, ROWS = 64 / PER_ROW;
-#pragma unroll 1
-        for (int r = l / PER_ROW; r < 32; r += ROWS) {
-            const int c = (l % PER_ROW) * E;
-            const int64_t m = m0 + r;
-            const int n = n0 + c;
-            if (m >= a.q.rows || n >= a.out_cols)
-                continue;
-            float g[E], u[E], d[E];
-            epi_get<E>(lds + r * kEpiStride + c, g);
-            epi_get<E>(lds + r * kEpiStride + 32 + c, u);
-            if constexpr (BWD)
-                Elem<T>::unpack(load_chunk(a.dh + m * a.lddh, n, a.p.rows), d);
-            gate_act<sizeof(T) == 4, BWD, E>(a.act, g, u, d, a.coef);
-            if constexpr (BWD) {
-                // The workspace rows are padded: zeros past the last unit.
+// Eight consecutive values, as loaded.
+template <typename T>
+struct Eight {
+    static constexpr int V = sizeof(T) / 2;
+    u32x4 v[V];
+    __device__ void load(const T* p)
+    {
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    g[j] = n + j < a.p.rows ? g[j] : 0.0f;
-                    u[j] = n + j < a.p.rows ? u[j] : 0.0f;
-                }
-                store_chunk(a.out[0] + m * a.ldo[0], n, a.out_cols, g);
-                store_chunk(a.out[1] + m * a.ldo[1], n, a.out_cols, u);
-                if (a.h)
-                    store_chunk(a.h + m * a.ldh, n, a.p.rows, d);
+        for (int i = 0; i < V; ++i)
+            v[i] = load16(p + i * Elem<T>::kPerVec);
+    }
+    __device__ void values(float* f) const
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            Elem<T>::unpack(v[i], f + i * Elem<T>::kPerVec);
+    }
+    __device__ static void store(T* p, const float* f)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            store16(p + i * Elem<T>::kPerVec, Elem<T>::pack(f + i * Elem<T>::kPerVec));
+    }
+};
+
+// The unit on whole vectors of eight, without the activations' rare branches.
+// True in a lane that met one (or a row's last, partial vector): the wave is
+// then done again by gate_slow, to the same places.
+template <class Op, typename T, bool BWD, int MT, int NT>
+__device__ __forceinline__ bool gate_fast(const GemmArgs<T>& a, int64_t m0, int n0,
+                                          const f32x4 (&acc)[MT][NT])
+{
+    constexpr bool P = sizeof(T) == 4;
+    const int l = late_lane();
+    const int64_t m = m0 + l % 16;
+    const int n = n0 + 8 * (l / 16);
+    float key = 0.0f;
+    bool partial = false;
+    constexpr int kVecs = MT * NT / 4;
+    Eight<T> d[BWD ? kVecs : 1];  // the wave's part of dh, in flight together
+    if constexpr (BWD) {
+#pragma unroll
+        for (int t = 0; t < kVecs; ++t) {
+            const int64_t row = m + 16 * (t / (NT / 4));
+            const int c = n + 32 * (t % (NT / 4));
+            if (row < a.q.rows && c + 8 <= a.p.rows)
+                d[t].load(a.dh + row * a.lddh + c);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kVecs; ++t) {
+        const int i = t / (NT / 4), b = t % (NT / 4) * 4;
+        const int64_t row = m + 16 * i;
+        const int c = n + 8 * b;
+        float o[8], du[8], h[8], up[8];
+        if constexpr (BWD)
+            d[t].values(up);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float g = acc[i][b + e / 4][e % 4], u = acc[i][b + 2 + e / 4][e % 4];
+            const float f = Op::template fwd<P>(g, a.coef, key);
+            if constexpr (BWD) {
+                o[e] = Op::template bwd<P>(g, up[e] * u, a.coef, key);
+                du[e] = up[e] * f;
+                h[e] = f * u;
             } else {
-                store_chunk(a.out[0] + m * a.ldo[0], n, a.out_cols, g);
+                o[e] = f * u;
             }
         }
-    } else {
-        constexpr int PER_ROW = 64 / E, ROWS = 64 / PER_ROW;
+        const bool in = c + 8 <= a.p.rows;
+        if (row < a.q.rows && c < a.out_cols) {
+            if (!in && c < a.p.rows) {
+                partial = true;
+            } else if constexpr (BWD) {
+                // The workspace's rows are padded: zeros past the last unit.
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    o[e] = in ? o[e] : 0.0f;
+                    du[e] = in ? du[e] : 0.0f;
+                }
+                Eight<T>::store(a.out[0] + row * a.ldo[0] + c, o);
+                Eight<T>::store(a.out[1] + row * a.ldo[1] + c, du);
+                if (a.h && in)
+                    Eight<T>::store(a.h + row * a.ldh + c, h);
+            } else {
+                Eight<T>::store(a.out[0] + row * a.ldo[0] + c, o);
+            }
+        }
+    }
+    return partial || key > Op::template rare_thr<P>();
+}
+
+template <class Op, typename T, bool BWD, int MT, int NT>
+__device__ __forceinline__ void gate_slow(const GemmArgs<T>& a, int64_t m0, int n0,
+                                          const f32x4 (&acc)[MT][NT])
+{
+    constexpr bool P = sizeof(T) == 4;
+    const int l = late_lane();
 #pragma unroll 1
-        for (int r = l / PER_ROW; r < 32; r += ROWS) {
-            const int c = (l % PER_ROW) * E;
-            const int64_t m = m0 + r;
-            const int n = n0 + c;
-            if (m >= a.q.rows || n >= a.out_cols)
+    for (int t = 0; t < MT * NT / 2; ++t) {
+        const int i = t / (NT / 2), j = t % (NT / 2);  // j: 32 units, then four of eight
+        f32x4 g = f32x4{}, u = f32x4{};
+#pragma unroll
+        for (int k = 0; k < MT * NT / 2; ++k)  // a uniform choice of registers
+            if (k == t) {
+                g = acc[k / (NT / 2)][k % (NT / 2) / 2 * 4 + k % 2];
+                u = acc[k / (NT / 2)][k % (NT / 2) / 2 * 4 + 2 + k % 2];
+            }
+        const int64_t m = m0 + l % 16 + 16 * i;
+        const int n = n0 + 8 * (l / 16) + 32 * (j / 2) + 4 * (j % 2);
+        if (m >= a.q.rows)
+            continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = n + e;
+            if (c >= a.p.rows) {
+                if (BWD && c < a.out_cols) {
+                    a.out[0][m * a.ldo[0] + c] = Elem<T>::put(0.0f);
+                    a.out[1][m * a.ldo[1] + c] = Elem<T>::put(0.0f);
+                }
                 continue;
-            float f[E];
-            epi_get<E>(lds + r * kEpiStride + c, f);
-            store_chunk(a.out[plane] + m * a.ldo[plane], n, a.out_cols, f);
+            }
+            const float f = act_value<Op, P>(g[e], a.coef);
+            if constexpr (BWD) {
+                const float d = Elem<T>::get(a.dh[m * a.lddh + c]);
+                a.out[0][m * a.ldo[0] + c] =
+                    Elem<T>::put(act_slope<Op, P>(g[e], d * u[e], a.coef));
+                a.out[1][m * a.ldo[1] + c] = Elem<T>::put(d * f);
+                if (a.h)
+                    a.h[m * a.ldh + c] = Elem<T>::put(f * u[e]);
+            } else {
+                a.out[0][m * a.ldo[0] + c] = Elem<T>::put(f * u[e]);
+            }
         }
     }
 }
 
-// The whole wave's results, 32 x 64 at a time.  The loop stays a loop (the
-// activations' code once); which accumulators it takes is a uniform branch.
-template <typename T, int MODE, bool BWD, int MT, int NT>
-__device__ __forceinline__ void epilogue(const GemmArgs<T>& a, float* lds, int64_t m0, int n0,
-                                         int plane, const f32x4 (&acc)[MT][NT])
+template <class Op, typename T, bool BWD, int MT, int NT>
+__device__ __forceinline__ void gate(const GemmArgs<T>& a, int64_t m0, int n0,
+                                     const f32x4 (&acc)[MT][NT])
 {
-    constexpr int MB = MT / 2, NB = NT / 4;
-#pragma unroll 1
-    for (int i = 0; i < MB * NB; ++i) {
-        wave_sync();  // the previous rows have been read
-#pragma unroll
-        for (int k = 0; k < MB * NB; ++k)
-            if (k == i)
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    epi_put(lds, t / 4 * 16, t % 4 * 16,
-                            acc[k / NB * 2 + t / 4][k % NB * 4 + t % 4]);
-        wave_sync();
-        epi_rows<T, MODE, BWD>(a, lds, m0 + 32 * (i / NB),
-                               n0 + (MODE == kUp ? 32 : 64) * (i % NB), plane);
+    if (__any(gate_fast<Op, T, BWD>(a, m0, n0, acc)))
+        gate_slow<Op, T, BWD>(a, m0, n0, acc);
+}
+
+template <typename T, int MODE, bool BWD, int MT, int NT>
+__device__ __forceinline__ void epilogue(const GemmArgs<T>& a, int64_t m0, int n0, int plane,
+                                         const f32x4 (&acc)[MT][NT])
+{
+    if constexpr (MODE != kUp) {
+        store_results(a, m0, n0, plane, acc);
+    } else {
+        using namespace meswish;
+        switch (a.act) {
+        case kRelu:
+            gate<ActOp<kRelu>, T, BWD>(a, m0, n0, acc);
+            break;
+        case kLeakyRelu:
+            gate<ActOp<kLeakyRelu>, T, BWD>(a, m0, n0, acc);
+            break;
+        case kSigmoid:
+            gate<ActOp<kSigmoid>, T, BWD>(a, m0, n0, acc);
+            break;
+        case kTanh:
+            gate<ActOp<kTanh>, T, BWD>(a, m0, n0, acc);
+            break;
+        case kGeluErf:
+            gate<ActOp<kGeluErf>, T, BWD>(a, m0, n0, acc);
+            break;
+        case kGeluTanh:
+            gate<ActOp<kGeluTanh>, T, BWD>(a, m0, n0, acc);
+            break;
+        default:
+            gate<ActOp<kSwish>, T, BWD>(a, m0, n0, acc);
+            break;
+        }
     }
 }
 
 // Tiles in an order that keeps the blocks of one XCD (every eighth block) on
 // neighbouring tiles, whose operands they then share in that XCD's L2:
 // columns of 8 tiles along m, then along n.
-__device__ __forceinline__ void tile_of_block(int tiles_m, int tiles_n, int& tm, int& tn)
+__device__ __forceinline__ void tile_of_block(int id, int tiles_m, int tiles_n, int& tm, int& tn)
 {
     const int total = tiles_m * tiles_n;
-    int id = blockIdx.x;
     const int per = total / 8, rest = total % 8;
     const int xcd = id % 8, at = id / 8;
     id = xcd * per + (xcd < rest ? xcd : rest) + at;
@@ -314,7 +408,7 @@ constexpr int kAnyTile = 128;
 // A tile of 128 rows (k contiguous: 64 bytes of k a row, 80 apart in LDS) or
 // of 64 bytes' worth of k rows (n contiguous: 128 values a row, padded by 32
 // bytes): both strides spread a wave's reads over all banks.
-template <typename T, bool KC>
+template <typename T, bool KC, bool PAIR>
 struct AnyTile {
     static constexpr int E = Elem<T>::kPerVec;
     static constexpr int kK = 64 / sizeof(T);
@@ -338,7 +432,7 @@ struct AnyTile {
         const int l = threadIdx.x % 64;
         if constexpr (KC) {
             return *reinterpret_cast<const typename Step<T>::Frag*>(
-                lds + (row0 + l % 16) * kStride + l / 16 * 16);
+                lds + frag_row<PAIR>(row0) * kStride + l / 16 * 16);
         } else if constexpr (sizeof(T) == 2) {
             const char* p = lds + (8 * (l / 16) + l % 16 / 4) * kStride + (row0 + 4 * (l % 4)) * 2;
             return join(lds_transpose(p), lds_transpose(p + 4 * kStride));
@@ -357,22 +451,22 @@ template <typename T, int MODE, bool BWD>
 __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
 {
     constexpr bool PK = MODE == kUp, QK = MODE != kDw;
-    using PT = AnyTile<T, PK>;
-    using QT = AnyTile<T, QK>;
+    using PT = AnyTile<T, PK, PK>;
+    using QT = AnyTile<T, QK, false>;
     constexpr int kK = PT::kK;
     constexpr int kBytes = PT::kBytes + QT::kBytes;
-    __shared__ __attribute__((aligned(16))) char lds[kBytes > 4 * kEpiBytes ? kBytes : 4 * kEpiBytes];
+    __shared__ __attribute__((aligned(16))) char lds[kBytes];
     char* const lp = lds;
     char* const lq = lds + PT::kBytes;
 
     int tm, tn, plane = 0;
     if constexpr (MODE == kDw) {
         // The tiles of dWg, then those of dWu.
-        tile_of_block(2 * a.tiles_m, a.tiles_n, tm, tn);
+        tile_of_block(blockIdx.x, 2 * a.tiles_m, a.tiles_n, tm, tn);
         plane = tm >= a.tiles_m;
         tm -= plane * a.tiles_m;
     } else {
-        tile_of_block(a.tiles_m, a.tiles_n, tm, tn);
+        tile_of_block(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
     }
     const int64_t m0 = (int64_t)tm * kAnyTile;
     const int n0 = tn * (MODE == kUp ? kAnyTile / 2 : kAnyTile);
@@ -445,9 +539,7 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
             for (int j = 0; j < 4; ++j)
                 acc[i][j] = Step<T>::mma(fp[j], fq[i], acc[i][j]);
     }
-    __syncthreads();
-    float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
-    epilogue<T, MODE, BWD, 4, 4>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
+    epilogue<T, MODE, BWD>(a, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -461,7 +553,8 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
 // conflicts are made by choosing which 16 bytes each lane fetches:
 //   k contiguous: rows of 128 bytes; 16-byte slot s of row r holds chunk
 //     s ^ (r / 2 % 8).  Sixteen lanes read one chunk of 16 consecutive rows,
-//     which then covers all 64 banks once.
+//     which then covers all 64 banks once.  (P of kUp: of rows 8 a + b, a and
+//     b < 4; s ^ (r / 2 % 2 + 2 (r / 8 % 4)) does the same for them.)
 //   n contiguous: a k row holds the tile's columns.  bf16: 32-byte unit c of
 //     row k holds unit c ^ (k % 4 + 4 (k / 8 % 2)); 32 lanes of a transposing
 //     read take one unit of rows k .. k + 3 and k + 8 .. k + 11, again all
@@ -470,35 +563,6 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
 // (or are pointed there), which reads as zero.  Rows and columns past an
 // edge repeat the last one: their results are not stored.
 // ---------------------------------------------------------------------------
-#ifndef RPM
-#define RPM 2
-#endif
-#ifndef PRIO
-#define PRIO 0
-#endif
-#ifndef BIG_SHAPE
-#define BIG_SHAPE 2, 4, 8, 4
-#endif
-#ifndef BIG_PF
-#define BIG_PF 0
-#endif
-#ifndef SMALL_PF
-#define SMALL_PF 0
-#endif
-#ifndef BIG_SP
-#define BIG_SP 1
-#endif
-#ifndef SMALL_SP
-#define SMALL_SP 1
-#endif
-#ifndef BIG_KB
-#define BIG_KB 128
-#define BIG_NS 2
-#endif
-#ifndef SMALL_KB
-#define SMALL_KB 128
-#define SMALL_NS 2
-#endif
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr uint32_t kBufferBytes = 0xc0000000u;  // no tile reaches this far
 constexpr uint32_t kOutside = 0xf0000000u;
@@ -507,14 +571,6 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t offset, i32x4 
 {
     // The wait for it is explicit (wait_loads) and ends before a barrier.
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(offset), "s"(rsrc)
-                 : "memory");
-}
-
-__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t offset, i32x4 rsrc)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(offset), "s"(rsrc)
                  : "memory");
@@ -537,9 +593,10 @@ __device__ __forceinline__ i32x4 buffer(const void* p, uint32_t bytes)
 }
 
 // A tile of ROWS values of m or n and KB bytes of k, filled by WAVES waves.
-template <typename T, bool KC, int ROWS, int WAVES, int KB>
+template <typename T, bool KC, bool PAIR, int ROWS, int WAVES, int KB>
 struct FastTile {
     static constexpr int E = Elem<T>::kPerVec;
+    static_assert(KB == 128, "the layouts below");
     static constexpr int kK = KB / sizeof(T);
     static constexpr int kBytes = ROWS * KB;
     static constexpr int kRowBytes = KC ? KB : ROWS * (int)sizeof(T);
@@ -549,25 +606,26 @@ struct FastTile {
     __device__ static int swizzle(int r)  // of 16-byte slots
     {
         if (KC)
-            return KB == 128 ? r / 2 % 8 : r / 4 % 4;
+            return PAIR ? r / 2 % 2 + r / 8 % 4 * 2 : r / 2 % 8;
         return sizeof(T) == 2 ? (r % 4 + r / 8 % 2 * 4) * 2 : r / 4 % 4 * 4;
     }
     // This lane's part of load i: the tile row it falls in and the chunk of it.
-    __device__ static int row(int wave, int i)
+    __device__ static int row(int lane, int wave, int i)
     {
-        return ((wave * kLoads + i) * 1024 + (int)(threadIdx.x % 64) * 16) / kRowBytes;
+        return ((wave * kLoads + i) * 1024 + lane * 16) / kRowBytes;
     }
-    __device__ static int chunk(int wave, int i)
+    __device__ static int chunk(int lane, int wave, int i)
     {
         static_assert(kRowBytes <= 1024, "a load covers whole rows");
-        return (int)(threadIdx.x % 64) * 16 % kRowBytes / 16 ^ swizzle(row(wave, i));
+        return lane * 16 % kRowBytes / 16 ^ swizzle(row(lane, wave, i));
     }
     __device__ static typename Step<T>::Frag frag(const char* lds, int step, int row0)
     {
         const int l = threadIdx.x % 64;
         if constexpr (KC) {
+            const int r = frag_row<PAIR>(row0);
             return *reinterpret_cast<const typename Step<T>::Frag*>(
-                lds + (row0 + l % 16) * KB + ((step * 4 + l / 16) ^ swizzle(l % 16)) * 16);
+                lds + r * KB + ((step * 4 + l / 16) ^ swizzle(r % 32)) * 16);
         } else if constexpr (sizeof(T) == 2) {
             const int k = 8 * (l / 16) + l % 16 / 4;
             const char* p = lds + (step * 32 + k) * kRowBytes +
@@ -586,60 +644,70 @@ struct FastTile {
     }
 };
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP, int PF>
-__global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<T> a)
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP>
+__global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmArgs<T> a)
 {
     constexpr bool PK = MODE == kUp, QK = MODE != kDw;
     constexpr int BM = WM * MT * 16, BN = WN * NT * 16, WAVES = WM * WN;
-    using PT = FastTile<T, PK, BN, WAVES, KB>;
-    using QT = FastTile<T, QK, BM, WAVES, KB>;
+    using PT = FastTile<T, PK, PK, BN, WAVES, KB>;
+    using QT = FastTile<T, QK, false, BM, WAVES, KB>;
     constexpr int kK = PT::kK, E = Elem<T>::kPerVec, STEPS = KB / 64;
     constexpr int kStage = PT::kBytes + QT::kBytes;
-    constexpr int kLds = NS * kStage > WAVES * kEpiBytes ? NS * kStage : WAVES * kEpiBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[kLds + (PF ? WAVES * 256 : 0)];
+    constexpr int kLds = NS * kStage;
+    __shared__ __attribute__((aligned(1024))) char lds[kLds];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(MEBLOCK_LDS char*)lds;
 
-    int tm, tn, plane = 0;
-    if constexpr (MODE == kDw) {
-        tile_of_block(2 * a.tiles_m, a.tiles_n, tm, tn);
-        plane = tm >= a.tiles_m;
-        tm -= plane * a.tiles_m;
-    } else {
-        tile_of_block(a.tiles_m, a.tiles_n, tm, tn);
-    }
-    const int64_t m0 = (int64_t)tm * BM;
-    const int n0 = tn * (MODE == kUp ? BN / 2 : BN);
+    const int tiles = a.tiles_m * a.tiles_n * (MODE == kDw ? 2 : 1);
     const int steps = (a.k + kK - 1) / kK;
-    const int total = MODE == kDx ? 2 * steps : steps;
+    // An empty sum is one step of zeros.
+    const int total = steps == 0 ? 1 : MODE == kDx ? 2 * steps : steps;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = wave / WN * (MT * 16), wn = wave % WN * (NT * 16);
 
+    // The tile whose operands are being loaded: it runs ahead of the one that
+    // is multiplied.
+    int64_t m0;
+    int n0, plane, tm, tn;
     // Offsets of this lane's 16 bytes in each load, from the tile's first
     // element; (kUp) Wu's from Wu's own first row.
     uint32_t offp[PT::kLoads], offq[QT::kLoads];
-#pragma unroll
-    for (int i = 0; i < PT::kLoads; ++i) {
-        const int r = PT::row(wave, i), c = PT::chunk(wave, i) * E;
-        if constexpr (MODE == kUp) {
-            // Rows of the tile: 32 of Wg, 32 of Wu, in turn.
-            int n = r / 64 * 32 + r % 32;
-            n = n0 + n < a.p.rows ? n : a.p.rows - 1 - n0;
-            offp[i] = (uint32_t)((int64_t)n * a.p.ld[r / 32 % 2] + c) * (uint32_t)sizeof(T);
+    auto place_tile = [&](int tile) {
+        const int lane = late_lane();
+        plane = 0;
+        if constexpr (MODE == kDw) {
+            tile_of_block(tile, 2 * a.tiles_m, a.tiles_n, tm, tn);
+            plane = tm >= a.tiles_m;
+            tm -= plane * a.tiles_m;
         } else {
-            const int n = n0 + c < a.p.rows ? c : a.p.rows - E - n0;
-            offp[i] = (uint32_t)((int64_t)r * a.p.ld[0] + n) * (uint32_t)sizeof(T);
+            tile_of_block(tile, a.tiles_m, a.tiles_n, tm, tn);
         }
-    }
+        m0 = (int64_t)tm * BM;
+        n0 = tn * (MODE == kUp ? BN / 2 : BN);
 #pragma unroll
-    for (int i = 0; i < QT::kLoads; ++i) {
-        const int r = QT::row(wave, i), c = QT::chunk(wave, i) * E;
-        if constexpr (QK) {
-            const int m = m0 + r < a.q.rows ? r : (int)(a.q.rows - 1 - m0);
-            offq[i] = (uint32_t)((int64_t)m * a.q.ld[0] + c) * (uint32_t)sizeof(T);
-        } else {
-            const int m = m0 + c < a.q_cols ? c : (int)(a.q_cols - E - m0);
-            offq[i] = (uint32_t)((int64_t)r * a.q.ld[0] + m) * (uint32_t)sizeof(T);
+        for (int i = 0; i < PT::kLoads; ++i) {
+            const int r = PT::row(lane, wave, i), c = PT::chunk(lane, wave, i) * E;
+            if constexpr (MODE == kUp) {
+                // Rows of the tile: 32 of Wg, 32 of Wu, in turn.
+                int n = r / 64 * 32 + r % 32;
+                n = n0 + n < a.p.rows ? n : a.p.rows - 1 - n0;
+                offp[i] = (uint32_t)((int64_t)n * a.p.ld[r / 32 % 2] + c) * (uint32_t)sizeof(T);
+            } else {
+                const int n = n0 + c < a.p.rows ? c : a.p.rows - E - n0;
+                offp[i] = (uint32_t)((int64_t)r * a.p.ld[0] + n) * (uint32_t)sizeof(T);
+            }
         }
-    }
+#pragma unroll
+        for (int i = 0; i < QT::kLoads; ++i) {
+            const int r = QT::row(lane, wave, i), c = QT::chunk(lane, wave, i) * E;
+            if constexpr (QK) {
+                const int m = m0 + r < a.q.rows ? r : (int)(a.q.rows - 1 - m0);
+                offq[i] = (uint32_t)((int64_t)m * a.q.ld[0] + c) * (uint32_t)sizeof(T);
+            } else {
+                const int m = m0 + c < a.q_cols ? c : (int)(a.q_cols - E - m0);
+                offq[i] = (uint32_t)((int64_t)r * a.q.ld[0] + m) * (uint32_t)sizeof(T);
+            }
+        }
+    };
 
     // Where the next step's loads start, in scalar registers: address, bytes
     // left of the sum from there (what lies past them reads as zero).
@@ -679,16 +747,23 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
         }
     };
     i32x4 rp, ru, rq;
-    const char* curt = reinterpret_cast<const char*>(
-        wave % 2 ? a.p.base[1] + (int64_t)n0 * a.p.ld[1] : a.p.base[0] + (int64_t)n0 * a.p.ld[0]);
-    int ahead = 0;  // the step whose loads come next
+    int ahead = 0, tile_ahead = blockIdx.x;  // the step whose loads come next
     auto next_step = [&]() {
-        if (MODE == kDx ? ahead == 0 || ahead == steps : ahead == 0)
-            start(ahead != 0);
-        // Past the last step nothing is read (zeros are written).
-        const bool any = ahead < total;
+        if (ahead == total) {
+            ahead = 0;
+            tile_ahead += gridDim.x;
+        }
+        // Past the last tile nothing is read (zeros are written).
+        const bool any = tile_ahead < tiles;
+        const bool some = any && a.k > 0;
+        if (ahead == 0 && any) {
+            place_tile(tile_ahead);
+            start(0);
+        }
+        if (MODE == kDx && ahead == steps && any)
+            start(1);
         auto bytes = [&](int64_t left) {
-            return any ? (uint32_t)(left < (int64_t)kBufferBytes ? left : (int64_t)kBufferBytes) : 0u;
+            return some ? (uint32_t)(left < (int64_t)kBufferBytes ? left : (int64_t)kBufferBytes) : 0u;
         };
         rp = buffer(curp, bytes(leftp));
         if constexpr (kBoth) {
@@ -704,68 +779,18 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
             leftq -= incq;
         if constexpr (MODE == kUp) {
             // A last step that is cut short: chunks past the end are pointed
-            // outside, for good (no step follows).
+            // outside; the next tile has offsets of its own.
             if (ahead == total - 1 && a.k % kK) {
-                const int k0 = ahead * kK;
+                const int k0 = ahead * kK, lane = late_lane();
 #pragma unroll
                 for (int i = 0; i < PT::kLoads; ++i)
-                    offp[i] = k0 + PT::chunk(wave, i) * E < a.k ? offp[i] : kOutside;
+                    offp[i] = k0 + PT::chunk(lane, wave, i) * E < a.k ? offp[i] : kOutside;
 #pragma unroll
                 for (int i = 0; i < QT::kLoads; ++i)
-                    offq[i] = k0 + QT::chunk(wave, i) * E < a.k ? offq[i] : kOutside;
+                    offq[i] = k0 + QT::chunk(lane, wave, i) * E < a.k ? offq[i] : kOutside;
             }
         }
         ++ahead;
-    };
-    // Touching the lines of a later step brings them into the XCD's L2.
-    uint32_t offt = kOutside;
-    bool touch_p = false;
-    if constexpr (PF > 0) {
-        static_assert(BM + BN == WAVES * 64 && KB == 128, "one line a lane");
-        touch_p = wave < BN / 64;
-        const int line = (touch_p ? wave : wave - BN / 64) * 64 + (int)(threadIdx.x % 64);
-        if (touch_p) {
-            if (line % 8 == tm % 8) {
-                if constexpr (MODE == kUp) {
-                    // Waves in turn take rows of Wg and of Wu.
-                    int n = line / 128 * 64 + line % 64;
-                    n = n0 + n < a.p.rows ? n : a.p.rows - 1 - n0;
-                    offt = (uint32_t)((int64_t)n * (wave % 2 ? a.p.ld[1] : a.p.ld[0])) *
-                           (uint32_t)sizeof(T);
-                } else {
-                    constexpr int kLines = BN * (int)sizeof(T) / 128;
-                    const int c = line % kLines * (128 / (int)sizeof(T));
-                    const int n = n0 + c < a.p.rows ? c : a.p.rows - E - n0;
-                    offt = (uint32_t)((int64_t)(line / kLines) * a.p.ld[0] + n) * (uint32_t)sizeof(T);
-                }
-            }
-        } else if (line % 4 == tn % 4) {
-            if constexpr (QK) {
-                const int m = m0 + line < a.q.rows ? line : (int)(a.q.rows - 1 - m0);
-                offt = (uint32_t)((int64_t)m * a.q.ld[0]) * (uint32_t)sizeof(T);
-            } else {
-                constexpr int kLines = BM * (int)sizeof(T) / 128;
-                const int c = line % kLines * (128 / (int)sizeof(T));
-                const int m = m0 + c < a.q_cols ? c : (int)(a.q_cols - E - m0);
-                offt = (uint32_t)((int64_t)(line / kLines) * a.q.ld[0] + m) * (uint32_t)sizeof(T);
-            }
-        }
-    }
-    auto touch = [&]() {
-        const int at = ahead - 1 + PF;
-        const bool any = at < total && !(MODE == kDx && ahead - 1 < steps && at >= steps);
-        const char* p = (touch_p ? curp : curq) + (PF - 1) * (touch_p ? incp : incq);
-        int64_t left = kBufferBytes;
-        if constexpr (MODE == kUp) {
-            if (touch_p)
-                p = curt + (int64_t)at * 128;
-        }
-        if (!PK && touch_p)
-            left = leftp - (PF - 1) * incp;
-        if (!QK && !touch_p)
-            left = leftq - (PF - 1) * incq;
-        const uint32_t bytes = any && left > 0 ? (uint32_t)(left < (int64_t)kBufferBytes ? left : (int64_t)kBufferBytes) : 0u;
-        load_lds4(lds0 + kLds + wave * 256, offt, buffer(p, bytes));
     };
     const uint32_t ldsp = lds0 + wave * (PT::kLoads * 1024);
     const uint32_t ldsq = lds0 + PT::kBytes + wave * (QT::kLoads * 1024);
@@ -777,14 +802,7 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
             load_lds16(ldsq + place + (i - PT::kLoads) * 1024, offq[i - PT::kLoads], rq);
     };
 
-    const int wm = wave / WN * (MT * 16), wn = wave % WN * (NT * 16);
     f32x4 acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            acc[i][j] = f32x4{};
-
     // A step's loads are spread over SP parts of a step from its last part on.
     constexpr int kSlot = kLoads / SP;
     static_assert(kLoads % SP == 0 && SP <= STEPS, "equal slots");
@@ -800,26 +818,24 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
     };
     static_assert(STEPS % 2 == 0, "P's sets alternate across steps");
 
-    if (total > 0) {
-        // As if steps before the first had issued them.
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            next_step();
-#pragma unroll
-            for (int i = 0; i < (s == NS - 1 ? kSlot : kLoads); ++i)
-                issue(s * kStage, i);
-            if (PF && (s < NS - 1 || SP == 1))
-                touch();
-        }
-        wait_loads<(NS - 2) * kLoads + kSlot + (PF ? NS - (SP > 1) : 0)>();
-        __builtin_amdgcn_s_barrier();
+    auto first_part = [&](uint32_t place) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            read_p(0, 0, 0, j);
+            read_p(0, place, 0, j);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            read_q(0, 0, i);
+            read_q(place, 0, i);
+    };
+    // As if steps before the first had issued them.
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        next_step();
+#pragma unroll
+        for (int i = 0; i < (s == NS - 1 ? kSlot : kLoads); ++i)
+            issue(s * kStage, i);
     }
+    wait_loads<(NS - 2) * kLoads + kSlot>();
+    __builtin_amdgcn_s_barrier();
     // Step s: its first fragments are in registers.  Its last reads are issued
     // before its last part; a row of products into that part (BG), the barrier
     // behind which step s + 1 is in LDS and the place of step s is free for
@@ -828,7 +844,24 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
     constexpr int BG = 1;
     uint32_t place = 0, before = (NS - 1) * kStage;
 #pragma unroll 1
-    for (int s = 0; s < total; ++s) {
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    int om, on, op = 0;  // this tile's place in the output
+    if constexpr (MODE == kDw) {
+        tile_of_block(tile, 2 * a.tiles_m, a.tiles_n, om, on);
+        op = om >= a.tiles_m;
+        om -= op * a.tiles_m;
+    } else {
+        tile_of_block(tile, a.tiles_m, a.tiles_n, om, on);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            acc[i][j] = f32x4{};
+    first_part(place);
+    int s = 0;
+#pragma unroll 1
+    do {
         const uint32_t next = place + kStage == NS * kStage ? 0 : place + kStage;
 #pragma unroll
         for (int t = 0; t < STEPS; ++t) {
@@ -843,9 +876,8 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
                     acc[i][j] = Step<T>::mma(fp[t & 1][j], fq[i], acc[i][j]);
                 if (last && i == BG) {
                     __builtin_amdgcn_sched_barrier(0);
-                    // Loads of steps s + 2 .. s + NS - 1 may stay in flight
-                    // (and the touch that came after the loads).
-                    wait_loads<(NS - 2) * kLoads + (PF ? NS - 1 : 0)>();
+                    // Loads of steps s + 2 .. s + NS - 1 may stay in flight.
+                    wait_loads<(NS - 2) * kLoads>();
                     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
                     __builtin_amdgcn_s_barrier();
                     __builtin_amdgcn_sched_barrier(0);
@@ -870,19 +902,18 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_fast_kernel(const GemmArgs<
 #pragma unroll
                     for (int k = r * kSlot / rows; k < (r + 1) * kSlot / rows; ++k)
                         issue(last ? place : before, slot * kSlot + k);
-                    if (PF && slot == SP - 1 && i == MT - 1)
-                        touch();
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
         before = place;
         place = next;
+    } while (++s < total);
+    // The next tile's first steps arrive meanwhile.
+    epilogue<T, MODE, BWD>(a, (int64_t)om * BM + wm,
+                           on * (MODE == kUp ? BN / 2 : BN) + (MODE == kUp ? wn / 2 : wn), op, acc);
     }
-    wait_loads<0>();
-    __syncthreads();
-    float* epi = reinterpret_cast<float*>(lds + wave * kEpiBytes);
-    epilogue<T, MODE, BWD, MT, NT>(a, epi, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
+    wait_loads<0>();  // no load writes LDS after the block has ended
 }
 
 // ---------------------------------------------------------------------------
@@ -948,8 +979,20 @@ static bool matrix_ok(const void* p, size_t rows, size_t cols, size_t ld, size_t
 
 static size_t padded(size_t hidden) { return (hidden + 63) / 64 * 64; }
 
+// Blocks that are on the GPU together, by their LDS (160 KiB a CU); a
+// multiple of the 8 XCDs.
+static int resident_blocks(int lds_bytes)
+{
+    int device = 0, cus = 0;
+    if (hipGetDevice(&device) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess)
+        cus = 256;
+    const int n = cus * ((160 << 10) / lds_bytes) / 8 * 8;
+    return n > 8 ? n : 8;
+}
+
 template <typename T, int MODE>
-static int gemm_launch(GemmArgs<T>& a, const void* fn, int bm, int bn, int block,
+static int gemm_launch(GemmArgs<T>& a, const void* fn, int bm, int bn, int block, int resident,
                        hipStream_t stream)
 {
     const int cols = MODE == kUp ? bn / 2 : bn;
@@ -961,7 +1004,8 @@ static int gemm_launch(GemmArgs<T>& a, const void* fn, int bm, int bn, int block
     if (grid >= ((int64_t)1 << 23))
         return MESWISH_EINVAL;
     void* args[] = {&a};
-    return launch(fn, dim3((unsigned)grid), block, args, stream);
+    return launch(fn, dim3((unsigned)(resident && grid > resident ? resident : grid)), block, args,
+                  stream);
 }
 
 // Every row of the operands starts on a 16-byte boundary and the loads' 16
@@ -980,12 +1024,13 @@ static bool aligned_rows(const GemmArgs<T>& a)
     return MODE != kDx || (a.p.ld[0] == a.p.ld[1] && a.q.ld[0] == a.q.ld[1]);
 }
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP, int PF>
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP>
 static int gemm_fast(GemmArgs<T>& a, hipStream_t stream)
 {
     return gemm_launch<T, MODE>(
-        a, reinterpret_cast<const void*>(&gemm_fast_kernel<T, MODE, BWD, WM, WN, MT, NT, KB, NS, SP, PF>),
-        WM * MT * 16, WN * NT * 16, WM * WN * 64, stream);
+        a, reinterpret_cast<const void*>(&gemm_fast_kernel<T, MODE, BWD, WM, WN, MT, NT, KB, NS, SP>),
+        WM * MT * 16, WN * NT * 16, WM * WN * 64,
+        MODE == kUp ? resident_blocks(NS * (WM * MT + WN * NT) * 16 * KB) : 0, stream);
 }
 
 template <typename T, int MODE, bool BWD>
@@ -996,11 +1041,11 @@ static int gemm_run(GemmArgs<T>& a, hipStream_t stream)
         const int64_t big = (int64_t)((a.q.rows + 255) / 256) * ((a.out_cols + cols - 1) / cols) *
                             (MODE == kDw ? 2 : 1);
         if (big >= 256)
-            return gemm_fast<T, MODE, BWD, BIG_SHAPE, BIG_KB, BIG_NS, BIG_SP, BIG_PF>(a, stream);
-        return gemm_fast<T, MODE, BWD, 2, 2, 4, 4, SMALL_KB, SMALL_NS, SMALL_SP, SMALL_PF>(a, stream);
+            return gemm_fast<T, MODE, BWD, 2, 4, 8, 4, 128, 2, 1>(a, stream);
+        return gemm_fast<T, MODE, BWD, 2, 2, 4, 4, 128, 2, 1>(a, stream);
     }
     return gemm_launch<T, MODE>(
-        a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD>), kAnyTile, kAnyTile, 256,
+        a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD>), kAnyTile, kAnyTile, 256, 0,
         stream);
 }
 
