@@ -22,6 +22,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "act_math.h"
 #include "block_common.h"
 #include "gated_ffn.h"
@@ -59,6 +61,10 @@ struct GemmArgs {
     int64_t lddh;
     T* h;         // kUp, backward: the forward's result, or NULL
     int64_t ldh;
+    // A sum that is split: `splits` binary32 parts, each [planes * q.rows]
+    // [part_ld] (kUp: columns as P's rows, 32 of Wg and 32 of Wu in turn).
+    float* part;
+    int splits, part_ld;
     int act;
     Coef coef;
 };
@@ -176,26 +182,26 @@ __device__ __forceinline__ void store_some(T* p, f32x4 f, int n)  // the first n
             p[j] = Elem<T>::put(f[j]);
 }
 
-// dx, dWg, dWu.
-template <typename T, int MT, int NT>
-__device__ __forceinline__ void store_results(const GemmArgs<T>& a, int64_t m0, int n0, int plane,
-                                              const f32x4 (&acc)[MT][NT])
+// Results as they are: dx, dWg, dWu, or the parts of a split sum.
+template <bool PAIR, typename U, int MT, int NT>
+__device__ __forceinline__ void store_results(U* out, int64_t ld, int64_t rows, int cols, int64_t m0,
+                                              int n0, const f32x4 (&acc)[MT][NT])
 {
     const int l = late_lane();
     const int64_t m = m0 + l % 16;
-    const int n = n0 + 4 * (l / 16);
-    const int64_t ld = plane ? a.ldo[1] : a.ldo[0];
-    T* out = (plane ? a.out[1] : a.out[0]) + m * ld + n;
+    out += m * ld;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        if (m + 16 * i < a.q.rows)
+        if (m + 16 * i < rows)
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const int left = a.out_cols - (n + 16 * j);
+                const int n = n0 + (PAIR ? 32 * (j / 2) + 8 * (l / 16) + 4 * (j % 2)
+                                         : 16 * j + 4 * (l / 16));
+                const int left = cols - n;
                 if (left >= 4)
-                    store4(out + 16 * j, acc[i][j]);
+                    store4(out + n, acc[i][j]);
                 else if (left > 0)
-                    store_some(out + 16 * j, acc[i][j], left);
+                    store_some(out + n, acc[i][j], left);
             }
         out += 16 * ld;
     }
@@ -293,6 +299,60 @@ __device__ __forceinline__ bool gate_fast(const GemmArgs<T>& a, int64_t m0, int 
     return partial || key > Op::template rare_thr<P>();
 }
 
+// One element of the unit's result, written where it belongs: exactly (with
+// the rare branches).  c is below a.out_cols.
+template <class Op, typename T, bool BWD>
+__device__ __forceinline__ void gate_one(const GemmArgs<T>& a, int64_t m, int c, float g, float u)
+{
+    constexpr bool P = sizeof(T) == 4;
+    if (c >= a.p.rows) {
+        if constexpr (BWD) {
+            // The workspace's rows are padded: zeros past the last unit.
+            a.out[0][m * a.ldo[0] + c] = Elem<T>::put(0.0f);
+            a.out[1][m * a.ldo[1] + c] = Elem<T>::put(0.0f);
+        }
+        return;
+    }
+    const float f = act_value<Op, P>(g, a.coef);
+    if constexpr (BWD) {
+        const float d = Elem<T>::get(a.dh[m * a.lddh + c]);
+        a.out[0][m * a.ldo[0] + c] = Elem<T>::put(act_slope<Op, P>(g, d * u, a.coef));
+        a.out[1][m * a.ldo[1] + c] = Elem<T>::put(d * f);
+        if (a.h)
+            a.h[m * a.ldh + c] = Elem<T>::put(f * u);
+    } else {
+        a.out[0][m * a.ldo[0] + c] = Elem<T>::put(f * u);
+    }
+}
+
+// The same for the activation of the call.
+template <typename T, bool BWD>
+struct Gate {
+    const GemmArgs<T>& a;
+    __device__ __forceinline__ void operator()(int64_t m, int c, float g, float u) const
+    {
+        using namespace meswish;
+        if (c >= a.out_cols)
+            return;
+        switch (a.act) {
+        case kRelu:
+            return gate_one<ActOp<kRelu>, T, BWD>(a, m, c, g, u);
+        case kLeakyRelu:
+            return gate_one<ActOp<kLeakyRelu>, T, BWD>(a, m, c, g, u);
+        case kSigmoid:
+            return gate_one<ActOp<kSigmoid>, T, BWD>(a, m, c, g, u);
+        case kTanh:
+            return gate_one<ActOp<kTanh>, T, BWD>(a, m, c, g, u);
+        case kGeluErf:
+            return gate_one<ActOp<kGeluErf>, T, BWD>(a, m, c, g, u);
+        case kGeluTanh:
+            return gate_one<ActOp<kGeluTanh>, T, BWD>(a, m, c, g, u);
+        default:
+            return gate_one<ActOp<kSwish>, T, BWD>(a, m, c, g, u);
+        }
+    }
+};
+
 template <class Op, typename T, bool BWD, int MT, int NT>
 __device__ __forceinline__ void gate_slow(const GemmArgs<T>& a, int64_t m0, int n0,
                                           const f32x4 (&acc)[MT][NT])
@@ -314,27 +374,9 @@ __device__ __forceinline__ void gate_slow(const GemmArgs<T>& a, int64_t m0, int 
         if (m >= a.q.rows)
             continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = n + e;
-            if (c >= a.p.rows) {
-                if (BWD && c < a.out_cols) {
-                    a.out[0][m * a.ldo[0] + c] = Elem<T>::put(0.0f);
-                    a.out[1][m * a.ldo[1] + c] = Elem<T>::put(0.0f);
-                }
-                continue;
-            }
-            const float f = act_value<Op, P>(g[e], a.coef);
-            if constexpr (BWD) {
-                const float d = Elem<T>::get(a.dh[m * a.lddh + c]);
-                a.out[0][m * a.ldo[0] + c] =
-                    Elem<T>::put(act_slope<Op, P>(g[e], d * u[e], a.coef));
-                a.out[1][m * a.ldo[1] + c] = Elem<T>::put(d * f);
-                if (a.h)
-                    a.h[m * a.ldh + c] = Elem<T>::put(f * u[e]);
-            } else {
-                a.out[0][m * a.ldo[0] + c] = Elem<T>::put(f * u[e]);
-            }
-        }
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.out_cols)
+                gate_one<Op, T, BWD>(a, m, n + e, g[e], u[e]);
     }
 }
 
@@ -346,13 +388,20 @@ __device__ __forceinline__ void gate(const GemmArgs<T>& a, int64_t m0, int n0,
         gate_slow<Op, T, BWD>(a, m0, n0, acc);
 }
 
-template <typename T, int MODE, bool BWD, int MT, int NT>
+// n0: the wave's first column of P's rows (kUp) or of the result.
+template <typename T, int MODE, bool BWD, bool PARTS, int MT, int NT>
 __device__ __forceinline__ void epilogue(const GemmArgs<T>& a, int64_t m0, int n0, int plane,
                                          const f32x4 (&acc)[MT][NT])
 {
-    if constexpr (MODE != kUp) {
-        store_results(a, m0, n0, plane, acc);
+    if constexpr (PARTS) {
+        const int64_t part = (int64_t)blockIdx.y * (MODE == kDw ? 2 : 1) + plane;
+        store_results<MODE == kUp>(a.part + part * a.q.rows * a.part_ld, a.part_ld, a.q.rows,
+                                   a.part_ld, m0, n0, acc);
+    } else if constexpr (MODE != kUp) {
+        store_results<false>(plane ? a.out[1] : a.out[0], plane ? a.ldo[1] : a.ldo[0], a.q.rows,
+                             a.out_cols, m0, n0, acc);
     } else {
+        n0 /= 2;
         using namespace meswish;
         switch (a.act) {
         case kRelu:
@@ -395,6 +444,14 @@ __device__ __forceinline__ void tile_of_block(int id, int tiles_m, int tiles_n, 
     const int rows = tiles_m - first < kGroup ? tiles_m - first : kGroup;
     tm = first + id % width % rows;
     tn = id % width / rows;
+}
+
+// Steps [first, total) of a sum of `total` steps: block row y's share.
+__device__ __forceinline__ void part_of_sum(int splits, int& first, int& total)
+{
+    const int whole = total, y = blockIdx.y;
+    first = (int)((int64_t)whole * y / splits);
+    total = (int)((int64_t)whole * (y + 1) / splits);
 }
 
 // ---------------------------------------------------------------------------
@@ -447,7 +504,7 @@ struct AnyTile {
     }
 };
 
-template <typename T, int MODE, bool BWD>
+template <typename T, int MODE, bool BWD, bool PARTS>
 __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
 {
     constexpr bool PK = MODE == kUp, QK = MODE != kDw;
@@ -471,7 +528,9 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
     const int64_t m0 = (int64_t)tm * kAnyTile;
     const int n0 = tn * (MODE == kUp ? kAnyTile / 2 : kAnyTile);
     const int steps = (a.k + kK - 1) / kK;
-    const int total = MODE == kDx ? 2 * steps : steps;
+    int first = 0, total = MODE == kDx ? 2 * steps : steps;
+    if constexpr (PARTS)
+        part_of_sum(a.splits, first, total);
 
     u32x4 rp[PT::kChunks], rq[QT::kChunks];
     const u32x4 zero = {0, 0, 0, 0};
@@ -514,9 +573,9 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[i][j] = f32x4{};
-    if (total > 0)
-        load(0);
-    for (int s = 0; s < total; ++s) {
+    if (first < total)
+        load(first);
+    for (int s = first; s < total; ++s) {
         __syncthreads();  // the previous step has been read
 #pragma unroll
         for (int i = 0; i < PT::kChunks; ++i)
@@ -539,7 +598,7 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
             for (int j = 0; j < 4; ++j)
                 acc[i][j] = Step<T>::mma(fp[j], fq[i], acc[i][j]);
     }
-    epilogue<T, MODE, BWD>(a, m0 + wm, n0 + (MODE == kUp ? wn / 2 : wn), plane, acc);
+    epilogue<T, MODE, BWD, PARTS>(a, m0 + wm, tn * kAnyTile + wn, plane, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -644,7 +703,8 @@ struct FastTile {
     }
 };
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP>
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP,
+          bool PARTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmArgs<T> a)
 {
     constexpr bool PK = MODE == kUp, QK = MODE != kDw;
@@ -660,7 +720,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
     const int tiles = a.tiles_m * a.tiles_n * (MODE == kDw ? 2 : 1);
     const int steps = (a.k + kK - 1) / kK;
     // An empty sum is one step of zeros.
-    const int total = steps == 0 ? 1 : MODE == kDx ? 2 * steps : steps;
+    int first = 0, total = steps == 0 ? 1 : MODE == kDx ? 2 * steps : steps;
+    const int whole = total;
+    if constexpr (PARTS)
+        part_of_sum(a.splits, first, total);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wm = wave / WN * (MT * 16), wn = wave % WN * (NT * 16);
 
@@ -747,21 +810,31 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
         }
     };
     i32x4 rp, ru, rq;
-    int ahead = 0, tile_ahead = blockIdx.x;  // the step whose loads come next
+    int ahead = first, tile_ahead = blockIdx.x;  // the step whose loads come next
     auto next_step = [&]() {
         if (ahead == total) {
-            ahead = 0;
+            ahead = first;
             tile_ahead += gridDim.x;
         }
         // Past the last tile nothing is read (zeros are written).
         const bool any = tile_ahead < tiles;
         const bool some = any && a.k > 0;
-        if (ahead == 0 && any) {
+        if (ahead == first && any) {
             place_tile(tile_ahead);
-            start(0);
-        }
-        if (MODE == kDx && ahead == steps && any)
+            start(MODE == kDx && first >= steps && steps > 0);
+            if constexpr (PARTS) {
+                const int64_t skip = MODE == kDx && first >= steps ? first - steps : first;
+                curp += skip * incp;
+                curu += skip * incp;
+                curq += skip * incq;
+                if constexpr (!PK)
+                    leftp -= skip * incp;
+                if constexpr (!QK)
+                    leftq -= skip * incq;
+            }
+        } else if (MODE == kDx && ahead == steps && any) {
             start(1);
+        }
         auto bytes = [&](int64_t left) {
             return some ? (uint32_t)(left < (int64_t)kBufferBytes ? left : (int64_t)kBufferBytes) : 0u;
         };
@@ -780,7 +853,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
         if constexpr (MODE == kUp) {
             // A last step that is cut short: chunks past the end are pointed
             // outside; the next tile has offsets of its own.
-            if (ahead == total - 1 && a.k % kK) {
+            if (ahead == whole - 1 && a.k % kK) {
                 const int k0 = ahead * kK, lane = late_lane();
 #pragma unroll
                 for (int i = 0; i < PT::kLoads; ++i)
@@ -859,7 +932,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
         for (int j = 0; j < NT; ++j)
             acc[i][j] = f32x4{};
     first_part(place);
-    int s = 0;
+    int s = first;
 #pragma unroll 1
     do {
         const uint32_t next = place + kStage == NS * kStage ? 0 : place + kStage;
@@ -884,21 +957,21 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
                 }
                 const uint32_t from = last ? next : place;
                 const int tt = last ? 0 : t + 1;
-                const int first = last ? BG : 0;  // row of products whose reads come first
-                if (i >= first) {
-                    if (i == first)
+                const int lead = last ? BG : 0;  // the row of products behind which reads start
+                if (i >= lead) {
+                    if (i == lead)
 #pragma unroll
-                        for (int k = 0; k < first; ++k)
+                        for (int k = 0; k < lead; ++k)
                             read_q(from, tt, k);
                     read_q(from, tt, i);
                     const int jn = NT / (MT / 2 - 1 > 0 ? (MT / 2 < NT ? MT / 2 : NT) : 1);
 #pragma unroll
-                    for (int j = (i - first) * jn; j < (i - first + 1) * jn && j < NT; ++j)
+                    for (int j = (i - lead) * jn; j < (i - lead + 1) * jn && j < NT; ++j)
                         read_p(~t & 1, from, tt, j);
                 }
                 const int slot = last ? 0 : t + 1;
-                if (slot < SP && i >= first) {
-                    const int rows = MT - first, r = i - first;
+                if (slot < SP && i >= lead) {
+                    const int rows = MT - lead, r = i - lead;
 #pragma unroll
                     for (int k = r * kSlot / rows; k < (r + 1) * kSlot / rows; ++k)
                         issue(last ? place : before, slot * kSlot + k);
@@ -910,10 +983,161 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
         place = next;
     } while (++s < total);
     // The next tile's first steps arrive meanwhile.
-    epilogue<T, MODE, BWD>(a, (int64_t)om * BM + wm,
-                           on * (MODE == kUp ? BN / 2 : BN) + (MODE == kUp ? wn / 2 : wn), op, acc);
+    epilogue<T, MODE, BWD, PARTS>(a, (int64_t)om * BM + wm, on * BN + wn, op, acc);
     }
     wait_loads<0>();  // no load writes LDS after the block has ended
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the weights are read once, and their bytes bound the time.  A
+// block takes 16 PT hidden units and all (at most 16 QT) tokens; its NW waves
+// take a share of the sum each, load the weights' fragments from memory
+// straight into registers (16 bytes a lane at element alignment, U steps in
+// flight) with x's fragments beside them (from the caches), and add their
+// parts through LDS in the order of the wave.
+// ---------------------------------------------------------------------------
+template <typename T, bool BWD, int PT, int QT, int NW>
+__global__ __launch_bounds__(NW * 64) void few_tokens_kernel(const GemmArgs<T> a)
+{
+    typedef typename Step<T>::Frag Frag;
+    constexpr int E = Elem<T>::kPerVec, kK = 64 / sizeof(T), kTiles = 2 * PT * QT;
+    constexpr int U = PT * QT > 4 ? 2 : 4;
+    __shared__ float part[NW][kTiles][256];
+    const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int n0 = blockIdx.x * (16 * PT);
+    const int k0 = l / 16 * E;
+    const T* w[2][PT];
+    const T* x[QT];
+#pragma unroll
+    for (int j = 0; j < PT; ++j) {
+        const int n = n0 + 16 * j + l % 16;
+        const int64_t r = n < a.p.rows ? n : a.p.rows - 1;
+        w[0][j] = a.p.base[0] + r * a.p.ld[0];
+        w[1][j] = a.p.base[1] + r * a.p.ld[1];
+    }
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+        const int m = 16 * i + l % 16;
+        x[i] = a.q.base[0] + (m < a.q.rows ? m : a.q.rows - 1) * a.q.ld[0];
+    }
+    f32x4 acc[2][PT][QT];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < PT; ++j)
+#pragma unroll
+            for (int i = 0; i < QT; ++i)
+                acc[h][j][i] = f32x4{};
+    // N steps from k, loads first; the last step of the sum may be cut short.
+    auto steps = [&](int64_t k, auto count, auto whole) {
+        constexpr int N = decltype(count)::value;
+        u32x4 fw[N][2][PT], fx[N][QT];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int64_t kk = k + u * kK + k0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < PT; ++j)
+                    fw[u][h][j] = decltype(whole)::value ? load16(w[h][j] + kk)
+                                                         : load_chunk(w[h][j], (int)kk, a.k);
+#pragma unroll
+            for (int i = 0; i < QT; ++i)
+                fx[u][i] = decltype(whole)::value ? load16(x[i] + kk)
+                                                  : load_chunk(x[i], (int)kk, a.k);
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < PT; ++j)
+#pragma unroll
+                    for (int i = 0; i < QT; ++i)
+                        acc[h][j][i] = Step<T>::mma(__builtin_bit_cast(Frag, fw[u][h][j]),
+                                                    __builtin_bit_cast(Frag, fx[u][i]),
+                                                    acc[h][j][i]);
+    };
+    const int whole = a.k / kK, all = (a.k + kK - 1) / kK;
+    int s = (int)((int64_t)all * wave / NW);
+    const int end = (int)((int64_t)all * (wave + 1) / NW);
+    const int full = end < whole ? end : whole;
+    using std::integral_constant;
+    for (; s + U <= full; s += U)
+        steps((int64_t)s * kK, integral_constant<int, U>(), integral_constant<bool, true>());
+    for (; s < full; ++s)
+        steps((int64_t)s * kK, integral_constant<int, 1>(), integral_constant<bool, true>());
+    if (s < end)
+        steps((int64_t)s * kK, integral_constant<int, 1>(), integral_constant<bool, false>());
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < PT; ++j)
+#pragma unroll
+            for (int i = 0; i < QT; ++i)
+                *reinterpret_cast<f32x4*>(&part[wave][(h * PT + j) * QT + i][l * 4]) = acc[h][j][i];
+    __syncthreads();
+    const Gate<T, BWD> gate{a};
+    for (int t = threadIdx.x; t < 256 * PT * QT; t += NW * 64) {
+        const int n = t % (16 * PT), m = t / (16 * PT);
+        const int tile = n / 16 * QT + m / 16, at = (n % 16 / 4 * 16 + m % 16) * 4 + n % 4;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NW; ++v) {
+            g += part[v][tile][at];
+            u += part[v][PT * QT + tile][at];
+        }
+        if (m < a.q.rows)
+            gate(m, n0 + n, g, u);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The parts of a split sum, added in order.
+// ---------------------------------------------------------------------------
+
+// dx, dWg, dWu: four columns a thread.
+template <typename T, int MODE>
+__global__ __launch_bounds__(256) void sum_parts_kernel(const GemmArgs<T> a)
+{
+    constexpr int kPlanes = MODE == kDw ? 2 : 1;
+    const int64_t per_row = a.part_ld / 4, rows = (int64_t)a.q.rows * kPlanes;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= rows * per_row)
+        return;
+    const int64_t row = at / per_row;
+    const int n = (int)(at % per_row) * 4;
+    const float* p = a.part + row * a.part_ld + n;
+    f32x4 v = f32x4{};
+    for (int s = 0; s < a.splits; ++s)
+        v += *reinterpret_cast<const f32x4*>(p + s * rows * a.part_ld);
+    const int plane = row >= a.q.rows;
+    T* out = (plane ? a.out[1] : a.out[0]) +
+             (row - (plane ? a.q.rows : 0)) * (plane ? a.ldo[1] : a.ldo[0]) + n;
+    const int left = a.out_cols - n;
+    if (left >= 4)
+        store4(out, v);
+    else
+        store_some(out, v, left);
+}
+
+// g and u, and the unit: one element a thread.
+template <typename T, bool BWD>
+__global__ __launch_bounds__(256) void gate_parts_kernel(const GemmArgs<T> a)
+{
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = at / a.out_cols;
+    if (m >= a.q.rows)
+        return;
+    const int c = (int)(at % a.out_cols);
+    const float* p = a.part + m * a.part_ld + c / 32 * 64 + c % 32;
+    float g = 0.0f, u = 0.0f;
+    for (int s = 0; s < a.splits; ++s) {
+        g += p[0];
+        u += p[32];
+        p += (int64_t)a.q.rows * a.part_ld;
+    }
+    Gate<T, BWD>{a}(m, c, g, u);
 }
 
 // ---------------------------------------------------------------------------
@@ -979,19 +1203,86 @@ static bool matrix_ok(const void* p, size_t rows, size_t cols, size_t ld, size_t
 
 static size_t padded(size_t hidden) { return (hidden + 63) / 64 * 64; }
 
-// Blocks that are on the GPU together, by their LDS (160 KiB a CU); a
-// multiple of the 8 XCDs.
-static int resident_blocks(int lds_bytes)
+constexpr int kCus = 256;
+
+// How a product is computed: 256 x 256 tiles or 128 x 128, and in how many
+// parts its sum is split (128 x 128 tiles only).
+struct Plan {
+    bool big;
+    int splits;
+};
+
+// The least of the estimated times.  A block's step of 128 bytes of k takes
+// what its instructions take (a bf16 128 x 128 step 0.4 us of a CU, binary32
+// 1.75 us; a 256 x 256 step 1.2 and 7 us), and no less than the 0.7 us its
+// loads take, which two blocks of a CU share; parts are written and read
+// again at some 4 TB/s, by one more launch (3 us).  Measured, bf16, one
+// unsplit tile shape against the other and splits of 1 to 16 on both sides
+// of each choice: see the figures beside gemm_run.
+static Plan make_plan(int64_t rows, int64_t cols, int64_t k, int planes, int sums, size_t es,
+                      bool aligned)
 {
-    int device = 0, cus = 0;
-    if (hipGetDevice(&device) != hipSuccess ||
-        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess)
-        cus = 256;
-    const int n = cus * ((160 << 10) / lds_bytes) / 8 * 8;
-    return n > 8 ? n : 8;
+    const int64_t steps = (k + 128 / (int64_t)es - 1) / (128 / (int64_t)es) * sums;
+    const double work = es == 2 ? 0.4 : 1.75, big_step = es == 2 ? 1.2 : 7.0;
+    const int64_t tiles = (rows + 127) / 128 * ((cols + 127) / 128) * planes;
+    const int64_t bigs = (rows + 255) / 256 * ((cols + 255) / 256) * planes;
+    Plan best{false, 1};
+    double least = 1e30;
+    for (int s = 1; s <= 32 && (s == 1 || s * 2 <= steps); s *= 2) {
+        const int64_t blocks = (tiles * s + kCus - 1) / kCus;  // of a CU
+        double step = work * (double)blocks, loads = 0.7 * (double)((blocks + 1) / 2);
+        step = step > loads ? step : loads;
+        double t = step * (double)((steps + s - 1) / s);
+        if (s > 1)
+            t += 3.0 + (double)(tiles * s) * (128 * 128 * 8) / 4e6;
+        if (t < least) {
+            least = t;
+            best.splits = s;
+        }
+    }
+    if (aligned && (double)((bigs + kCus - 1) / kCus) * big_step * (double)steps < least)
+        best = Plan{true, 1};
+    return best;
 }
 
-template <typename T, int MODE>
+// Columns of a part: P's rows (kUp) or the result's, in whole vectors.
+static int64_t part_ld(int mode, int64_t cols)
+{
+    return mode == kUp ? (cols + 63) / 64 * 128 : (cols + 3) / 4 * 4;
+}
+
+static size_t part_bytes(int mode, int64_t rows, int64_t cols, int64_t k, size_t es)
+{
+    size_t most = 0;
+    const int planes = mode == kDw ? 2 : 1;
+    for (int aligned = 0; aligned < 2; ++aligned) {
+        const Plan p = make_plan(rows, mode == kUp ? 2 * cols : cols, k, planes,
+                                 mode == kDx ? 2 : 1, es, aligned != 0);
+        const size_t n = p.splits > 1
+                             ? (size_t)p.splits * planes * rows * part_ld(mode, cols) * sizeof(float)
+                             : 0;
+        most = n > most ? n : most;
+    }
+    return most;
+}
+
+// Most tokens of the kernel that reads the weights once.
+constexpr int kFewTokens = 32;
+
+// Blocks that are on the GPU together, by their LDS (160 KiB a CU); a
+// multiple of the 8 XCDs.
+static int resident_blocks(int lds_bytes) { return kCus * ((160 << 10) / lds_bytes); }
+
+static int launch_over(const void* fn, int64_t n, void** args, hipStream_t stream)
+{
+    const int64_t grid = (n + 255) / 256;
+    if (grid >= ((int64_t)1 << 24))
+        return MESWISH_EINVAL;
+    return launch(fn, dim3((unsigned)grid), 256, args, stream);
+}
+
+// resident > 0: at most so many blocks, each looping over tiles.
+template <typename T, int MODE, bool BWD>
 static int gemm_launch(GemmArgs<T>& a, const void* fn, int bm, int bn, int block, int resident,
                        hipStream_t stream)
 {
@@ -1004,8 +1295,17 @@ static int gemm_launch(GemmArgs<T>& a, const void* fn, int bm, int bn, int block
     if (grid >= ((int64_t)1 << 23))
         return MESWISH_EINVAL;
     void* args[] = {&a};
-    return launch(fn, dim3((unsigned)(resident && grid > resident ? resident : grid)), block, args,
-                  stream);
+    int rc = launch(fn, dim3((unsigned)(resident && grid > resident ? resident : grid), a.splits),
+                    block, args, stream);
+    if (rc != MESWISH_OK || a.splits == 1)
+        return rc;
+    if constexpr (MODE == kUp)
+        return launch_over(reinterpret_cast<const void*>(&gate_parts_kernel<T, BWD>),
+                           (int64_t)a.q.rows * a.out_cols, args, stream);
+    else
+        return launch_over(reinterpret_cast<const void*>(&sum_parts_kernel<T, MODE>),
+                           (int64_t)a.q.rows * (MODE == kDw ? 2 : 1) * (a.part_ld / 4), args,
+                           stream);
 }
 
 // Every row of the operands starts on a 16-byte boundary and the loads' 16
@@ -1024,29 +1324,58 @@ static bool aligned_rows(const GemmArgs<T>& a)
     return MODE != kDx || (a.p.ld[0] == a.p.ld[1] && a.q.ld[0] == a.q.ld[1]);
 }
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP>
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, bool PARTS>
 static int gemm_fast(GemmArgs<T>& a, hipStream_t stream)
 {
-    return gemm_launch<T, MODE>(
-        a, reinterpret_cast<const void*>(&gemm_fast_kernel<T, MODE, BWD, WM, WN, MT, NT, KB, NS, SP>),
+    constexpr int kLds = 2 * (WM * MT + WN * NT) * 16 * 128;
+    return gemm_launch<T, MODE, BWD>(
+        a,
+        reinterpret_cast<const void*>(
+            &gemm_fast_kernel<T, MODE, BWD && !PARTS, WM, WN, MT, NT, 128, 2, 1, PARTS>),
         WM * MT * 16, WN * NT * 16, WM * WN * 64,
-        MODE == kUp ? resident_blocks(NS * (WM * MT + WN * NT) * 16 * KB) : 0, stream);
+        MODE == kUp && !PARTS ? resident_blocks(kLds) : 0, stream);
 }
 
-template <typename T, int MODE, bool BWD>
-static int gemm_run(GemmArgs<T>& a, hipStream_t stream)
+template <typename T, bool BWD, int PT, int QT>
+static int few_tokens(GemmArgs<T>& a, hipStream_t stream)
 {
-    if (aligned_rows<T, MODE>(a)) {
-        const int cols = MODE == kUp ? 128 : 256;
-        const int64_t big = (int64_t)((a.q.rows + 255) / 256) * ((a.out_cols + cols - 1) / cols) *
-                            (MODE == kDw ? 2 : 1);
-        if (big >= 256)
-            return gemm_fast<T, MODE, BWD, 2, 4, 8, 4, 128, 2, 1>(a, stream);
-        return gemm_fast<T, MODE, BWD, 2, 2, 4, 4, 128, 2, 1>(a, stream);
+    void* args[] = {&a};
+    return launch(reinterpret_cast<const void*>(&few_tokens_kernel<T, BWD, PT, QT, 8>),
+                  dim3((unsigned)((a.out_cols + 16 * PT - 1) / (16 * PT))), 512, args, stream);
+}
+
+// part: memory for the parts of a split sum.
+template <typename T, int MODE, bool BWD>
+static int gemm_run(GemmArgs<T>& a, float* part, hipStream_t stream)
+{
+    a.splits = 1;
+    if (a.q.rows == 0 || a.out_cols == 0)
+        return MESWISH_OK;
+    if constexpr (MODE == kUp) {
+        if (a.q.rows <= kFewTokens)
+            return a.q.rows <= 16 ? few_tokens<T, BWD, 1, 1>(a, stream)
+                                  : few_tokens<T, BWD, 2, 2>(a, stream);
     }
-    return gemm_launch<T, MODE>(
-        a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD>), kAnyTile, kAnyTile, 256, 0,
-        stream);
+    const bool fast = aligned_rows<T, MODE>(a);
+    // kUp's result is as wide as the workspace's rows; the plan goes by the
+    // hidden units.
+    const int64_t cols = MODE == kUp ? a.p.rows : a.out_cols;
+    const Plan p = make_plan(a.q.rows, MODE == kUp ? 2 * cols : cols, a.k, MODE == kDw ? 2 : 1,
+                             MODE == kDx ? 2 : 1, sizeof(T), fast);
+    a.splits = p.splits;
+    a.part = part;
+    a.part_ld = (int)part_ld(MODE, cols);
+    if (p.splits > 1)
+        return fast ? gemm_fast<T, MODE, BWD, 2, 2, 4, 4, true>(a, stream)
+                    : gemm_launch<T, MODE, BWD>(
+                          a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, false, true>),
+                          kAnyTile, kAnyTile, 256, 0, stream);
+    if (!fast)
+        return gemm_launch<T, MODE, BWD>(
+            a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD, false>), kAnyTile,
+            kAnyTile, 256, 0, stream);
+    return p.big ? gemm_fast<T, MODE, BWD, 2, 4, 8, 4, false>(a, stream)
+                 : gemm_fast<T, MODE, BWD, 2, 2, 4, 4, false>(a, stream);
 }
 
 template <typename T>
@@ -1060,7 +1389,7 @@ static Operand<T> operand(const void* a, size_t lda, const void* b, size_t ldb, 
 template <typename T>
 static int fwd(int act, float param, const void* x, size_t ldx, const void* wg, size_t ldwg,
                const void* wu, size_t ldwu, size_t tokens, size_t dim, size_t hidden, void* h,
-               size_t ldh, hipStream_t stream)
+               size_t ldh, void* workspace, hipStream_t stream)
 {
     GemmArgs<T> a{};
     a.p = operand<T>(wg, ldwg, wu, ldwu, hidden);
@@ -1071,7 +1400,7 @@ static int fwd(int act, float param, const void* x, size_t ldx, const void* wg, 
     a.out_cols = (int)hidden;
     a.act = act;
     a.coef = make_coef(act, param);
-    return gemm_run<T, kUp, false>(a, stream);
+    return gemm_run<T, kUp, false>(a, static_cast<float*>(workspace), stream);
 }
 
 template <typename T>
@@ -1083,6 +1412,7 @@ static int bwd(int act, float param, const void* x, size_t ldx, const void* wg, 
     const size_t fp = padded(hidden);
     T* dg = static_cast<T*>(workspace);
     T* du = dg + tokens * fp;
+    float* part = reinterpret_cast<float*>(du + tokens * fp);
     GemmArgs<T> a{};
     a.p = operand<T>(wg, ldwg, wu, ldwu, hidden);
     a.q = operand<T>(x, ldx, x, ldx, tokens);
@@ -1097,7 +1427,7 @@ static int bwd(int act, float param, const void* x, size_t ldx, const void* wg, 
     a.ldh = (int64_t)ldh;
     a.act = act;
     a.coef = make_coef(act, param);
-    int rc = gemm_run<T, kUp, true>(a, stream);
+    int rc = gemm_run<T, kUp, true>(a, part, stream);
     if (rc == MESWISH_OK && dx) {
         GemmArgs<T> b{};
         b.p = operand<T>(wg, ldwg, wu, ldwu, dim);
@@ -1106,7 +1436,7 @@ static int bwd(int act, float param, const void* x, size_t ldx, const void* wg, 
         b.out[0] = static_cast<T*>(dx);
         b.ldo[0] = (int64_t)lddx;
         b.out_cols = (int)dim;
-        rc = gemm_run<T, kDx, false>(b, stream);
+        rc = gemm_run<T, kDx, false>(b, part, stream);
     }
     if (rc == MESWISH_OK && dwg) {
         GemmArgs<T> b{};
@@ -1119,7 +1449,7 @@ static int bwd(int act, float param, const void* x, size_t ldx, const void* wg, 
         b.ldo[0] = (int64_t)lddwg;
         b.ldo[1] = (int64_t)lddwu;
         b.out_cols = (int)dim;
-        rc = gemm_run<T, kDw, false>(b, stream);
+        rc = gemm_run<T, kDw, false>(b, part, stream);
     }
     return rc;
 }
@@ -1145,9 +1475,18 @@ using namespace meblock;
 extern "C" size_t gated_ffn_workspace_bytes(size_t tokens, size_t dim, size_t hidden, int dtype,
                                             int backward)
 {
-    if (!dtype_ok(dtype) || !sizes_ok(tokens, dim, hidden) || !backward)
+    if (!dtype_ok(dtype) || !sizes_ok(tokens, dim, hidden))
         return 0;
-    return 2 * tokens * padded(hidden) * elem_size(dtype);
+    const size_t es = elem_size(dtype);
+    const int64_t m = (int64_t)tokens, d = (int64_t)dim, f = (int64_t)hidden;
+    size_t part = tokens <= (size_t)kFewTokens ? 0 : part_bytes(kUp, m, f, d, es);
+    if (!backward)
+        return part;
+    // dg and du, then the parts of one split sum at a time.
+    const size_t dx = part_bytes(kDx, m, d, f, es), dw = part_bytes(kDw, f, d, m, es);
+    part = part > dx ? part : dx;
+    part = part > dw ? part : dw;
+    return 2 * tokens * padded(hidden) * es + part;
 }
 
 extern "C" int gated_ffn_fwd(int act, float param, const void* x, size_t ldx, const void* wg,
@@ -1172,8 +1511,10 @@ extern "C" int gated_ffn_fwd(int act, float param, const void* x, size_t ldx, co
         return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
     return dtype == MESWISH_F32
-               ? fwd<float>(act, param, x, ldx, wg, ldwg, wu, ldwu, tokens, dim, hidden, h, ldh, s)
-               : fwd<bf16_t>(act, param, x, ldx, wg, ldwg, wu, ldwu, tokens, dim, hidden, h, ldh, s);
+               ? fwd<float>(act, param, x, ldx, wg, ldwg, wu, ldwu, tokens, dim, hidden, h, ldh, workspace,
+                            s)
+               : fwd<bf16_t>(act, param, x, ldx, wg, ldwg, wu, ldwu, tokens, dim, hidden, h, ldh, workspace,
+                             s);
 }
 
 extern "C" int gated_ffn_bwd(int act, float param, const void* x, size_t ldx, const void* wg,
