@@ -26,28 +26,30 @@ import torch
 import torch.nn as nn
 
 from . import _lib
-from .dense import EPS, SharedBuffer, _current
-from .functional import _act_code, _dtype_code, _require_device, _stream
-from .norm import _out_rows, as_rows, layer_norm_bwd, layer_norm_fwd
+from .dense import EPS, SharedBuffer
+from .functional import _act_code, _dtype_code, _require_device
+from .norm import _out_rows, as_rows, launch, layer_norm_bwd, layer_norm_fwd, library
+
+
+def _weight(x: torch.Tensor, w: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
+    """w and its row distance, checked against x."""
+    if not w.is_cuda:
+        _require_device(w, name)
+    if w.get_device() != x.get_device():
+        raise ValueError(f"x and {name} are on different devices")
+    if w.dtype is not x.dtype:
+        raise TypeError(f"x and {name} have different dtypes ({x.dtype}, {w.dtype})")
+    if w.dim() != 2 or w.shape[1] != x.shape[-1]:
+        raise ValueError(f"{name} must be [hidden, {x.shape[-1]}], got {tuple(w.shape)}")
+    w, _, _, ld = as_rows(w, name)
+    return w, ld
 
 
 def _weights(x, w_gate, w_up):
-    """Both weights as (tensor, ld), checked against x."""
-    got = []
-    for name, w in (("w_gate", w_gate), ("w_up", w_up)):
-        _require_device(w, name)
-        if w.device != x.device:
-            raise ValueError(f"x and {name} are on different devices")
-        if w.dtype != x.dtype:
-            raise TypeError(f"x and {name} have different dtypes ({x.dtype}, {w.dtype})")
-        if w.dim() != 2 or w.shape[1] != x.shape[-1]:
-            raise ValueError(f"{name} must be [hidden, {x.shape[-1]}], got {tuple(w.shape)}")
-        w, _, _, ld = as_rows(w, name)
-        got.append((w, ld))
     if w_gate.shape != w_up.shape:
         raise ValueError(f"w_gate and w_up have different shapes ({tuple(w_gate.shape)}, "
                          f"{tuple(w_up.shape)})")
-    return got
+    return _weight(x, w_gate, "w_gate"), _weight(x, w_up, "w_up")
 
 
 def _param_value(kind: str, param: float | None) -> float:
@@ -57,16 +59,16 @@ def _param_value(kind: str, param: float | None) -> float:
 def _tokens(x: torch.Tensor) -> int:
     n = 1
     for s in x.shape[:-1]:
-        n *= int(s)
+        n *= s
     return n
 
 
 def _workspace(tokens, dim, hidden, code, backward, device, shared):
-    nbytes = _lib.library().gated_ffn_workspace_bytes(tokens, dim, hidden, code, backward)
+    nbytes = library().gated_ffn_workspace_bytes(tokens, dim, hidden, code, backward)
     if nbytes == 0:
         return None, 0
     ws = (shared or SharedBuffer()).workspace(nbytes, device)
-    return ws, ws.numel()
+    return ws, nbytes
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -90,13 +92,11 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, kin
         if out.shape != shape or out.dtype != x.dtype or out.device != x.device:
             raise ValueError(f"out must be a {x.dtype} tensor of shape {shape} on {x.device}")
         h, ldh = _out_rows(out, out, "out")
-    ws, nbytes = _workspace(tokens, dim, hidden, code, 0, x.device, shared)
-    with _current(x.device):
-        st = _lib.library().gated_ffn_fwd(
-            act, _param_value(kind, param), x.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(),
-            ldu, tokens, dim, hidden, h.data_ptr(), ldh, _ptr(ws), nbytes, code,
-            _stream(x.device))
-    _lib.check(st, f"gated_ffn_fwd({kind})")
+    device = x.device
+    ws, nbytes = _workspace(tokens, dim, hidden, code, 0, device, shared)
+    launch("gated_ffn_fwd", f"gated_ffn_fwd({kind})", device, act, _param_value(kind, param),
+           x.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu, tokens, dim, hidden,
+           h.data_ptr(), ldh, _ptr(ws), nbytes, code)
     return h
 
 
@@ -109,7 +109,8 @@ def gated_ffn_bwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, dh:
     What is not needed is None.  ``shared`` lends its workspace."""
     act = _act_code(kind)
     code = _dtype_code(x)
-    _require_device(dh, "dh")
+    if not dh.is_cuda:
+        _require_device(dh, "dh")
     x, _, dim, ldx = as_rows(x, "x")
     (wg, ldg), (wu, ldu) = _weights(x, w_gate, w_up)
     tokens, hidden = _tokens(x), w_gate.shape[0]
@@ -123,13 +124,12 @@ def gated_ffn_bwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, dh:
         dwg = torch.empty((hidden, dim), dtype=x.dtype, device=x.device)
         dwu = torch.empty((hidden, dim), dtype=x.dtype, device=x.device)
     h = torch.empty(dh.shape, dtype=x.dtype, device=x.device) if need_h else None
-    ws, nbytes = _workspace(tokens, dim, hidden, code, 1, x.device, shared)
-    with _current(x.device):
-        st = _lib.library().gated_ffn_bwd(
-            act, _param_value(kind, param), x.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(),
-            ldu, dh.data_ptr(), lddh, tokens, dim, hidden, _ptr(dx), dim, _ptr(dwg), dim,
-            _ptr(dwu), dim, _ptr(h), hidden, _ptr(ws), nbytes, code, _stream(x.device))
-    _lib.check(st, f"gated_ffn_bwd({kind})")
+    device = x.device
+    ws, nbytes = _workspace(tokens, dim, hidden, code, 1, device, shared)
+    launch("gated_ffn_bwd", f"gated_ffn_bwd({kind})", device, act, _param_value(kind, param),
+           x.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu, dh.data_ptr(), lddh, tokens,
+           dim, hidden, _ptr(dx), dim, _ptr(dwg), dim, _ptr(dwu), dim, _ptr(h), hidden, _ptr(ws),
+           nbytes, code)
     return (dx, dwg, dwu, h) if need_h else (dx, dwg, dwu)
 
 

@@ -22,23 +22,48 @@ import torch
 import torch.nn as nn
 
 from . import _lib
-from .dense import EPS, SharedBuffer, _current
-from .functional import _dtype_code, _require_device, _same, _stream
+from .dense import EPS, SharedBuffer
+from .functional import _dtype_code, _require_device, _same
+
+# The current stream's handle by device index, and the current device,
+# without building objects for every call (0.1 us each against 2 and 0.5 of a
+# call's 10).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_device_index = torch._C._cuda_getDevice
+
+
+def library():
+    return _lib._LIB or _lib.library()
+
+
+def launch(name: str, what: str, device: torch.device, *args) -> None:
+    """The library's function on the device's current stream; raises on a
+    status that is not zero."""
+    i = device.index
+    if i == _device_index():
+        st = getattr(library(), name)(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(device):
+            st = getattr(library(), name)(*args, _raw_stream(i))
+    if st:
+        _lib.check(st, what)
 
 
 def as_rows(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int, int, int]:
     """(t, rows, n, ld): t as rows of n contiguous elements, ld elements
     apart; copied only if its strides allow no such reading."""
-    _require_device(t, name)
-    if t.dim() == 0:
+    if not t.is_cuda:
+        _require_device(t, name)
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    n = t.shape[-1]
+    n = shape[-1]
     if t.is_contiguous():
         return t, (t.numel() // n if n else 0), n, n
     if t.stride(-1) == 1 or n == 1:
         # Every leading dimension steps over whole blocks of the next.
         ld, ok, span = None, t.numel() > 0, 1
-        for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
             if size == 1:
                 continue
             if ld is None:
@@ -56,17 +81,16 @@ def as_rows(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int, int, int]:
 def _param(p: torch.Tensor | None, n: int, like: torch.Tensor, name: str) -> int | None:
     if p is None:
         return None
-    if p.dtype not in (torch.float32, torch.bfloat16):
+    if p.dtype is not torch.float32 and p.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be float32 or bfloat16, got {p.dtype}")
-    if p.shape != (n,) or not p.is_contiguous() or p.device != like.device:
+    if p.shape != (n,) or not p.is_contiguous() or p.get_device() != like.get_device():
         raise ValueError(f"{name} must be a contiguous tensor of {n} values on {like.device}")
     return p.data_ptr()
 
 
 def _out_rows(out: torch.Tensor | None, x: torch.Tensor, name: str):
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        return out, x.shape[-1]
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[-1]
     _same(x, out, "x", name)
     view, _, _, ld = as_rows(out, name)
     if view is not out:
@@ -91,13 +115,10 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None,
     wp, bp = _param(weight, n, x, "weight"), _param(bias, n, x, "bias")
     pcode = _param_code(weight, bias, x)
     y, ldy = _out_rows(out, x, "out")
-    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
-    with _current(x.device):
-        st = _lib.library().layer_norm_fwd(x.data_ptr(), ldx, wp, bp, rows, n, float(eps),
-                                           y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(),
-                                           code, pcode, _stream(x.device))
-    _lib.check(st, "layer_norm_fwd")
+    device = x.device
+    mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=device).unbind(0)
+    launch("layer_norm_fwd", "layer_norm_fwd", device, x.data_ptr(), ldx, wp, bp, rows, n, eps,
+           y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), code, pcode)
     return y, mean, rstd
 
 
@@ -109,34 +130,30 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: 
     statistics the forward returned.  dweight and dbias have weight's dtype
     (x's without a weight); None if ``need_params`` is False.  ``shared``
     lends its workspace."""
-    _require_device(x, "x")
-    _require_device(dy, "dy")
-    _same(x, dy, "x", "dy")
     code = _dtype_code(x)
     x, rows, n, ldx = as_rows(x, "x")
     dy, _, _, lddy = as_rows(dy, "dy")
+    _same(x, dy, "x", "dy")
+    device, lead = x.device, x.shape[:-1]
     for name, t in (("mean", mean), ("rstd", rstd)):
-        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or t.device != x.device or \
+        if t.dtype is not torch.float32 or t.shape != lead or t.device != device or \
                 not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous float32 tensor of shape "
-                             f"{tuple(x.shape[:-1])} on {x.device}")
+                             f"{tuple(lead)} on {device}")
     wp = _param(weight, n, x, "weight")
     pcode = _param_code(weight, None, x)
     dx, lddx = _out_rows(out, x, "out")
-    dw = db = ws = None
+    dw = db = wsp = None
+    nbytes = 0
     if need_params:
-        params = torch.empty((2, n), dtype=x.dtype if weight is None else weight.dtype,
-                             device=x.device)
-        dw, db = params[0], params[1]
-        nbytes = _lib.library().layer_norm_workspace_bytes(rows, n)
-        ws = (shared or SharedBuffer()).workspace(nbytes, x.device)
-    with _current(x.device):
-        st = _lib.library().layer_norm_bwd(
-            x.data_ptr(), ldx, dy.data_ptr(), lddy, mean.data_ptr(), rstd.data_ptr(), wp, rows, n,
-            dx.data_ptr(), lddx, dw.data_ptr() if need_params else None,
-            db.data_ptr() if need_params else None, ws.data_ptr() if need_params else None,
-            ws.numel() if need_params else 0, code, pcode, _stream(x.device))
-    _lib.check(st, "layer_norm_bwd")
+        dw, db = torch.empty((2, n), dtype=x.dtype if weight is None else weight.dtype,
+                             device=device).unbind(0)
+        ws = (shared or SharedBuffer()).workspace(library().layer_norm_workspace_bytes(rows, n), device)
+        wsp, nbytes = ws.data_ptr(), ws.numel()
+    launch("layer_norm_bwd", "layer_norm_bwd", device, x.data_ptr(), ldx, dy.data_ptr(), lddy,
+           mean.data_ptr(), rstd.data_ptr(), wp, rows, n, dx.data_ptr(), lddx,
+           dw.data_ptr() if need_params else None, db.data_ptr() if need_params else None, wsp,
+           nbytes, code, pcode)
     return dx, dw, db
 
 
