@@ -1,12 +1,16 @@
 // layer_norm.hip -- layer normalization of libmeswish for gfx950, forward
 // and backward.  Formulas and contracts: include/layer_norm.h.
 //
-// Bound: HBM bandwidth (8 flops an element forward, 15 backward).  Both
+// Bound: HBM bandwidth (8 flops an element forward, 15 backward).  Measured on
+// bf16 16384 x 4096: forward 46 us (5.8 TB/s of the rows read and written),
+// backward 90 us (4.5 TB/s); the framework's plain copy moves 6.3 TB/s.  Both
 // directions read each row once and keep it in registers, packed as loaded:
 //   * A group of G threads owns a row, thread g holding the 16-byte vectors
-//     g, G + g, ... (V of them).  G is 4 or 16 lanes of a wave, a wave, or a
-//     block of 256 or 1024 threads, so the two sums of a row cost lane
-//     exchanges only, or one exchange through LDS a batch of rows.
+//     g, G + g, ... (V of them).  G is 4 to 64 lanes of a wave, or a block of
+//     256 or 1024 threads, so the sums of a row cost lane exchanges only, or
+//     one exchange through LDS a batch of R rows.  (bf16 16384 x 4096 forward:
+//     a block a row 46 us; a wave a row, V = 8, 66 us: its registers leave too
+//     few waves.)
 //   * The variance is the mean of squared differences from the mean, from
 //     the registers: no cancellation of E[x^2] - mean^2.
 //   * Backward: a thread owns the same columns in every row its block takes,
@@ -26,8 +30,14 @@
 
 namespace meblock {
 
-// Most blocks of the backward, each with its own partial sums.
+// Most blocks of the backward, each with its own partial sums
+// (512: two of 256 threads on a CU.  Measured, bf16 16384 x 4096 backward: 384
+// blocks 102 us, 512 92, 768 95, 1024 115: more of them write more parts.)
 constexpr int kMaxParts = 512;
+// Most blocks of the forward, each keeping its columns of the parameters in
+// registers: eight of 256 threads on a CU (bf16 16384 x 4096: 2048 blocks 47 us,
+// 1536 55; one block a row, reading the parameters again, 64).
+constexpr int kFwdBlocks = 2048;
 constexpr int64_t kMaxGrid = 1 << 23;
 
 template <int G>
@@ -38,9 +48,11 @@ struct Group {
 };
 
 // Sum of K values over each group of G threads, the result in every thread.
-// Waves combine through `lds` (K * kWaves floats); two barriers.
+// Waves combine through `lds` (2 K kWaves floats); calls alternate between
+// its halves (`turn`), so that one barrier a call is enough: a half is written
+// again only after the barrier of the call between.
 template <int G, int K>
-__device__ __forceinline__ void group_sum(float (&v)[K], float* lds)
+__device__ __forceinline__ void group_sum(float (&v)[K], float* lds, int& turn)
 {
 #pragma unroll
     for (int m = 1; m < (G < 64 ? G : 64); m <<= 1)
@@ -50,7 +62,8 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float* lds)
     if constexpr (G > 64) {
         constexpr int W = Group<G>::kWaves;
         const int wave = threadIdx.x / 64;
-        __syncthreads();
+        lds += turn * (K * W);
+        turn ^= 1;
         if (threadIdx.x % 64 == 0)
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -67,107 +80,114 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float* lds)
     }
 }
 
-// E whole parameters from e0, or `none` where there are no parameters.
+// Parameters e0 .. e0 + E - 1 of n, `none` past the end and where there are no
+// parameters.
 template <int E, typename P>
-__device__ __forceinline__ void load_params(const P* p, int e0, float none, float* f)
+__device__ __forceinline__ void load_params(const P* p, int e0, int n, float none, float* f)
 {
     constexpr int K = Elem<P>::kPerVec;
-    if (!p) {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            f[j] = none;
-    } else if constexpr (E >= K) {
+    if (p && e0 + E <= n && E >= K) {
 #pragma unroll
         for (int j = 0; j < E; j += K)
             Elem<P>::unpack(load16(p + e0 + j), f + j);
     } else {
 #pragma unroll
         for (int j = 0; j < E; ++j)
-            f[j] = Elem<P>::get(p[e0 + j]);
+            f[j] = p && e0 + j < n ? Elem<P>::get(p[e0 + j]) : none;
     }
 }
 
 // ---------------------------------------------------------------------------
 // Forward.
 // ---------------------------------------------------------------------------
-template <typename T, typename P, int G, int V>
+// The block keeps its columns of weight and bias in registers and loops over
+// rows, R of a group at a time (their loads in flight together, their sums in
+// one exchange).
+template <typename T, typename P, int G, int V, int R>
 __global__ __launch_bounds__(Group<G>::kThreads) void ln_fwd_kernel(
-    const T* __restrict__ x, int64_t ldx, const P* __restrict__ w, const P* __restrict__ b,
-    int64_t rows, int n, float eps, T* y, int64_t ldy, float* __restrict__ mean,
-    float* __restrict__ rstd)
+    const T* x, int64_t ldx, const P* __restrict__ w, const P* __restrict__ b, int64_t rows, int n,
+    float eps, T* y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd)
 {
     constexpr int E = Elem<T>::kPerVec;
     constexpr int NG = Group<G>::kGroups;
-    __shared__ float lds[G > 64 ? Group<G>::kWaves : 1];
-    const int g = threadIdx.x % G;
+    __shared__ float lds[G > 64 ? 2 * R * Group<G>::kWaves : 1];
+    int turn = 0;
+    const int g = threadIdx.x % G, grp = threadIdx.x / G;
     const float inv_n = 1.0f / (float)n;
-    // Threads of one group agree on the row; a group of whole blocks meets
+    float wf[V][E], bf[V][E];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        load_params<E>(w, (v * G + g) * E, n, 1.0f, wf[v]);
+        load_params<E>(b, (v * G + g) * E, n, 0.0f, bf[v]);
+    }
+    // Threads of one group agree on the rows; a group of whole blocks meets
     // every barrier together.
-    for (int64_t row = (int64_t)blockIdx.x * NG + threadIdx.x / G; row < rows;
-         row += (int64_t)gridDim.x * NG) {
-        const T* xr = x + row * ldx;
-        u32x4 raw[V];
+    for (int64_t base = (int64_t)blockIdx.x * (NG * R); base < rows;
+         base += (int64_t)gridDim.x * (NG * R)) {
+        u32x4 raw[R][V];
+        float s[R], q[R];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            raw[v] = load_chunk(xr, (v * G + g) * E, n);
-        float s[1] = {0.0f};
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = base + r * NG + grp;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float f[E];
-            Elem<T>::unpack(raw[v], f);
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                s[0] += f[j];
+            for (int v = 0; v < V; ++v)  // a row past the end counts as an empty one
+                raw[r][v] = load_chunk(x + row * ldx, (v * G + g) * E, row < rows ? n : 0);
         }
-        group_sum<G>(s, lds);
-        const float mu = s[0] * inv_n;
-        float q[1] = {0.0f};
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e0 = (v * G + g) * E;
-            float f[E];
-            Elem<T>::unpack(raw[v], f);
-            if (e0 + E <= n) {
+        for (int r = 0; r < R; ++r) {
+            s[r] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float f[E];
+                Elem<T>::unpack(raw[r][v], f);
 #pragma unroll
                 for (int j = 0; j < E; ++j)
-                    q[0] = fmaf(f[j] - mu, f[j] - mu, q[0]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j)
-                    q[0] += e0 + j < n ? (f[j] - mu) * (f[j] - mu) : 0.0f;
+                    s[r] += f[j];
             }
         }
-        group_sum<G>(q, lds);
-        const float r = 1.0f / sqrtf(fmaf(q[0], inv_n, eps));
-        if (g == 0) {
-            if (mean)
-                mean[row] = mu;
-            if (rstd)
-                rstd[row] = r;
+        group_sum<G>(s, lds, turn);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] *= inv_n;
+            q[r] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e0 = (v * G + g) * E;
+                float f[E];
+                Elem<T>::unpack(raw[r][v], f);
+                if (e0 + E <= n) {
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        q[r] = fmaf(f[j] - s[r], f[j] - s[r], q[r]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        q[r] += e0 + j < n ? (f[j] - s[r]) * (f[j] - s[r]) : 0.0f;
+                }
+            }
         }
-        T* yr = y + row * ldy;
+        group_sum<G>(q, lds, turn);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e0 = (v * G + g) * E;
-            if (e0 >= n)
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = base + r * NG + grp;
+            if (row >= rows)
                 continue;
-            float f[E];
-            Elem<T>::unpack(raw[v], f);
-            if (e0 + E <= n) {
-                float wf[E], bf[E];
-                load_params<E>(w, e0, 1.0f, wf);
-                load_params<E>(b, e0, 0.0f, bf);
+            const float rs = 1.0f / sqrtf(fmaf(q[r], inv_n, eps));
+            if (g == 0) {
+                if (mean)
+                    mean[row] = s[r];
+                if (rstd)
+                    rstd[row] = rs;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e0 = (v * G + g) * E;
+                float f[E];
+                Elem<T>::unpack(raw[r][v], f);
 #pragma unroll
                 for (int j = 0; j < E; ++j)
-                    f[j] = fmaf((f[j] - mu) * r, wf[j], bf[j]);
-                store16(yr + e0, Elem<T>::pack(f));
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j)
-                    if (e0 + j < n)
-                        yr[e0 + j] = Elem<T>::put(fmaf((f[j] - mu) * r,
-                                                       w ? Elem<P>::get(w[e0 + j]) : 1.0f,
-                                                       b ? Elem<P>::get(b[e0 + j]) : 0.0f));
+                    f[j] = fmaf((f[j] - s[r]) * rs, wf[v][j], bf[v][j]);
+                store_chunk(y + row * ldy, e0, n, f);
             }
         }
     }
@@ -180,7 +200,8 @@ __global__ __launch_bounds__(1024) void ln_fwd_long_kernel(
     float eps, T* y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd)
 {
     constexpr int E = Elem<T>::kPerVec;
-    __shared__ float lds[16];
+    __shared__ float lds[32];
+    int turn = 0;
     const float inv_n = 1.0f / (float)n;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T* xr = x + row * ldx;
@@ -193,7 +214,7 @@ __global__ __launch_bounds__(1024) void ln_fwd_long_kernel(
             for (int j = 0; j < E; ++j)
                 s[0] += f[j];
         }
-        group_sum<1024>(s, lds);
+        group_sum<1024>(s, lds, turn);
         const float mu = s[0] * inv_n;
         float q[1] = {0.0f};
         for (int64_t e0 = (int64_t)threadIdx.x * E; e0 < n; e0 += 1024 * E) {
@@ -203,7 +224,7 @@ __global__ __launch_bounds__(1024) void ln_fwd_long_kernel(
             for (int j = 0; j < E; ++j)
                 q[0] += e0 + j < n ? (f[j] - mu) * (f[j] - mu) : 0.0f;
         }
-        group_sum<1024>(q, lds);
+        group_sum<1024>(q, lds, turn);
         const float r = 1.0f / sqrtf(fmaf(q[0], inv_n, eps));
         if (threadIdx.x == 0) {
             if (mean)
@@ -228,8 +249,25 @@ __global__ __launch_bounds__(1024) void ln_fwd_long_kernel(
 // Backward.
 // ---------------------------------------------------------------------------
 
-// R rows a group and batch: their loads are in flight together and their
-// sums share one exchange.
+// A thread's columns of a block's partial sums.
+template <int E, int G, int V>
+__device__ __forceinline__ void store_part(float* pw, int n, int g, const float (&w)[V][E],
+                                           const float (&b)[V][E])
+{
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const int e = (v * G + g) * E + j;
+            if (e < n) {
+                pw[e] = w[v][j];
+                pw[n + e] = b[v][j];
+            }
+        }
+}
+
+// R rows a group and batch: their sums share one exchange, and the next
+// batch's loads are in flight while this one is worked on.
 template <typename T, typename P, int G, int V, int R>
 __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
     const T* x, int64_t ldx, const T* dy, int64_t lddy, const float* __restrict__ mean,
@@ -238,22 +276,21 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
 {
     constexpr int E = Elem<T>::kPerVec;
     constexpr int NG = Group<G>::kGroups;
-    __shared__ float lds[G > 64 ? 2 * R * Group<G>::kWaves : 1];
+    __shared__ float lds[G > 64 ? 4 * R * Group<G>::kWaves : 1];
+    int turn = 0;
     const int g = threadIdx.x % G, grp = threadIdx.x / G;
     const float inv_n = 1.0f / (float)n;
     float wf[V][E], aw[V][E], ab[V][E];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+        load_params<E>(w, (v * G + g) * E, n, 1.0f, wf[v]);
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int e = (v * G + g) * E + j;
-            wf[v][j] = w && e < n ? Elem<P>::get(w[e]) : 1.0f;
+        for (int j = 0; j < E; ++j)
             aw[v][j] = ab[v][j] = 0.0f;
-        }
-    for (int64_t base = (int64_t)blockIdx.x * (NG * R); base < rows;
-         base += (int64_t)gridDim.x * (NG * R)) {
-        u32x4 rx[R][V], rd[R][V];
-        float mu[R], rs[R];
+    }
+    u32x4 rx[R][V], rd[R][V];
+    float mu[R], rs[R];
+    auto load = [&](int64_t base) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = base + r * NG + grp;
@@ -267,18 +304,36 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
                 rd[r][v] = load_chunk(dy + row * lddy, (v * G + g) * E, in ? n : 0);
             }
         }
-        float s[2 * R];
+    };
+    const int64_t step = (int64_t)gridDim.x * (NG * R);
+    int64_t base = (int64_t)blockIdx.x * (NG * R);
+    load(base);
+    for (; base < rows; base += step) {
+        float s[2 * R], m[R], t[R];
+        u32x4 cx[R][V], cd[R][V];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = mu[r];
+            t[r] = rs[r];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                cx[r][v] = rx[r][v];
+                cd[r][v] = rd[r][v];
+            }
+        }
+        if (base + step < rows)
+            load(base + step);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float fx[E], fd[E];
-                Elem<T>::unpack(rx[r][v], fx);
-                Elem<T>::unpack(rd[r][v], fd);
+                Elem<T>::unpack(cx[r][v], fx);
+                Elem<T>::unpack(cd[r][v], fd);
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    const float xh = (fx[j] - mu[r]) * rs[r];
+                    const float xh = (fx[j] - m[r]) * t[r];
                     const float gg = fd[j] * wf[v][j];
                     s1 += gg;
                     s2 = fmaf(gg, xh, s2);
@@ -289,7 +344,7 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
             s[2 * r] = s1;
             s[2 * r + 1] = s2;
         }
-        group_sum<G>(s, lds);
+        group_sum<G>(s, lds, turn);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = base + r * NG + grp;
@@ -298,18 +353,15 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
             const float m1 = s[2 * r] * inv_n, m2 = s[2 * r + 1] * inv_n;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int e0 = (v * G + g) * E;
-                if (e0 >= n)
-                    continue;
                 float fx[E], fd[E];
-                Elem<T>::unpack(rx[r][v], fx);
-                Elem<T>::unpack(rd[r][v], fd);
+                Elem<T>::unpack(cx[r][v], fx);
+                Elem<T>::unpack(cd[r][v], fd);
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    const float xh = (fx[j] - mu[r]) * rs[r];
-                    fd[j] = rs[r] * (fmaf(fd[j], wf[v][j], -m1) - xh * m2);
+                    const float xh = (fx[j] - m[r]) * t[r];
+                    fd[j] = t[r] * (fmaf(fd[j], wf[v][j], -m1) - xh * m2);
                 }
-                store_chunk(dx + row * lddx, e0, n, fd);
+                store_chunk(dx + row * lddx, (v * G + g) * E, n, fd);
             }
         }
     }
@@ -317,35 +369,27 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
         return;
     float* pw = part + (int64_t)blockIdx.x * 2 * n;
     if constexpr (NG > 1) {
-        // Columns of the block's groups, added in order of the group.
-        __shared__ float sums[2][256 * V * E];
+        // The groups' columns, added in order of the group.
+        constexpr int kSums = G * V * E;
+        __shared__ float sums[2][NG * kSums];
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const int e = (v * G + g) * E + j;
-                sums[0][grp * (G * V * E) + e] = aw[v][j];
-                sums[1][grp * (G * V * E) + e] = ab[v][j];
+                const int at = grp * kSums + (v * G + g) * E + j;
+                sums[0][at] = aw[v][j];
+                sums[1][at] = ab[v][j];
             }
         __syncthreads();
         for (int e = threadIdx.x; e < 2 * n; e += Group<G>::kThreads) {
             const int which = e >= n, col = e - which * n;
-            float s = 0.0f;
+            float t = 0.0f;
             for (int k = 0; k < NG; ++k)
-                s += sums[which][k * (G * V * E) + col];
-            pw[e] = s;
+                t += sums[which][k * kSums + col];
+            pw[e] = t;
         }
     } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int e = (v * G + g) * E + j;
-                if (e < n) {
-                    pw[e] = aw[v][j];
-                    pw[n + e] = ab[v][j];
-                }
-            }
+        store_part<E, G, V>(pw, n, g, aw, ab);
     }
 }
 
@@ -360,8 +404,15 @@ __global__ __launch_bounds__(1024) void ln_params_kernel(const float* __restrict
     const int64_t col = (int64_t)blockIdx.x * 32 + c;  // of 2 n: dweight's, then dbias's
     float s = 0.0f;
     if (col < 2 * (int64_t)n)
-        for (int p = k; p < parts; p += 32)
-            s += part[(int64_t)p * 2 * n + col];
+        for (int p = k; p < parts; p += 32 * 8) {
+            float f[8];  // eight loads in flight
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] = p + 32 * i < parts ? part[(int64_t)(p + 32 * i) * 2 * n + col] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s += f[i];
+        }
     lds[k][c] = s;
     __syncthreads();
     // Thread (c', k') takes column k', part c': a half wave a column.
@@ -385,7 +436,8 @@ __global__ __launch_bounds__(1024) void ln_bwd_long_kernel(
     int64_t lddx)
 {
     constexpr int E = Elem<T>::kPerVec;
-    __shared__ float lds[32];
+    __shared__ float lds[64];
+    int turn = 0;
     const float inv_n = 1.0f / (float)n;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T* xr = x + row * ldx;
@@ -405,7 +457,7 @@ __global__ __launch_bounds__(1024) void ln_bwd_long_kernel(
                 s[1] = fmaf(gg, (fx[j] - mu) * rs, s[1]);
             }
         }
-        group_sum<1024>(s, lds);
+        group_sum<1024>(s, lds, turn);
         const float m1 = s[0] * inv_n, m2 = s[1] * inv_n;
         for (int64_t e0 = (int64_t)threadIdx.x * E; e0 < n; e0 += 1024 * E) {
             float fx[E], fd[E];
@@ -476,19 +528,6 @@ struct LnArgs {
     hipStream_t stream;
 };
 
-template <typename T, typename P, int G, int V>
-static int fwd_launch(LnArgs<T, P>& a)
-{
-    constexpr int NG = Group<G>::kGroups;
-    int64_t grid = (a.rows + NG - 1) / NG;
-    if (grid > kMaxGrid)
-        grid = kMaxGrid;
-    void* args[] = {&a.x, &a.ldx, &a.w, &a.b, &a.rows, &a.n, &a.eps, &a.out, &a.ldo, &a.mean,
-                    &a.rstd};
-    return launch(reinterpret_cast<const void*>(&ln_fwd_kernel<T, P, G, V>), dim3((unsigned)grid),
-                  Group<G>::kThreads, args, a.stream);
-}
-
 // 16-byte vectors a row.
 template <typename T>
 static int64_t chunks(int n)
@@ -497,28 +536,43 @@ static int64_t chunks(int n)
     return ((int64_t)n + E - 1) / E;
 }
 
+template <typename T, typename P, int G, int V, int R>
+static int fwd_launch(LnArgs<T, P>& a)
+{
+    constexpr int NG = Group<G>::kGroups;
+    int64_t grid = (a.rows + NG * R - 1) / (NG * R);
+    if (grid > kFwdBlocks)
+        grid = kFwdBlocks;
+    void* args[] = {&a.x, &a.ldx, &a.w, &a.b, &a.rows, &a.n, &a.eps, &a.out, &a.ldo, &a.mean,
+                    &a.rstd};
+    return launch(reinterpret_cast<const void*>(&ln_fwd_kernel<T, P, G, V, R>), dim3((unsigned)grid),
+                  Group<G>::kThreads, args, a.stream);
+}
+
 template <typename T, typename P>
 static int fwd_run(LnArgs<T, P>& a)
 {
     const int64_t c = chunks<T>(a.n);
     if (c <= 4)
-        return fwd_launch<T, P, 4, 1>(a);
+        return fwd_launch<T, P, 4, 1, 2>(a);
+    if (c <= 8)
+        return fwd_launch<T, P, 8, 1, 2>(a);
     if (c <= 16)
-        return fwd_launch<T, P, 16, 1>(a);
+        return fwd_launch<T, P, 16, 1, 2>(a);
+    if (c <= 32)
+        return fwd_launch<T, P, 32, 1, 2>(a);
     if (c <= 64)
-        return fwd_launch<T, P, 64, 1>(a);
+        return fwd_launch<T, P, 64, 1, 2>(a);
     if (c <= 128)
-        return fwd_launch<T, P, 64, 2>(a);
+        return fwd_launch<T, P, 64, 2, 2>(a);
     if (c <= 256)
-        return fwd_launch<T, P, 256, 1>(a);
+        return fwd_launch<T, P, 256, 1, 2>(a);
     if (c <= 512)
-        return fwd_launch<T, P, 256, 2>(a);
+        return fwd_launch<T, P, 256, 2, 2>(a);
     if (c <= 1024)
-        return fwd_launch<T, P, 256, 4>(a);
+        return fwd_launch<T, P, 256, 4, 1>(a);
     if (c <= 2048)
-        return fwd_launch<T, P, 256, 8>(a);
-    if (c <= 4096)
-        return fwd_launch<T, P, 1024, 4>(a);
+        return fwd_launch<T, P, 1024, 2, 1>(a);
     int64_t grid = a.rows < kMaxGrid ? a.rows : kMaxGrid;
     void* args[] = {&a.x, &a.ldx, &a.w, &a.b, &a.rows, &a.n, &a.eps, &a.out, &a.ldo, &a.mean,
                     &a.rstd};
@@ -559,13 +613,19 @@ static int bwd_run(LnArgs<T, P>& a)
         return a.part ? params_launch<P>(a.part, 0, a.n, a.dweight, a.dbias, a.stream) : MESWISH_OK;
     const int64_t c = chunks<T>(a.n);
     if (c <= 4)
-        return bwd_launch<T, P, 4, 1, 1>(a);
+        return bwd_launch<T, P, 4, 1, 2>(a);
+    if (c <= 8)
+        return bwd_launch<T, P, 8, 1, 2>(a);
     if (c <= 16)
         return bwd_launch<T, P, 16, 1, 2>(a);
+    if (c <= 32)
+        return bwd_launch<T, P, 32, 1, 2>(a);
     if (c <= 64)
         return bwd_launch<T, P, 64, 1, 2>(a);
+    if (c <= 128)
+        return bwd_launch<T, P, 64, 2, 1>(a);
     if (c <= 256)
-        return bwd_launch<T, P, 256, 1, 4>(a);
+        return bwd_launch<T, P, 256, 1, 2>(a);
     if (c <= 512)
         return bwd_launch<T, P, 256, 2, 2>(a);
     if (c <= 1024)
