@@ -85,19 +85,52 @@ template <> struct Elem<bf16_t> {
     }
 };
 
+// The last elements of a row, from e0 (e0 < n < e0 + kPerVec) on, zeros behind
+// them: the row's last whole vector shifted down; a row shorter than a vector
+// element by element.  Few registers: this is inlined wherever rows are read.
+template <typename T>
+__device__ __forceinline__ u32x4 load_tail(const T* row, int e0, int n)
+{
+    constexpr int E = Elem<T>::kPerVec, kPerWord = 4 / (int)sizeof(T);
+    uint32_t a = 0, b = 0, c = 0, d = 0;
+    if (n >= E) {
+        const u32x4 v = load16(row + n - E);
+        a = v[0], b = v[1], c = v[2], d = v[3];
+        const int s = e0 - (n - E);  // elements to drop, 1 .. E - 1
+        if (s & 2 * kPerWord)
+            a = c, b = d, c = d = 0;
+        if (s & kPerWord)
+            a = b, b = c, c = d, d = 0;
+        if (kPerWord == 2 && s & 1) {
+            a = a >> 16 | b << 16;
+            b = b >> 16 | c << 16;
+            c = c >> 16 | d << 16;
+            d >>= 16;
+        }
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < n - e0; ++j) {
+            uint32_t bits = 0;
+            __builtin_memcpy(&bits, row + e0 + j, sizeof(T));
+            bits <<= j % kPerWord * 16;
+            const int w = j / kPerWord;
+            a |= w == 0 ? bits : 0;
+            b |= w == 1 ? bits : 0;
+            c |= w == 2 ? bits : 0;
+            d |= w == 3 ? bits : 0;
+        }
+    }
+    return u32x4{a, b, c, d};
+}
+
 // Elements e0 .. e0 + kPerVec - 1 of a row of n, as one packed vector; those
 // past the end are zero and are not read.
 template <typename T>
 __device__ __forceinline__ u32x4 load_chunk(const T* row, int e0, int n)
 {
-    constexpr int E = Elem<T>::kPerVec;
-    if (e0 + E <= n)
+    if (e0 + Elem<T>::kPerVec <= n)
         return load16(row + e0);
-    float f[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-        f[j] = e0 + j < n ? Elem<T>::get(row[e0 + j]) : 0.0f;
-    return Elem<T>::pack(f);
+    return e0 < n ? load_tail(row, e0, n) : u32x4{0, 0, 0, 0};
 }
 
 template <typename T>

@@ -232,38 +232,82 @@ struct Eight {
     }
 };
 
-// The unit on whole vectors of eight, without the activations' rare branches.
-// True in a lane that met one (or a row's last, partial vector): the wave is
-// then done again by gate_slow, to the same places.
+template <typename T>
+__device__ __forceinline__ void store_some8(T* p, const float* f, int n)  // the first n of eight
+{
+    if (n >= 8) {
+        Eight<T>::store(p, f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < n)
+                p[j] = Elem<T>::put(f[j]);
+    }
+}
+
+// What a wave needs of dh: eight units of row m + 16 i for each of its MT rows
+// and NT / 4 groups of 32 columns; all in flight together.
+template <typename T, int MT, int NT>
+struct Upstream {
+    Eight<T> v[MT * NT / 4];
+    __device__ __forceinline__ void load(const GemmArgs<T>& a, int64_t m0, int n0)
+    {
+        const int l = late_lane();
+        const int64_t row = m0 + l % 16;
+        const int n = n0 + 8 * (l / 16);
+        const T* p = a.dh + row * a.lddh;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int b = 0; b < NT / 4; ++b)
+                if (row + 16 * i < a.q.rows && n + 32 * b + 8 <= a.p.rows)
+                    v[i * (NT / 4) + b].load(p + 16 * i * a.lddh + n + 32 * b);
+        // A row's last, partial vector, apart (the code of the wide loads
+        // stays free of it).
+        if (a.p.rows % 8 && n0 + 8 * NT > a.p.rows)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int b = 0; b < NT / 4; ++b) {
+                    const int c = n + 32 * b;
+                    if (row + 16 * i < a.q.rows && c < a.p.rows && c + 8 > a.p.rows)
+#pragma unroll
+                        for (int k = 0; k < Eight<T>::V; ++k)
+                            v[i * (NT / 4) + b].v[k] = load_chunk(
+                                p + 16 * i * a.lddh, c + k * Elem<T>::kPerVec, a.p.rows);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+    }
+};
+
+// The unit on vectors of eight, without the activations' rare branches.  True
+// in a lane that met one: the wave is then done again by gate_slow, to the
+// same places.
 template <class Op, typename T, bool BWD, int MT, int NT>
 __device__ __forceinline__ bool gate_fast(const GemmArgs<T>& a, int64_t m0, int n0,
                                           const f32x4 (&acc)[MT][NT])
 {
     constexpr bool P = sizeof(T) == 4;
     const int l = late_lane();
-    const int64_t m = m0 + l % 16;
+    int64_t row = m0 + l % 16;
     const int n = n0 + 8 * (l / 16);
+    T* out0 = a.out[0] + row * a.ldo[0];
+    T* out1 = BWD ? a.out[1] + row * a.ldo[1] : nullptr;
+    T* outh = BWD && a.h ? a.h + row * a.ldh : nullptr;
+    // Loaded here and not once before the choice of activation: what that
+    // would let the compiler compute early (all of dh unpacked) does not fit
+    // the registers.
+    Upstream<T, MT, NT> d;
+    if constexpr (BWD)
+        d.load(a, m0, n0);
     float key = 0.0f;
-    bool partial = false;
-    constexpr int kVecs = MT * NT / 4;
-    Eight<T> d[BWD ? kVecs : 1];  // the wave's part of dh, in flight together
-    if constexpr (BWD) {
 #pragma unroll
-        for (int t = 0; t < kVecs; ++t) {
-            const int64_t row = m + 16 * (t / (NT / 4));
-            const int c = n + 32 * (t % (NT / 4));
-            if (row < a.q.rows && c + 8 <= a.p.rows)
-                d[t].load(a.dh + row * a.lddh + c);
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < kVecs; ++t) {
+    for (int t = 0; t < MT * NT / 4; ++t) {
         const int i = t / (NT / 4), b = t % (NT / 4) * 4;
-        const int64_t row = m + 16 * i;
         const int c = n + 8 * b;
         float o[8], du[8], h[8], up[8];
         if constexpr (BWD)
-            d[t].values(up);
+            d.v[t].values(up);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float g = acc[i][b + e / 4][e % 4], u = acc[i][b + 2 + e / 4][e % 4];
@@ -276,27 +320,36 @@ __device__ __forceinline__ bool gate_fast(const GemmArgs<T>& a, int64_t m0, int 
                 o[e] = f * u;
             }
         }
-        const bool in = c + 8 <= a.p.rows;
+        const int left = a.p.rows - c;
         if (row < a.q.rows && c < a.out_cols) {
-            if (!in && c < a.p.rows) {
-                partial = true;
-            } else if constexpr (BWD) {
+            if constexpr (BWD) {
                 // The workspace's rows are padded: zeros past the last unit.
+                if (left < 8)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    o[e] = in ? o[e] : 0.0f;
-                    du[e] = in ? du[e] : 0.0f;
-                }
-                Eight<T>::store(a.out[0] + row * a.ldo[0] + c, o);
-                Eight<T>::store(a.out[1] + row * a.ldo[1] + c, du);
-                if (a.h && in)
-                    Eight<T>::store(a.h + row * a.ldh + c, h);
+                    for (int e = 0; e < 8; ++e) {
+                        o[e] = e < left ? o[e] : 0.0f;
+                        du[e] = e < left ? du[e] : 0.0f;
+                    }
+                Eight<T>::store(out0 + c, o);
+                Eight<T>::store(out1 + c, du);
+                if (a.h)
+                    store_some8(outh + c, h, left);
             } else {
-                Eight<T>::store(a.out[0] + row * a.ldo[0] + c, o);
+                store_some8(out0 + c, o, left);
             }
         }
+        if (t % (NT / 4) == NT / 4 - 1) {
+            row += 16;
+            out0 += 16 * a.ldo[0];
+            if constexpr (BWD) {
+                out1 += 16 * a.ldo[1];
+                if (a.h)
+                    outh += 16 * a.ldh;
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // few results at a time
     }
-    return partial || key > Op::template rare_thr<P>();
+    return key > Op::template rare_thr<P>();
 }
 
 // One element of the unit's result, written where it belongs: exactly (with
@@ -357,7 +410,6 @@ template <class Op, typename T, bool BWD, int MT, int NT>
 __device__ __forceinline__ void gate_slow(const GemmArgs<T>& a, int64_t m0, int n0,
                                           const f32x4 (&acc)[MT][NT])
 {
-    constexpr bool P = sizeof(T) == 4;
     const int l = late_lane();
 #pragma unroll 1
     for (int t = 0; t < MT * NT / 2; ++t) {
