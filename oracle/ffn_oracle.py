@@ -82,8 +82,8 @@ def norm_forward(x, w, b, eps):
     n = X.shape[-1]
     mean, rstd = norm_stats(x, eps)
     c = X - mean[..., None]
-    W = torch.ones(n, dtype=torch.float64) if w is None else f64(w)
-    B = torch.zeros(n, dtype=torch.float64) if b is None else f64(b)
+    W = torch.ones(n, dtype=torch.float64, device=X.device) if w is None else f64(w)
+    B = torch.zeros(n, dtype=torch.float64, device=X.device) if b is None else f64(b)
     y = c * rstd[..., None] * W + B
     d = sum_depth(n)
     emean = (d + 2) * U * X.abs().sum(-1) / n
@@ -103,7 +103,7 @@ def norm_backward(x, dy, mean, rstd, w):
     X, D = f64(x), f64(dy)
     n = X.shape[-1]
     mu, r = f64(mean)[..., None], f64(rstd)[..., None]
-    W = torch.ones(n, dtype=torch.float64) if w is None else f64(w)
+    W = torch.ones(n, dtype=torch.float64, device=X.device) if w is None else f64(w)
     xh = (X - mu) * r
     g = D * W
     m1 = g.sum(-1, keepdim=True) / n
