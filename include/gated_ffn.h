@@ -28,9 +28,11 @@
  *     to nearest even.
  *   - ld*: elements between the starts of consecutive rows, at least the
  *     row's length and at most GATED_FFN_MAX_LD; rows are contiguous.
- *     Element alignment is required.  Matrices whose rows all start on
- *     16-byte boundaries (pointers, and ld a multiple of 16 bytes) take the
- *     faster loads.
+ *     Element alignment is required.  Where a row of x, wg or wu does not
+ *     start on a 16-byte boundary (pointers, ld a multiple of 16 bytes, the
+ *     same ld for wg and wu), or dim is not a multiple of 16 bytes, all three
+ *     are first copied to padded rows in the workspace (not for the forward
+ *     of at most 32 tokens, which takes any rows).
  *   - act, param: as meswish_act_fwd.
  *   - Results are deterministic: sums have a fixed order, no atomics.
  *   - Limits: tokens < 2^30; dim, hidden <= GATED_FFN_MAX_LD.
@@ -53,12 +55,14 @@ extern "C" {
 
 /* Bytes of workspace gated_ffn_fwd (backward == 0) or gated_ffn_bwd
  * (backward != 0) needs; 0 where it needs none or the sizes are out of
- * range. */
+ * range.  aligned: whether the rows of x, wg and wu are, as above (0 gives a
+ * size that serves any rows; a dim that is not a multiple of 16 bytes counts
+ * as 0). */
 size_t gated_ffn_workspace_bytes(size_t tokens, size_t dim, size_t hidden, int dtype,
-                                 int backward);
+                                 int backward, int aligned);
 
 /* h [tokens, hidden] from x, wg, wu.  workspace: 16-byte aligned, at least
- * gated_ffn_workspace_bytes(..., 0) bytes (NULL where that is 0). */
+ * gated_ffn_workspace_bytes(..., 0, aligned) bytes (NULL where that is 0). */
 int gated_ffn_fwd(int act, float param, const void *x, size_t ldx, const void *wg, size_t ldwg,
                   const void *wu, size_t ldwu, size_t tokens, size_t dim, size_t hidden, void *h,
                   size_t ldh, void *workspace, size_t workspace_bytes, int dtype, void *stream);
@@ -68,8 +72,8 @@ int gated_ffn_fwd(int act, float param, const void *x, size_t ldx, const void *w
  * and dwu together: what is NULL is not computed.  h: NULL, or [tokens,
  * hidden], where the forward's result is written again (for the gradient
  * of the projection that follows, which then need not keep it either).
- * workspace: 16-byte aligned, at least gated_ffn_workspace_bytes(..., 1)
- * bytes. */
+ * workspace: 16-byte aligned, at least gated_ffn_workspace_bytes(..., 1,
+ * aligned) bytes. */
 int gated_ffn_bwd(int act, float param, const void *x, size_t ldx, const void *wg, size_t ldwg,
                   const void *wu, size_t ldwu, const void *dh, size_t lddh, size_t tokens,
                   size_t dim, size_t hidden, void *dx, size_t lddx, void *dwg, size_t lddwg,

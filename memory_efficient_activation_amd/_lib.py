@@ -110,7 +110,7 @@ def _block_signatures() -> dict:
         "layer_norm_workspace_bytes": ([sz, sz], sz),
         "layer_norm_bwd": ([vp, sz, vp, sz, vp, vp, vp, sz, sz, vp, sz, vp, vp, vp, sz, i, i, vp],
                            i),
-        "gated_ffn_workspace_bytes": ([sz, sz, sz, i, i], sz),
+        "gated_ffn_workspace_bytes": ([sz, sz, sz, i, i, i], sz),
         "gated_ffn_fwd": ([i, f, vp, sz, vp, sz, vp, sz, sz, sz, sz, vp, sz, vp, sz, i, vp], i),
         "gated_ffn_bwd": ([i, f, vp, sz, vp, sz, vp, sz, vp, sz, sz, sz, sz, vp, sz, vp, sz, vp,
                            sz, vp, sz, vp, sz, i, vp], i),

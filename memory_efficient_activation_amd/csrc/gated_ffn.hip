@@ -507,153 +507,6 @@ __device__ __forceinline__ void part_of_sum(int splits, int& first, int& total)
 }
 
 // ---------------------------------------------------------------------------
-// Products for any alignment and size: 128 x 128 tiles, four waves of 64 x 64,
-// k in steps of 64 bytes; the next step's operands are loaded into registers
-// (16 bytes at element alignment, zeros past every edge) while the current
-// one is multiplied.
-// ---------------------------------------------------------------------------
-constexpr int kAnyTile = 128;
-
-// A tile of 128 rows (k contiguous: 64 bytes of k a row, 80 apart in LDS) or
-// of 64 bytes' worth of k rows (n contiguous: 128 values a row, padded by 32
-// bytes): both strides spread a wave's reads over all banks.
-template <typename T, bool KC, bool PAIR>
-struct AnyTile {
-    static constexpr int E = Elem<T>::kPerVec;
-    static constexpr int kK = 64 / sizeof(T);
-    static constexpr int kStride = KC ? 80 : kAnyTile * (int)sizeof(T) + 32;
-    static constexpr int kBytes = KC ? kAnyTile * kStride : kK * kStride;
-    static constexpr int kChunks = kAnyTile * 64 / 16 / 256;  // a thread's
-
-    // Chunk i of this thread: its row of the tile and its first element in it.
-    __device__ static int row(int i)
-    {
-        const int c = threadIdx.x + i * 256;
-        return KC ? c / 4 : c / (kAnyTile / E);
-    }
-    __device__ static int col(int i)
-    {
-        const int c = threadIdx.x + i * 256;
-        return KC ? c % 4 * E : c % (kAnyTile / E) * E;
-    }
-    __device__ static typename Step<T>::Frag frag(const char* lds, int row0)
-    {
-        const int l = threadIdx.x % 64;
-        if constexpr (KC) {
-            return *reinterpret_cast<const typename Step<T>::Frag*>(
-                lds + frag_row<PAIR>(row0) * kStride + l / 16 * 16);
-        } else if constexpr (sizeof(T) == 2) {
-            const char* p = lds + (8 * (l / 16) + l % 16 / 4) * kStride + (row0 + 4 * (l % 4)) * 2;
-            return join(lds_transpose(p), lds_transpose(p + 4 * kStride));
-        } else {
-            const char* p = lds + 4 * (l / 16) * kStride + (row0 + l % 16) * 4;
-            f32x4 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = *reinterpret_cast<const float*>(p + j * kStride);
-            return v;
-        }
-    }
-};
-
-template <typename T, int MODE, bool BWD, bool PARTS>
-__global__ __launch_bounds__(256) void gemm_any_kernel(const GemmArgs<T> a)
-{
-    constexpr bool PK = MODE == kUp, QK = MODE != kDw;
-    using PT = AnyTile<T, PK, PK>;
-    using QT = AnyTile<T, QK, false>;
-    constexpr int kK = PT::kK;
-    constexpr int kBytes = PT::kBytes + QT::kBytes;
-    __shared__ __attribute__((aligned(16))) char lds[kBytes];
-    char* const lp = lds;
-    char* const lq = lds + PT::kBytes;
-
-    int tm, tn, plane = 0;
-    if constexpr (MODE == kDw) {
-        // The tiles of dWg, then those of dWu.
-        tile_of_block(blockIdx.x, 2 * a.tiles_m, a.tiles_n, tm, tn);
-        plane = tm >= a.tiles_m;
-        tm -= plane * a.tiles_m;
-    } else {
-        tile_of_block(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
-    }
-    const int64_t m0 = (int64_t)tm * kAnyTile;
-    const int n0 = tn * (MODE == kUp ? kAnyTile / 2 : kAnyTile);
-    const int steps = (a.k + kK - 1) / kK;
-    int first = 0, total = MODE == kDx ? 2 * steps : steps;
-    if constexpr (PARTS)
-        part_of_sum(a.splits, first, total);
-
-    u32x4 rp[PT::kChunks], rq[QT::kChunks];
-    const u32x4 zero = {0, 0, 0, 0};
-    auto load = [&](int s) {
-        const int seg = MODE == kDx && s >= steps;
-        const int k0 = (s - seg * steps) * kK;
-#pragma unroll
-        for (int i = 0; i < PT::kChunks; ++i) {
-            const int r = PT::row(i), c = PT::col(i);
-            if constexpr (MODE == kUp) {
-                const int which = r / 32 % 2, n = n0 + r / 64 * 32 + r % 32;
-                rp[i] = n < a.p.rows
-                            ? load_chunk(a.p.base[which] + (int64_t)n * a.p.ld[which], k0 + c, a.k)
-                            : zero;
-            } else {
-                rp[i] = k0 + r < a.k ? load_chunk(a.p.base[seg] + (int64_t)(k0 + r) * a.p.ld[seg],
-                                                  n0 + c, a.p.rows)
-                                     : zero;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < QT::kChunks; ++i) {
-            const int r = QT::row(i), c = QT::col(i);
-            if constexpr (QK)
-                rq[i] = m0 + r < a.q.rows
-                            ? load_chunk(a.q.base[seg] + (m0 + r) * a.q.ld[seg], k0 + c, a.k)
-                            : zero;
-            else
-                rq[i] = k0 + r < a.k
-                            ? load_chunk(a.q.base[plane] + (int64_t)(k0 + r) * a.q.ld[plane],
-                                         (int)m0 + c, a.q.rows)
-                            : zero;
-        }
-    };
-
-    const int wave = threadIdx.x / 64, wm = wave / 2 * 64, wn = wave % 2 * 64;
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[i][j] = f32x4{};
-    if (first < total)
-        load(first);
-    for (int s = first; s < total; ++s) {
-        __syncthreads();  // the previous step has been read
-#pragma unroll
-        for (int i = 0; i < PT::kChunks; ++i)
-            *reinterpret_cast<u32x4*>(lp + PT::row(i) * PT::kStride + PT::col(i) * sizeof(T)) = rp[i];
-#pragma unroll
-        for (int i = 0; i < QT::kChunks; ++i)
-            *reinterpret_cast<u32x4*>(lq + QT::row(i) * QT::kStride + QT::col(i) * sizeof(T)) = rq[i];
-        __syncthreads();
-        if (s + 1 < total)
-            load(s + 1);
-        typename Step<T>::Frag fp[4], fq[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            fp[i] = PT::frag(lp, wn + 16 * i);
-            fq[i] = QT::frag(lq, wm + 16 * i);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = Step<T>::mma(fp[j], fq[i], acc[i][j]);
-    }
-    epilogue<T, MODE, BWD, PARTS>(a, m0 + wm, tn * kAnyTile + wn, plane, acc);
-}
-
-// ---------------------------------------------------------------------------
 // Products of matrices whose rows start on 16-byte boundaries.  WM x WN waves
 // of (32 MT) x 64 results each; k in steps of 128 bytes.  Operands go from
 // memory to LDS directly (buffer loads with the LDS bit, 16 bytes a lane),
@@ -1145,6 +998,45 @@ __global__ __launch_bounds__(NW * 64) void few_tokens_kernel(const GemmArgs<T> a
 }
 
 // ---------------------------------------------------------------------------
+// x, Wg and Wu in rows that start on 128-byte boundaries, zeros behind them:
+// for the products above where the caller's rows do not start on 16-byte
+// ones.  Measured against products that took rows at any alignment through
+// registers (128 x 128 tiles): bf16 4096 x 2047 -> 8191 forward 789 us to 296,
+// backward 2536 to 798; at 200 x 257 -> 131 the copy's launch costs 2 us of 16
+// forward and the backward still gains, 47 to 31.
+// ---------------------------------------------------------------------------
+template <typename T>
+struct PackArgs {
+    const T* from[3];
+    int64_t ld[3], rows[3];
+    T* to;
+    int cols, ld_to;
+    int row_bits;  // 2^row_bits threads a row
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(const PackArgs<T> a)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    const int64_t row = ((int64_t)blockIdx.x << (8 - a.row_bits)) + (threadIdx.x >> a.row_bits);
+    if (row >= a.rows[0] + a.rows[1] + a.rows[2])
+        return;
+    int64_t r = row, ld = a.ld[0];
+    const T* from = a.from[0];
+    if (r >= a.rows[0]) {
+        r -= a.rows[0];
+        const bool third = r >= a.rows[1];
+        r -= third ? a.rows[1] : 0;
+        from = third ? a.from[2] : a.from[1];
+        ld = third ? a.ld[2] : a.ld[1];
+    }
+    from += r * ld;
+    T* to = a.to + row * a.ld_to;
+    for (int c = (threadIdx.x & ((1 << a.row_bits) - 1)) * E; c < a.ld_to; c += E << a.row_bits)
+        store16(to + c, load_chunk(from, c, a.cols));
+}
+
+// ---------------------------------------------------------------------------
 // The parts of a split sum, added in order.
 // ---------------------------------------------------------------------------
 
@@ -1271,8 +1163,7 @@ struct Plan {
 // again at some 4 TB/s, by one more launch (3 us).  Measured, bf16, one
 // unsplit tile shape against the other and splits of 1 to 16 on both sides
 // of each choice: see the figures beside gemm_run.
-static Plan make_plan(int64_t rows, int64_t cols, int64_t k, int planes, int sums, size_t es,
-                      bool aligned)
+static Plan make_plan(int64_t rows, int64_t cols, int64_t k, int planes, int sums, size_t es)
 {
     const int64_t steps = (k + 128 / (int64_t)es - 1) / (128 / (int64_t)es) * sums;
     const double work = es == 2 ? 0.4 : 1.75, big_step = es == 2 ? 1.2 : 7.0;
@@ -1292,7 +1183,7 @@ static Plan make_plan(int64_t rows, int64_t cols, int64_t k, int planes, int sum
             best.splits = s;
         }
     }
-    if (aligned && (double)((bigs + kCus - 1) / kCus) * big_step * (double)steps < least)
+    if ((double)((bigs + kCus - 1) / kCus) * big_step * (double)steps < least)
         best = Plan{true, 1};
     return best;
 }
@@ -1305,17 +1196,9 @@ static int64_t part_ld(int mode, int64_t cols)
 
 static size_t part_bytes(int mode, int64_t rows, int64_t cols, int64_t k, size_t es)
 {
-    size_t most = 0;
     const int planes = mode == kDw ? 2 : 1;
-    for (int aligned = 0; aligned < 2; ++aligned) {
-        const Plan p = make_plan(rows, mode == kUp ? 2 * cols : cols, k, planes,
-                                 mode == kDx ? 2 : 1, es, aligned != 0);
-        const size_t n = p.splits > 1
-                             ? (size_t)p.splits * planes * rows * part_ld(mode, cols) * sizeof(float)
-                             : 0;
-        most = n > most ? n : most;
-    }
-    return most;
+    const Plan p = make_plan(rows, mode == kUp ? 2 * cols : cols, k, planes, mode == kDx ? 2 : 1, es);
+    return p.splits > 1 ? (size_t)p.splits * planes * rows * part_ld(mode, cols) * sizeof(float) : 0;
 }
 
 // Most tokens of the kernel that reads the weights once.
@@ -1360,22 +1243,6 @@ static int gemm_launch(GemmArgs<T>& a, const void* fn, int bm, int bn, int block
                            stream);
 }
 
-// Every row of the operands starts on a 16-byte boundary and the loads' 16
-// bytes lie whole in or out of it.
-template <typename T, int MODE>
-static bool aligned_rows(const GemmArgs<T>& a)
-{
-    constexpr int64_t E = Elem<T>::kPerVec;
-    if ((MODE == kUp ? a.k : a.p.rows) % E)
-        return false;
-    for (int i = 0; i < 2; ++i)
-        if (!aligned(a.p.base[i], 16) || !aligned(a.q.base[i], 16) || a.p.ld[i] % E ||
-            a.q.ld[i] % E)
-            return false;
-    // One offset serves both matrices of a sum.
-    return MODE != kDx || (a.p.ld[0] == a.p.ld[1] && a.q.ld[0] == a.q.ld[1]);
-}
-
 template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, bool PARTS>
 static int gemm_fast(GemmArgs<T>& a, hipStream_t stream)
 {
@@ -1396,9 +1263,10 @@ static int few_tokens(GemmArgs<T>& a, hipStream_t stream)
                   dim3((unsigned)((a.out_cols + 16 * PT - 1) / (16 * PT))), 512, args, stream);
 }
 
-// part: memory for the parts of a split sum.
+// part: memory for the parts of a split sum; k: the length that the plan (and
+// the size of that memory) goes by.
 template <typename T, int MODE, bool BWD>
-static int gemm_run(GemmArgs<T>& a, float* part, hipStream_t stream)
+static int gemm_run(GemmArgs<T>& a, int64_t k, float* part, hipStream_t stream)
 {
     a.splits = 1;
     if (a.q.rows == 0 || a.out_cols == 0)
@@ -1408,102 +1276,185 @@ static int gemm_run(GemmArgs<T>& a, float* part, hipStream_t stream)
             return a.q.rows <= 16 ? few_tokens<T, BWD, 1, 1>(a, stream)
                                   : few_tokens<T, BWD, 2, 2>(a, stream);
     }
-    const bool fast = aligned_rows<T, MODE>(a);
     // kUp's result is as wide as the workspace's rows; the plan goes by the
     // hidden units.
     const int64_t cols = MODE == kUp ? a.p.rows : a.out_cols;
-    const Plan p = make_plan(a.q.rows, MODE == kUp ? 2 * cols : cols, a.k, MODE == kDw ? 2 : 1,
-                             MODE == kDx ? 2 : 1, sizeof(T), fast);
+    const Plan p = make_plan(a.q.rows, MODE == kUp ? 2 * cols : cols, k, MODE == kDw ? 2 : 1,
+                             MODE == kDx ? 2 : 1, sizeof(T));
     a.splits = p.splits;
     a.part = part;
     a.part_ld = (int)part_ld(MODE, cols);
     if (p.splits > 1)
-        return fast ? gemm_fast<T, MODE, BWD, 2, 2, 4, 4, true>(a, stream)
-                    : gemm_launch<T, MODE, BWD>(
-                          a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, false, true>),
-                          kAnyTile, kAnyTile, 256, 0, stream);
-    if (!fast)
-        return gemm_launch<T, MODE, BWD>(
-            a, reinterpret_cast<const void*>(&gemm_any_kernel<T, MODE, BWD, false>), kAnyTile,
-            kAnyTile, 256, 0, stream);
+        return gemm_fast<T, MODE, BWD, 2, 2, 4, 4, true>(a, stream);
     return p.big ? gemm_fast<T, MODE, BWD, 2, 4, 8, 4, false>(a, stream)
                  : gemm_fast<T, MODE, BWD, 2, 2, 4, 4, false>(a, stream);
 }
 
 template <typename T>
-static Operand<T> operand(const void* a, size_t lda, const void* b, size_t ldb, size_t rows)
+static Operand<T> operand(const void* a, int64_t lda, const void* b, int64_t ldb, size_t rows)
 {
-    return Operand<T>{{static_cast<const T*>(a), static_cast<const T*>(b)},
-                      {(int64_t)lda, (int64_t)ldb},
-                      (int)rows};
+    return Operand<T>{{static_cast<const T*>(a), static_cast<const T*>(b)}, {lda, ldb}, (int)rows};
 }
 
-template <typename T>
-static int fwd(int act, float param, const void* x, size_t ldx, const void* wg, size_t ldwg,
-               const void* wu, size_t ldwu, size_t tokens, size_t dim, size_t hidden, void* h,
-               size_t ldh, void* workspace, hipStream_t stream)
+// Every row of x, wg and wu starts on a 16-byte boundary and is whole vectors
+// long, and one row distance serves both weights.
+static bool aligned_rows(const void* x, size_t ldx, const void* wg, size_t ldwg, const void* wu,
+                         size_t ldwu, size_t dim, size_t es)
 {
-    GemmArgs<T> a{};
-    a.p = operand<T>(wg, ldwg, wu, ldwu, hidden);
-    a.q = operand<T>(x, ldx, x, ldx, tokens);
-    a.k = (int)dim;
-    a.out[0] = static_cast<T*>(h);
-    a.ldo[0] = (int64_t)ldh;
-    a.out_cols = (int)hidden;
-    a.act = act;
-    a.coef = make_coef(act, param);
-    return gemm_run<T, kUp, false>(a, static_cast<float*>(workspace), stream);
+    return dim * es % 16 == 0 && aligned(x, 16) && aligned(wg, 16) && aligned(wu, 16) &&
+           ldx * es % 16 == 0 && ldwg * es % 16 == 0 && ldwg == ldwu;
 }
 
-template <typename T>
-static int bwd(int act, float param, const void* x, size_t ldx, const void* wg, size_t ldwg,
-               const void* wu, size_t ldwu, const void* dh, size_t lddh, size_t tokens, size_t dim,
-               size_t hidden, void* dx, size_t lddx, void* dwg, size_t lddwg, void* dwu,
-               size_t lddwu, void* h, size_t ldh, void* workspace, hipStream_t stream)
+static size_t packed_ld(size_t dim, size_t es) { return (dim * es + 127) / 128 * 128 / es; }
+
+// The workspace: dg and du (backward), the packed operands (where rows are not
+// aligned), the parts of one split sum at a time.  Each is whole 128-byte lines
+// long.
+struct Space {
+    size_t grads, packed, part;
+    size_t bytes() const { return grads + packed + part; }
+};
+
+static size_t lines(size_t bytes) { return (bytes + 127) / 128 * 128; }
+
+static Space space(size_t tokens, size_t dim, size_t hidden, size_t es, bool backward, bool aligned)
 {
-    const size_t fp = padded(hidden);
-    T* dg = static_cast<T*>(workspace);
-    T* du = dg + tokens * fp;
-    float* part = reinterpret_cast<float*>(du + tokens * fp);
+    const int64_t m = (int64_t)tokens, d = (int64_t)dim, f = (int64_t)hidden;
+    const bool few = tokens <= (size_t)kFewTokens;
+    Space s{};
+    // The kernel for few tokens takes any rows.
+    if (!aligned && (backward || !few))
+        s.packed = (tokens + 2 * hidden) * packed_ld(dim, es) * es;
+    s.part = few ? 0 : part_bytes(kUp, m, f, d, es);
+    if (backward) {
+        s.grads = lines(2 * tokens * padded(hidden) * es);
+        const size_t dx = part_bytes(kDx, m, d, f, es), dw = part_bytes(kDw, f, d, m, es);
+        s.part = s.part > dx ? s.part : dx;
+        s.part = s.part > dw ? s.part : dw;
+    }
+    return s;
+}
+
+// x, wg and wu as the products take them: as they are, or packed.
+template <typename T>
+struct Inputs {
+    const T *x, *wg, *wu;
+    int64_t ldx, ldg, ldu;
+    int dim;  // in whole vectors, zeros behind the caller's (packed)
+
+    int pack(T* to, size_t tokens, size_t hidden, hipStream_t stream)
+    {
+        constexpr int E = Elem<T>::kPerVec;
+        const int64_t ld = (int64_t)packed_ld((size_t)dim, sizeof(T));
+        PackArgs<T> a{{x, wg, wu},
+                      {ldx, ldg, ldu},
+                      {(int64_t)tokens, (int64_t)hidden, (int64_t)hidden},
+                      to,
+                      dim,
+                      (int)ld,
+                      0};
+        while (a.row_bits < 8 && (E << a.row_bits) < ld)
+            ++a.row_bits;
+        x = to;
+        wg = x + tokens * ld;
+        wu = wg + hidden * ld;
+        ldx = ldg = ldu = ld;
+        dim = (dim + E - 1) / E * E;
+        const int64_t rows = (int64_t)(tokens + 2 * hidden);
+        if (rows == 0 || ld == 0)
+            return MESWISH_OK;
+        void* args[] = {&a};
+        return launch_over(reinterpret_cast<const void*>(&pack_kernel<T>), rows << a.row_bits, args,
+                           stream);
+    }
+};
+
+// What a call was given, checked.
+struct Call {
+    int act;
+    float param;
+    const void *x, *wg, *wu, *dh;
+    int64_t ldx, ldg, ldu, lddh;
+    size_t tokens, dim, hidden;
+    void *dx, *dwg, *dwu, *h;
+    int64_t lddx, lddwg, lddwu, ldh;
+    char* workspace;
+    Space space;
+    hipStream_t stream;
+};
+
+template <typename T, bool BWD>
+static int run(const Call& c)
+{
+    Inputs<T> in{static_cast<const T*>(c.x),
+                 static_cast<const T*>(c.wg),
+                 static_cast<const T*>(c.wu),
+                 c.ldx,
+                 c.ldg,
+                 c.ldu,
+                 (int)c.dim};
+    Inputs<T> as_given = in;
+    float* part = reinterpret_cast<float*>(c.workspace + c.space.grads + c.space.packed);
+    int rc = MESWISH_OK;
+    if (c.space.packed)
+        rc = in.pack(reinterpret_cast<T*>(c.workspace + c.space.grads), c.tokens, c.hidden, c.stream);
+    if (rc != MESWISH_OK)
+        return rc;
+    const Inputs<T>& up = c.tokens <= (size_t)kFewTokens ? as_given : in;
+    const int64_t fp = (int64_t)padded(c.hidden);
+    T* dg = reinterpret_cast<T*>(c.workspace);
+    T* du = dg + (int64_t)c.tokens * fp;
     GemmArgs<T> a{};
-    a.p = operand<T>(wg, ldwg, wu, ldwu, hidden);
-    a.q = operand<T>(x, ldx, x, ldx, tokens);
-    a.k = (int)dim;
+    a.p = operand<T>(up.wg, up.ldg, up.wu, up.ldu, c.hidden);
+    a.q = operand<T>(up.x, up.ldx, up.x, up.ldx, c.tokens);
+    a.k = up.dim;
+    a.act = c.act;
+    a.coef = make_coef(c.act, c.param);
+    if constexpr (!BWD) {
+        a.out[0] = static_cast<T*>(c.h);
+        a.ldo[0] = c.ldh;
+        a.out_cols = (int)c.hidden;
+        return gemm_run<T, kUp, false>(a, (int64_t)c.dim, part, c.stream);
+    }
     a.out[0] = dg;
     a.out[1] = du;
-    a.ldo[0] = a.ldo[1] = (int64_t)fp;
+    a.ldo[0] = a.ldo[1] = fp;
     a.out_cols = (int)fp;
-    a.dh = static_cast<const T*>(dh);
-    a.lddh = (int64_t)lddh;
-    a.h = static_cast<T*>(h);
-    a.ldh = (int64_t)ldh;
-    a.act = act;
-    a.coef = make_coef(act, param);
-    int rc = gemm_run<T, kUp, true>(a, part, stream);
-    if (rc == MESWISH_OK && dx) {
+    a.dh = static_cast<const T*>(c.dh);
+    a.lddh = c.lddh;
+    a.h = static_cast<T*>(c.h);
+    a.ldh = c.ldh;
+    rc = gemm_run<T, kUp, true>(a, (int64_t)c.dim, part, c.stream);
+    if (rc == MESWISH_OK && c.dx) {
         GemmArgs<T> b{};
-        b.p = operand<T>(wg, ldwg, wu, ldwu, dim);
-        b.q = operand<T>(dg, fp, du, fp, tokens);
-        b.k = (int)hidden;
-        b.out[0] = static_cast<T*>(dx);
-        b.ldo[0] = (int64_t)lddx;
-        b.out_cols = (int)dim;
-        rc = gemm_run<T, kDx, false>(b, part, stream);
+        b.p = operand<T>(in.wg, in.ldg, in.wu, in.ldu, (size_t)in.dim);
+        b.q = operand<T>(dg, fp, du, fp, c.tokens);
+        b.k = (int)c.hidden;
+        b.out[0] = static_cast<T*>(c.dx);
+        b.ldo[0] = c.lddx;
+        b.out_cols = (int)c.dim;
+        rc = gemm_run<T, kDx, false>(b, (int64_t)c.hidden, part, c.stream);
     }
-    if (rc == MESWISH_OK && dwg) {
+    if (rc == MESWISH_OK && c.dwg) {
         GemmArgs<T> b{};
-        b.p = operand<T>(x, ldx, x, ldx, dim);
-        b.q = operand<T>(dg, fp, du, fp, hidden);
-        b.k = (int)tokens;
+        b.p = operand<T>(in.x, in.ldx, in.x, in.ldx, (size_t)in.dim);
+        b.q = operand<T>(dg, fp, du, fp, c.hidden);
+        b.k = (int)c.tokens;
         b.q_cols = (int)fp;
-        b.out[0] = static_cast<T*>(dwg);
-        b.out[1] = static_cast<T*>(dwu);
-        b.ldo[0] = (int64_t)lddwg;
-        b.ldo[1] = (int64_t)lddwu;
-        b.out_cols = (int)dim;
-        rc = gemm_run<T, kDw, false>(b, part, stream);
+        b.out[0] = static_cast<T*>(c.dwg);
+        b.out[1] = static_cast<T*>(c.dwu);
+        b.ldo[0] = c.lddwg;
+        b.ldo[1] = c.lddwu;
+        b.out_cols = (int)c.dim;
+        rc = gemm_run<T, kDw, false>(b, (int64_t)c.tokens, part, c.stream);
     }
     return rc;
+}
+
+template <bool BWD>
+static int run_dtype(int dtype, const Call& c)
+{
+    return dtype == MESWISH_F32 ? run<float, BWD>(c) : run<bf16_t, BWD>(c);
 }
 
 // No output touches an input or another output.
@@ -1525,20 +1476,12 @@ static int apart(const Span* out, int nout, const Span* in, int nin)
 using namespace meblock;
 
 extern "C" size_t gated_ffn_workspace_bytes(size_t tokens, size_t dim, size_t hidden, int dtype,
-                                            int backward)
+                                            int backward, int aligned)
 {
     if (!dtype_ok(dtype) || !sizes_ok(tokens, dim, hidden))
         return 0;
     const size_t es = elem_size(dtype);
-    const int64_t m = (int64_t)tokens, d = (int64_t)dim, f = (int64_t)hidden;
-    size_t part = tokens <= (size_t)kFewTokens ? 0 : part_bytes(kUp, m, f, d, es);
-    if (!backward)
-        return part;
-    // dg and du, then the parts of one split sum at a time.
-    const size_t dx = part_bytes(kDx, m, d, f, es), dw = part_bytes(kDw, f, d, m, es);
-    part = part > dx ? part : dx;
-    part = part > dw ? part : dw;
-    return 2 * tokens * padded(hidden) * es + part;
+    return space(tokens, dim, hidden, es, backward != 0, aligned && dim * es % 16 == 0).bytes();
 }
 
 extern "C" int gated_ffn_fwd(int act, float param, const void* x, size_t ldx, const void* wg,
@@ -1552,21 +1495,26 @@ extern "C" int gated_ffn_fwd(int act, float param, const void* x, size_t ldx, co
     if (!matrix_ok(x, tokens, dim, ldx, es) || !matrix_ok(wg, hidden, dim, ldwg, es) ||
         !matrix_ok(wu, hidden, dim, ldwu, es) || !matrix_ok(h, tokens, hidden, ldh, es))
         return MESWISH_EINVAL;
-    const size_t need = gated_ffn_workspace_bytes(tokens, dim, hidden, dtype, 0);
+    const Space sp = space(tokens, dim, hidden, es, false,
+                           aligned_rows(x, ldx, wg, ldwg, wu, ldwu, dim, es));
+    const size_t need = sp.bytes();
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return MESWISH_EINVAL;
     const Span in[] = {span(x, tokens, dim, ldx, es), span(wg, hidden, dim, ldwg, es),
                        span(wu, hidden, dim, ldwu, es)};
     const Span out[] = {span(h, tokens, hidden, ldh, es), span(workspace, need ? 1 : 0, need, need, 1)};
     int rc = apart(out, 2, in, 3);
-    if (rc != MESWISH_OK)
+    if (rc != MESWISH_OK || tokens == 0 || hidden == 0)
         return rc;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    return dtype == MESWISH_F32
-               ? fwd<float>(act, param, x, ldx, wg, ldwg, wu, ldwu, tokens, dim, hidden, h, ldh, workspace,
-                            s)
-               : fwd<bf16_t>(act, param, x, ldx, wg, ldwg, wu, ldwu, tokens, dim, hidden, h, ldh, workspace,
-                             s);
+    Call c{};
+    c.act = act, c.param = param;
+    c.x = x, c.wg = wg, c.wu = wu, c.h = h;
+    c.ldx = (int64_t)ldx, c.ldg = (int64_t)ldwg, c.ldu = (int64_t)ldwu, c.ldh = (int64_t)ldh;
+    c.tokens = tokens, c.dim = dim, c.hidden = hidden;
+    c.workspace = static_cast<char*>(workspace);
+    c.space = sp;
+    c.stream = static_cast<hipStream_t>(stream);
+    return run_dtype<false>(dtype, c);
 }
 
 extern "C" int gated_ffn_bwd(int act, float param, const void* x, size_t ldx, const void* wg,
@@ -1585,7 +1533,9 @@ extern "C" int gated_ffn_bwd(int act, float param, const void* x, size_t ldx, co
         (dwg && (!matrix_ok(dwg, hidden, dim, lddwg, es) || !matrix_ok(dwu, hidden, dim, lddwu, es))) ||
         (h && !matrix_ok(h, tokens, hidden, ldh, es)))
         return MESWISH_EINVAL;
-    const size_t need = gated_ffn_workspace_bytes(tokens, dim, hidden, dtype, 1);
+    const Space sp = space(tokens, dim, hidden, es, true,
+                           aligned_rows(x, ldx, wg, ldwg, wu, ldwu, dim, es));
+    const size_t need = sp.bytes();
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return MESWISH_EINVAL;
     const Span in[] = {span(x, tokens, dim, ldx, es), span(wg, hidden, dim, ldwg, es),
@@ -1598,10 +1548,15 @@ extern "C" int gated_ffn_bwd(int act, float param, const void* x, size_t ldx, co
     int rc = apart(out, 5, in, 4);
     if (rc != MESWISH_OK)
         return rc;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    return dtype == MESWISH_F32
-               ? bwd<float>(act, param, x, ldx, wg, ldwg, wu, ldwu, dh, lddh, tokens, dim, hidden,
-                            dx, lddx, dwg, lddwg, dwu, lddwu, h, ldh, workspace, s)
-               : bwd<bf16_t>(act, param, x, ldx, wg, ldwg, wu, ldwu, dh, lddh, tokens, dim, hidden,
-                             dx, lddx, dwg, lddwg, dwu, lddwu, h, ldh, workspace, s);
+    Call c{};
+    c.act = act, c.param = param;
+    c.x = x, c.wg = wg, c.wu = wu, c.dh = dh;
+    c.ldx = (int64_t)ldx, c.ldg = (int64_t)ldwg, c.ldu = (int64_t)ldwu, c.lddh = (int64_t)lddh;
+    c.tokens = tokens, c.dim = dim, c.hidden = hidden;
+    c.dx = dx, c.dwg = dwg, c.dwu = dwu, c.h = h;
+    c.lddx = (int64_t)lddx, c.lddwg = (int64_t)lddwg, c.lddwu = (int64_t)lddwu, c.ldh = (int64_t)ldh;
+    c.workspace = static_cast<char*>(workspace);
+    c.space = sp;
+    c.stream = static_cast<hipStream_t>(stream);
+    return run_dtype<true>(dtype, c);
 }

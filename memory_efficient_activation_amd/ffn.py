@@ -63,8 +63,15 @@ def _tokens(x: torch.Tensor) -> int:
     return n
 
 
-def _workspace(tokens, dim, hidden, code, backward, device, shared):
-    nbytes = library().gated_ffn_workspace_bytes(tokens, dim, hidden, code, backward)
+def _aligned(x, ldx, wg, ldg, wu, ldu, dim) -> bool:
+    """Whether the rows of all three start on 16-byte boundaries."""
+    per = 16 // x.element_size()
+    return not ((x.data_ptr() | wg.data_ptr() | wu.data_ptr()) % 16 or (ldx | ldg | dim) % per
+                or ldg != ldu)
+
+
+def _workspace(tokens, dim, hidden, code, backward, aligned, device, shared):
+    nbytes = library().gated_ffn_workspace_bytes(tokens, dim, hidden, code, backward, aligned)
     if nbytes == 0:
         return None, 0
     ws = (shared or SharedBuffer()).workspace(nbytes, device)
@@ -93,7 +100,8 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, kin
             raise ValueError(f"out must be a {x.dtype} tensor of shape {shape} on {x.device}")
         h, ldh = _out_rows(out, out, "out")
     device = x.device
-    ws, nbytes = _workspace(tokens, dim, hidden, code, 0, device, shared)
+    ws, nbytes = _workspace(tokens, dim, hidden, code, 0,
+                            _aligned(x, ldx, wg, ldg, wu, ldu, dim), device, shared)
     launch("gated_ffn_fwd", f"gated_ffn_fwd({kind})", device, act, _param_value(kind, param),
            x.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu, tokens, dim, hidden,
            h.data_ptr(), ldh, _ptr(ws), nbytes, code)
@@ -125,7 +133,8 @@ def gated_ffn_bwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, dh:
         dwu = torch.empty((hidden, dim), dtype=x.dtype, device=x.device)
     h = torch.empty(dh.shape, dtype=x.dtype, device=x.device) if need_h else None
     device = x.device
-    ws, nbytes = _workspace(tokens, dim, hidden, code, 1, device, shared)
+    ws, nbytes = _workspace(tokens, dim, hidden, code, 1,
+                            _aligned(x, ldx, wg, ldg, wu, ldu, dim), device, shared)
     launch("gated_ffn_bwd", f"gated_ffn_bwd({kind})", device, act, _param_value(kind, param),
            x.data_ptr(), ldx, wg.data_ptr(), ldg, wu.data_ptr(), ldu, dh.data_ptr(), lddh, tokens,
            dim, hidden, _ptr(dx), dim, _ptr(dwg), dim, _ptr(dwu), dim, _ptr(h), hidden, _ptr(ws),

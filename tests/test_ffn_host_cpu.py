@@ -132,7 +132,7 @@ def ffn_bwd(lib, act=0, param=1.0, x=X, ldx=64, wg=W, ldwg=64, wu=B, ldwu=64, dh
             tokens=4, dim=64, hidden=32, dx=DX, lddx=64, dwg=DWG, lddwg=64, dwu=DWU, lddwu=64,
             h=H, ldh=32, ws=WS, wsb=None, dtype=1):
     if wsb is None:
-        wsb = lib.gated_ffn_workspace_bytes(tokens, dim, hidden, dtype, 1)
+        wsb = lib.gated_ffn_workspace_bytes(tokens, dim, hidden, dtype, 1, 1)
     return lib.gated_ffn_bwd(act, param, x, ldx, wg, ldwg, wu, ldwu, dh, lddh, tokens, dim, hidden,
                              dx, lddx, dwg, lddwg, dwu, lddwu, h, ldh, ws, wsb, dtype, None)
 
@@ -147,7 +147,7 @@ def test_unit_backward_refusals(lib):
     for name in ("lddh", "lddx", "lddwg", "lddwu", "ldh"):
         assert ffn_bwd(lib, **{name: 31}) == E, name
     assert ffn_bwd(lib, ws=WS + 8) == E
-    assert ffn_bwd(lib, wsb=lib.gated_ffn_workspace_bytes(4, 64, 32, 1, 1) - 1) == E
+    assert ffn_bwd(lib, wsb=lib.gated_ffn_workspace_bytes(4, 64, 32, 1, 1, 1) - 1) == E
     for name in ("dx", "dwg", "dwu", "h", "ws"):
         assert ffn_bwd(lib, **{name: X}) == A, name
         assert ffn_bwd(lib, **{name: DY}) == A, name
@@ -156,11 +156,24 @@ def test_unit_backward_refusals(lib):
 
 
 def test_workspace_sizes(lib):
+    size = lib.gated_ffn_workspace_bytes
     for dtype, es in ((0, 4), (1, 2)):
-        # dg and du at the least.
-        assert lib.gated_ffn_workspace_bytes(10, 64, 100, dtype, 1) >= 2 * 10 * 100 * es
-    assert lib.gated_ffn_workspace_bytes(1 << 30, 64, 64, 1, 1) == 0
-    assert lib.gated_ffn_workspace_bytes(4, 64, 64, 3, 1) == 0
+        # dg and du at the least; the padded copies of x, wg and wu beside them
+        # where rows are not aligned, or cannot be.
+        assert size(10, 64, 100, dtype, 1, 1) >= 2 * 10 * 100 * es
+        assert size(10, 64, 100, dtype, 1, 0) >= size(10, 64, 100, dtype, 1, 1) + 210 * 64 * es
+        assert size(10, 63, 100, dtype, 1, 1) == size(10, 63, 100, dtype, 1, 0)
+        assert size(10, 63, 100, dtype, 0, 0) == 0  # few tokens: any rows
+        assert size(100, 63, 100, dtype, 0, 0) >= 300 * 63 * es
+    assert size(1 << 30, 64, 64, 1, 1, 1) == 0
+    assert size(4, 64, 64, 3, 1, 1) == 0
+
+
+def test_unaligned_rows_need_the_larger_workspace(lib):
+    small = lib.gated_ffn_workspace_bytes(100, 64, 32, 1, 1, 1)
+    assert small < lib.gated_ffn_workspace_bytes(100, 64, 32, 1, 1, 0)
+    for bad in ({"x": X + 2}, {"ldx": 65}, {"wg": W + 4}, {"ldwg": 72}, {"wu": B + 8}):
+        assert ffn_bwd(lib, tokens=100, wsb=small, **bad) == _lib.EINVAL, bad
 
 
 def test_cpu_tensors_are_refused():
