@@ -8,7 +8,7 @@ import torch.nn.functional as F
 import memory_efficient_activation_amd as mea
 from memory_efficient_activation_amd import dense, ffn, norm
 from oracle import ffn_oracle as o
-from tests.gpu_util import say
+from gpu_util import say
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"

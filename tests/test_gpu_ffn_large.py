@@ -7,7 +7,7 @@ import torch
 
 from memory_efficient_activation_amd import dense, ffn, norm
 from oracle import ffn_oracle as o
-from tests.gpu_util import say
+from gpu_util import say
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
