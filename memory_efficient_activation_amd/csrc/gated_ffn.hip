@@ -508,10 +508,24 @@ __device__ __forceinline__ void part_of_sum(int splits, int& first, int& total)
 
 // ---------------------------------------------------------------------------
 // Products of matrices whose rows start on 16-byte boundaries.  WM x WN waves
-// of (32 MT) x 64 results each; k in steps of 128 bytes.  Operands go from
-// memory to LDS directly (buffer loads with the LDS bit, 16 bytes a lane),
-// two tiles of each operand in LDS: while one is multiplied the next one
-// arrives.
+// of (16 MT) x (16 NT) results each; k in steps of 128 bytes.  Operands go
+// from memory to LDS directly (buffer loads with the LDS bit, 16 bytes a
+// lane), two tiles of each operand in LDS: while one is multiplied the next
+// one arrives.
+//
+// What bounds it, and why this shape (bf16, 16384 x 4096 -> 16384: forward
+// 1400 TFLOP/s, recomputation 1290, dx 1310, dWg and dWu 1270; binary32 8192 x
+// 2048 -> 4096: 147 of the 157 its matrix instructions have).  The matrix
+// cores are busy 71 % of the cycles and the card lowers its clock (1.75 GHz)
+// under the load: on zeros, which cost little power, the forward reaches 1580.
+// Without the loads the loop alone would be at 2270, so the rest is the wait
+// for them.  Measured against it: 16 x 16 matrix instructions instead of 32 x
+// 32, forward 1304 to 1352; products, reads and loads in the order written
+// instead of the compiler's, 1228 to 1304; eight waves of 128 x 64 against
+// four of 128 x 128, 1272 and 1162; 64 bytes of k a step with four or five
+// tiles in LDS, 1210 (twice the barriers, half lines fetched twice); loads
+// spread over the next step, 1305 against 1346; lines of later steps touched
+// into the L2 beforehand, 1490 to 1650 on zeros but 1217 to 1185 on numbers.
 //
 // A load writes 1 KiB of LDS in lane order, so the layouts that avoid bank
 // conflicts are made by choosing which 16 bytes each lane fetches:
@@ -537,7 +551,7 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t offset, i32x4 
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(offset), "s"(rsrc)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 template <int N>
@@ -556,11 +570,12 @@ __device__ __forceinline__ i32x4 buffer(const void* p, uint32_t bytes)
     return r;
 }
 
-// A tile of ROWS values of m or n and KB bytes of k, filled by WAVES waves.
-template <typename T, bool KC, bool PAIR, int ROWS, int WAVES, int KB>
+constexpr int KB = 128;  // bytes of k a step
+
+// A tile of ROWS values of m or n and one step of k, filled by WAVES waves.
+template <typename T, bool KC, bool PAIR, int ROWS, int WAVES>
 struct FastTile {
     static constexpr int E = Elem<T>::kPerVec;
-    static_assert(KB == 128, "the layouts below");
     static constexpr int kK = KB / sizeof(T);
     static constexpr int kBytes = ROWS * KB;
     static constexpr int kRowBytes = KC ? KB : ROWS * (int)sizeof(T);
@@ -608,18 +623,16 @@ struct FastTile {
     }
 };
 
-template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, int KB, int NS, int SP,
-          bool PARTS>
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, bool PARTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmArgs<T> a)
 {
     constexpr bool PK = MODE == kUp, QK = MODE != kDw;
     constexpr int BM = WM * MT * 16, BN = WN * NT * 16, WAVES = WM * WN;
-    using PT = FastTile<T, PK, PK, BN, WAVES, KB>;
-    using QT = FastTile<T, QK, false, BM, WAVES, KB>;
+    using PT = FastTile<T, PK, PK, BN, WAVES>;
+    using QT = FastTile<T, QK, false, BM, WAVES>;
     constexpr int kK = PT::kK, E = Elem<T>::kPerVec, STEPS = KB / 64;
     constexpr int kStage = PT::kBytes + QT::kBytes;
-    constexpr int kLds = NS * kStage;
-    __shared__ __attribute__((aligned(1024))) char lds[kLds];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(MEBLOCK_LDS char*)lds;
 
     const int tiles = a.tiles_m * a.tiles_n * (MODE == kDw ? 2 : 1);
@@ -679,42 +692,37 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
 
     // Where the next step's loads start, in scalar registers: address, bytes
     // left of the sum from there (what lies past them reads as zero).
-    constexpr int kStepK = kK;
-    const char *curp, *curu, *curq;  // curu (kUp): Wu's, curp Wg's
+    const char *curp, *curq;
     int64_t incp, incq, leftp, leftq;
-    // Loads of one weight's 32 rows; a wave loads of one weight, or of both.
-    constexpr int kTurn = 32 * KB / 1024;
-    constexpr bool kBoth = MODE == kUp && PT::kLoads > kTurn;
-    static_assert(kBoth ? PT::kLoads % (2 * kTurn) == 0 : kTurn % PT::kLoads == 0 || MODE != kUp,
-                  "which weight a load is of depends on its number, or on the wave");
+    // (kUp) A wave loads 32 rows of P, all of one weight.
+    static_assert(MODE != kUp || PT::kLoads * 1024 == 32 * KB, "waves in turn");
     auto start = [&](int seg) {
         if constexpr (MODE == kUp) {
-            const bool up = !kBoth && wave * PT::kLoads / kTurn % 2;
+            const bool up = wave % 2;
             const T* w = up ? a.p.base[1] : a.p.base[0];
             const int64_t ld = up ? a.p.ld[1] : a.p.ld[0];
             curp = reinterpret_cast<const char*>(w + (int64_t)n0 * ld);
-            curu = reinterpret_cast<const char*>(a.p.base[1] + (int64_t)n0 * a.p.ld[1]);
-            incp = kStepK * (int64_t)sizeof(T);
+            incp = kK * (int64_t)sizeof(T);
             leftp = kBufferBytes;
         } else {
             const int64_t ld = a.p.ld[0];
             curp = reinterpret_cast<const char*>((seg ? a.p.base[1] : a.p.base[0]) + n0);
-            incp = kStepK * ld * (int64_t)sizeof(T);
+            incp = kK * ld * (int64_t)sizeof(T);
             leftp = ((int64_t)(a.k - 1) * ld + a.p.rows - n0) * (int64_t)sizeof(T);
         }
         if constexpr (QK) {
             curq = reinterpret_cast<const char*>((seg ? a.q.base[1] : a.q.base[0]) +
                                                  m0 * a.q.ld[0]);
-            incq = kStepK * (int64_t)sizeof(T);
+            incq = kK * (int64_t)sizeof(T);
             leftq = kBufferBytes;
         } else {
             const int64_t ld = a.q.ld[0];
             curq = reinterpret_cast<const char*>((plane ? a.q.base[1] : a.q.base[0]) + m0);
-            incq = kStepK * ld * (int64_t)sizeof(T);
+            incq = kK * ld * (int64_t)sizeof(T);
             leftq = ((int64_t)(a.k - 1) * ld + a.q_cols - m0) * (int64_t)sizeof(T);
         }
     };
-    i32x4 rp, ru, rq;
+    i32x4 rp, rq;
     int ahead = first, tile_ahead = blockIdx.x;  // the step whose loads come next
     auto next_step = [&]() {
         if (ahead == total) {
@@ -730,7 +738,6 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
             if constexpr (PARTS) {
                 const int64_t skip = MODE == kDx && first >= steps ? first - steps : first;
                 curp += skip * incp;
-                curu += skip * incp;
                 curq += skip * incq;
                 if constexpr (!PK)
                     leftp -= skip * incp;
@@ -744,10 +751,6 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
             return some ? (uint32_t)(left < (int64_t)kBufferBytes ? left : (int64_t)kBufferBytes) : 0u;
         };
         rp = buffer(curp, bytes(leftp));
-        if constexpr (kBoth) {
-            ru = buffer(curu, bytes(leftp));
-            curu += incp;
-        }
         rq = buffer(curq, bytes(leftq));
         curp += incp;
         curq += incq;
@@ -775,15 +778,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
     constexpr int kLoads = PT::kLoads + QT::kLoads;
     auto issue = [&](uint32_t place, int i) {
         if (i < PT::kLoads)
-            load_lds16(ldsp + place + i * 1024, offp[i], kBoth && i / kTurn % 2 ? ru : rp);
+            load_lds16(ldsp + place + i * 1024, offp[i], rp);
         else
             load_lds16(ldsq + place + (i - PT::kLoads) * 1024, offq[i - PT::kLoads], rq);
     };
 
     f32x4 acc[MT][NT];
-    // A step's loads are spread over SP parts of a step from its last part on.
-    constexpr int kSlot = kLoads / SP;
-    static_assert(kLoads % SP == 0 && SP <= STEPS, "equal slots");
 
     // Fragments: P's twice, one set multiplied while the next is read; Q's
     // once, each read again as soon as its products have been issued.
@@ -804,91 +804,89 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
         for (int i = 0; i < MT; ++i)
             read_q(place, 0, i);
     };
-    // As if steps before the first had issued them.
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < 2; ++s) {
         next_step();
 #pragma unroll
-        for (int i = 0; i < (s == NS - 1 ? kSlot : kLoads); ++i)
+        for (int i = 0; i < kLoads; ++i)
             issue(s * kStage, i);
     }
-    wait_loads<(NS - 2) * kLoads + kSlot>();
+    wait_loads<kLoads>();
     __builtin_amdgcn_s_barrier();
     // Step s: its first fragments are in registers.  Its last reads are issued
     // before its last part; a row of products into that part (BG), the barrier
     // behind which step s + 1 is in LDS and the place of step s is free for
-    // step s + NS.  Reads and loads are spread between the products; the
+    // step s + 2.  Reads and loads are spread between the products; the
     // order is kept as written.
     constexpr int BG = 1;
-    uint32_t place = 0, before = (NS - 1) * kStage;
+    uint32_t place = 0;
 #pragma unroll 1
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    int om, on, op = 0;  // this tile's place in the output
-    if constexpr (MODE == kDw) {
-        tile_of_block(tile, 2 * a.tiles_m, a.tiles_n, om, on);
-        op = om >= a.tiles_m;
-        om -= op * a.tiles_m;
-    } else {
-        tile_of_block(tile, a.tiles_m, a.tiles_n, om, on);
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            acc[i][j] = f32x4{};
-    first_part(place);
-    int s = first;
-#pragma unroll 1
-    do {
-        const uint32_t next = place + kStage == NS * kStage ? 0 : place + kStage;
-#pragma unroll
-        for (int t = 0; t < STEPS; ++t) {
-            const bool last = t == STEPS - 1;
-            if (last)
-                next_step();
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = Step<T>::mma(fp[t & 1][j], fq[i], acc[i][j]);
-                if (last && i == BG) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    // Loads of steps s + 2 .. s + NS - 1 may stay in flight.
-                    wait_loads<(NS - 2) * kLoads>();
-                    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-                    __builtin_amdgcn_s_barrier();
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                const uint32_t from = last ? next : place;
-                const int tt = last ? 0 : t + 1;
-                const int lead = last ? BG : 0;  // the row of products behind which reads start
-                if (i >= lead) {
-                    if (i == lead)
-#pragma unroll
-                        for (int k = 0; k < lead; ++k)
-                            read_q(from, tt, k);
-                    read_q(from, tt, i);
-                    const int jn = NT / (MT / 2 - 1 > 0 ? (MT / 2 < NT ? MT / 2 : NT) : 1);
-#pragma unroll
-                    for (int j = (i - lead) * jn; j < (i - lead + 1) * jn && j < NT; ++j)
-                        read_p(~t & 1, from, tt, j);
-                }
-                const int slot = last ? 0 : t + 1;
-                if (slot < SP && i >= lead) {
-                    const int rows = MT - lead, r = i - lead;
-#pragma unroll
-                    for (int k = r * kSlot / rows; k < (r + 1) * kSlot / rows; ++k)
-                        issue(last ? place : before, slot * kSlot + k);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        int om, on, op = 0;  // this tile's place in the output
+        if constexpr (MODE == kDw) {
+            tile_of_block(tile, 2 * a.tiles_m, a.tiles_n, om, on);
+            op = om >= a.tiles_m;
+            om -= op * a.tiles_m;
+        } else {
+            tile_of_block(tile, a.tiles_m, a.tiles_n, om, on);
         }
-        before = place;
-        place = next;
-    } while (++s < total);
-    // The next tile's first steps arrive meanwhile.
-    epilogue<T, MODE, BWD, PARTS>(a, (int64_t)om * BM + wm, on * BN + wn, op, acc);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                acc[i][j] = f32x4{};
+        first_part(place);
+        int s = first;
+#pragma unroll 1
+        do {
+            const uint32_t next = place ^ kStage;
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) {
+                const bool last = t == STEPS - 1;
+                if (last)
+                    next_step();
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        acc[i][j] = Step<T>::mma(fp[t & 1][j], fq[i], acc[i][j]);
+                    if (last && i == BG) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        wait_loads<0>();
+                        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+                        __builtin_amdgcn_s_barrier();
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    // The next part's fragments: Q's row i behind its products
+                    // (and those the barrier held back), P's early.
+                    const uint32_t from = last ? next : place;
+                    const int part = last ? 0 : t + 1, lead = last ? BG : 0;
+                    if (i >= lead) {
+                        if (i == lead)
+#pragma unroll
+                            for (int k = 0; k < lead; ++k)
+                                read_q(from, part, k);
+                        read_q(from, part, i);
+                        constexpr int kP = MT > NT ? 1 : 2;  // P's fragments a row
+#pragma unroll
+                        for (int j = (i - lead) * kP; j < (i - lead + 1) * kP && j < NT; ++j)
+                            read_p(~t & 1, from, part, j);
+                    }
+                    if (last && i >= BG) {
+                        constexpr int kRows = MT - BG;
+#pragma unroll
+                        for (int k = (i - BG) * kLoads / kRows; k < (i - BG + 1) * kLoads / kRows;
+                             ++k)
+                            issue(place, k);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            place = next;
+        } while (++s < total);
+        // The next tile's first steps arrive meanwhile.
+        epilogue<T, MODE, BWD, PARTS>(a, (int64_t)om * BM + wm, on * BN + wn, op, acc);
     }
     wait_loads<0>();  // no load writes LDS after the block has ended
 }
@@ -1018,22 +1016,24 @@ template <typename T>
 __global__ __launch_bounds__(256) void pack_kernel(const PackArgs<T> a)
 {
     constexpr int E = Elem<T>::kPerVec;
-    const int64_t row = ((int64_t)blockIdx.x << (8 - a.row_bits)) + (threadIdx.x >> a.row_bits);
-    if (row >= a.rows[0] + a.rows[1] + a.rows[2])
-        return;
-    int64_t r = row, ld = a.ld[0];
-    const T* from = a.from[0];
-    if (r >= a.rows[0]) {
-        r -= a.rows[0];
-        const bool third = r >= a.rows[1];
-        r -= third ? a.rows[1] : 0;
-        from = third ? a.from[2] : a.from[1];
-        ld = third ? a.ld[2] : a.ld[1];
+    const int64_t rows = a.rows[0] + a.rows[1] + a.rows[2];
+    const int per_block = 256 >> a.row_bits;
+    for (int64_t row = (int64_t)blockIdx.x * per_block + (threadIdx.x >> a.row_bits); row < rows;
+         row += (int64_t)gridDim.x * per_block) {
+        int64_t r = row, ld = a.ld[0];
+        const T* from = a.from[0];
+        if (r >= a.rows[0]) {
+            r -= a.rows[0];
+            const bool third = r >= a.rows[1];
+            r -= third ? a.rows[1] : 0;
+            from = third ? a.from[2] : a.from[1];
+            ld = third ? a.ld[2] : a.ld[1];
+        }
+        from += r * ld;
+        T* to = a.to + row * a.ld_to;
+        for (int c = (threadIdx.x & ((1 << a.row_bits) - 1)) * E; c < a.ld_to; c += E << a.row_bits)
+            store16(to + c, load_chunk(from, c, a.cols));
     }
-    from += r * ld;
-    T* to = a.to + row * a.ld_to;
-    for (int c = (threadIdx.x & ((1 << a.row_bits) - 1)) * E; c < a.ld_to; c += E << a.row_bits)
-        store16(to + c, load_chunk(from, c, a.cols));
 }
 
 // ---------------------------------------------------------------------------
@@ -1250,7 +1250,7 @@ static int gemm_fast(GemmArgs<T>& a, hipStream_t stream)
     return gemm_launch<T, MODE, BWD>(
         a,
         reinterpret_cast<const void*>(
-            &gemm_fast_kernel<T, MODE, BWD && !PARTS, WM, WN, MT, NT, 128, 2, 1, PARTS>),
+            &gemm_fast_kernel<T, MODE, BWD && !PARTS, WM, WN, MT, NT, PARTS>),
         WM * MT * 16, WN * NT * 16, WM * WN * 64,
         MODE == kUp && !PARTS ? resident_blocks(kLds) : 0, stream);
 }
@@ -1363,9 +1363,10 @@ struct Inputs {
         const int64_t rows = (int64_t)(tokens + 2 * hidden);
         if (rows == 0 || ld == 0)
             return MESWISH_OK;
+        const int64_t blocks = ((rows << a.row_bits) + 255) / 256;
         void* args[] = {&a};
-        return launch_over(reinterpret_cast<const void*>(&pack_kernel<T>), rows << a.row_bits, args,
-                           stream);
+        return launch(reinterpret_cast<const void*>(&pack_kernel<T>),
+                      dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), 256, args, stream);
     }
 };
 
