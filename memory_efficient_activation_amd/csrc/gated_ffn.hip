@@ -1150,7 +1150,7 @@ static size_t padded(size_t hidden) { return (hidden + 63) / 64 * 64; }
 constexpr int kCus = 256;
 
 // How a product is computed: 256 x 256 tiles or 128 x 128, and in how many
-// parts its sum is split (128 x 128 tiles only).
+// parts its sum is split.
 struct Plan {
     bool big;
     int splits;
@@ -1158,33 +1158,43 @@ struct Plan {
 
 // The least of the estimated times.  A block's step of 128 bytes of k takes
 // what its instructions take (a bf16 128 x 128 step 0.4 us of a CU, binary32
-// 1.75 us; a 256 x 256 step 1.2 and 7 us), and no less than the 0.7 us its
+// 1.75 us; a 256 x 256 step 1.2 and 6.8 us), and no less than the 0.7 us its
 // loads take, which two blocks of a CU share; parts are written and read
-// again at some 4 TB/s, by one more launch (3 us).  Measured, bf16, one
-// unsplit tile shape against the other and splits of 1 to 16 on both sides
-// of each choice: see the figures beside gemm_run.
+// again at some 4 TB/s, by one more launch (3 us).
+//
+// Measured both ways, bf16, tokens x dim x hidden:
+//   256 x 256 against 128 x 128, unsplit: forward 16384 x 4096 x 16384 3118 us
+//   against 3981, 64 x 4096 x 16384 86 against 58, 777 x 1000 x 2736 26
+//   against 19; dWg and dWu 777 x 1000 x 2736 26 against 18.
+//   dx, 128 x 128: 64 x 4096 x 16384 308 us whole, 104 in 4 parts, 64 in 16;
+//   777 x 1000 x 2736 52, 25 in 4, 29 in 8; 16384 x 4096 x 16384 4017, 4456
+//   in 2.  dx, 256 x 256 in parts against 128 x 128 in parts: 1024 x 4096 x
+//   16384 246 against 297, 512 x 4096 x 16384 147 against 166.
+// Binary32, 256 x 256 against 128 x 128, unsplit: 8192 x 2048 x 4096 forward
+// 1853 us against 1904, dx 1857 against 1905; 2048 x 1024 x 4096 dWg and dWu
+// 476 against 250; dx there 512 whole, 272 in 2 parts.
 static Plan make_plan(int64_t rows, int64_t cols, int64_t k, int planes, int sums, size_t es)
 {
     const int64_t steps = (k + 128 / (int64_t)es - 1) / (128 / (int64_t)es) * sums;
-    const double work = es == 2 ? 0.4 : 1.75, big_step = es == 2 ? 1.2 : 7.0;
-    const int64_t tiles = (rows + 127) / 128 * ((cols + 127) / 128) * planes;
-    const int64_t bigs = (rows + 255) / 256 * ((cols + 255) / 256) * planes;
     Plan best{false, 1};
     double least = 1e30;
-    for (int s = 1; s <= 32 && (s == 1 || s * 2 <= steps); s *= 2) {
-        const int64_t blocks = (tiles * s + kCus - 1) / kCus;  // of a CU
-        double step = work * (double)blocks, loads = 0.7 * (double)((blocks + 1) / 2);
-        step = step > loads ? step : loads;
-        double t = step * (double)((steps + s - 1) / s);
-        if (s > 1)
-            t += 3.0 + (double)(tiles * s) * (128 * 128 * 8) / 4e6;
-        if (t < least) {
-            least = t;
-            best.splits = s;
+    for (int big = 0; big < 2; ++big) {
+        const int64_t side = big ? 256 : 128;
+        const int64_t tiles = (rows + side - 1) / side * ((cols + side - 1) / side) * planes;
+        const double work = big ? es == 2 ? 1.2 : 6.8 : es == 2 ? 0.4 : 1.75;
+        for (int s = 1; s <= 32 && (s == 1 || s * 2 <= steps); s *= 2) {
+            const int64_t blocks = (tiles * s + kCus - 1) / kCus;  // of a CU
+            double step = work * (double)blocks, loads = 0.7 * (double)((blocks + 1) / 2);
+            step = step > loads ? step : loads;
+            double t = step * (double)((steps + s - 1) / s);
+            if (s > 1)
+                t += 3.0 + (double)(tiles * s) * (double)(side * side * 8) / 4e6;
+            if (t < least) {
+                least = t;
+                best = Plan{big != 0, s};
+            }
         }
     }
-    if ((double)((bigs + kCus - 1) / kCus) * big_step * (double)steps < least)
-        best = Plan{true, 1};
     return best;
 }
 
@@ -1284,10 +1294,11 @@ static int gemm_run(GemmArgs<T>& a, int64_t k, float* part, hipStream_t stream)
     a.splits = p.splits;
     a.part = part;
     a.part_ld = (int)part_ld(MODE, cols);
-    if (p.splits > 1)
-        return gemm_fast<T, MODE, BWD, 2, 2, 4, 4, true>(a, stream);
-    return p.big ? gemm_fast<T, MODE, BWD, 2, 4, 8, 4, false>(a, stream)
-                 : gemm_fast<T, MODE, BWD, 2, 2, 4, 4, false>(a, stream);
+    if (p.big)
+        return p.splits > 1 ? gemm_fast<T, MODE, BWD, 2, 4, 8, 4, true>(a, stream)
+                            : gemm_fast<T, MODE, BWD, 2, 4, 8, 4, false>(a, stream);
+    return p.splits > 1 ? gemm_fast<T, MODE, BWD, 2, 2, 4, 4, true>(a, stream)
+                        : gemm_fast<T, MODE, BWD, 2, 2, 4, 4, false>(a, stream);
 }
 
 template <typename T>

@@ -31,9 +31,12 @@ def make(tokens, dim, hidden, dtype, seed):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("shape", [(4090, 4088, 2040), (4096, 2048, 4096), (1023, 2056, 6152),
-                                   (8190, 264, 1000)], ids=str)
+                                   (8190, 264, 1000), (200, 8192, 6140), (200, 32760, 4090),
+                                   (500, 1025, 16001), (8190, 200, 6140),
+                                   (12280, 200, 16380)], ids=str)
 def test_largest_tiles(shape, dtype, on_gpu):
-    """Every product in 256 x 256 tiles, with edges inside tiles and vectors."""
+    """The largest tiles, with edges inside tiles and vectors; in the last
+    five shapes one product's sum is split over such tiles."""
     x, wg, wu, dh = make(*shape, dtype, 11)
     shared = dense.SharedBuffer()
     h = ffn.gated_ffn_fwd(x, wg, wu, shared=shared)
