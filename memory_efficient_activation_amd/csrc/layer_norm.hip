@@ -7,7 +7,7 @@
 // directions read each row once and keep it in registers, packed as loaded:
 //   * A group of G threads owns a row, thread g holding the 16-byte vectors
 //     g, G + g, ... (V of them).  G is 4 to 64 lanes of a wave, or a block of
-//     256 or 1024 threads, so the sums of a row cost lane exchanges only, or
+//     128 to 1024 threads, so the sums of a row cost lane exchanges only, or
 //     one exchange through LDS a batch of R rows.  (bf16 16384 x 4096 forward:
 //     a block a row 46 us; a wave a row, V = 8, 66 us: its registers leave too
 //     few waves.)
@@ -42,7 +42,7 @@ constexpr int64_t kMaxGrid = 1 << 23;
 
 template <int G>
 struct Group {
-    static constexpr int kThreads = G > 256 ? G : 256;
+    static constexpr int kThreads = G > 64 ? G : 256;
     static constexpr int kGroups = kThreads / G;  // rows a block takes at once
     static constexpr int kWaves = G / 64;         // waves of a group, where it is whole waves
 };
@@ -549,30 +549,45 @@ static int fwd_launch(LnArgs<T, P>& a)
                   Group<G>::kThreads, args, a.stream);
 }
 
+// The smallest group whose vectors hold the row.  Which V and R go with it was
+// measured on bf16 tensors of 2^26 elements, group x vectors, rows at once (us):
+//   n = 128 to 512   8 to 32 x 2, 2 rows: 50-52    16 to 64 x 1, 2 rows: 59
+//                    (4 rows of either: 60-63)
+//   n = 64           8 x 1, 2 rows: 46             4 x 2: 54, 8 x 1, 4 rows: 60
+//   n = 1024         64 x 2, 2 rows: 51            32 x 4: 61, 64 x 2, 4 rows: 64
+//   n = 2048         128 x 2, 2 rows: 52           256 x 1, 64 x 4: 62
+//   n = 4096         256 x 2, 2 rows: 53           256 x 2, 1 row: 55, 512 x 1: 54-56
+//   n = 8192         512 x 2, 1 row: 56            1024 x 1: 58-72, 256 x 4: 78
+//   n = 16384        1024 x 2, 1 row: 69           512 x 4: 78, 256 x 8: 117
+// Binary32, whose vectors hold half as many values, differs where `kTwo` is used:
+//   n = 64 to 256    16 to 64 x 1, 2 rows: 101     8 to 32 x 2: 118
+//   n = 1024         256 x 1, 2 rows: 98           128 x 2: 105
+//   n = 8192         512 x 4, 1 row: 102           1024 x 2: 120
 template <typename T, typename P>
 static int fwd_run(LnArgs<T, P>& a)
 {
+    constexpr bool kTwo = sizeof(T) == 2;
     const int64_t c = chunks<T>(a.n);
     if (c <= 4)
         return fwd_launch<T, P, 4, 1, 2>(a);
     if (c <= 8)
         return fwd_launch<T, P, 8, 1, 2>(a);
     if (c <= 16)
-        return fwd_launch<T, P, 16, 1, 2>(a);
+        return fwd_launch<T, P, kTwo ? 8 : 16, kTwo ? 2 : 1, 2>(a);
     if (c <= 32)
-        return fwd_launch<T, P, 32, 1, 2>(a);
+        return fwd_launch<T, P, kTwo ? 16 : 32, kTwo ? 2 : 1, 2>(a);
     if (c <= 64)
-        return fwd_launch<T, P, 64, 1, 2>(a);
+        return fwd_launch<T, P, kTwo ? 32 : 64, kTwo ? 2 : 1, 2>(a);
     if (c <= 128)
         return fwd_launch<T, P, 64, 2, 2>(a);
     if (c <= 256)
-        return fwd_launch<T, P, 256, 1, 2>(a);
+        return fwd_launch<T, P, kTwo ? 128 : 256, kTwo ? 2 : 1, 2>(a);
     if (c <= 512)
         return fwd_launch<T, P, 256, 2, 2>(a);
     if (c <= 1024)
-        return fwd_launch<T, P, 256, 4, 1>(a);
+        return fwd_launch<T, P, 512, 2, 1>(a);
     if (c <= 2048)
-        return fwd_launch<T, P, 1024, 2, 1>(a);
+        return fwd_launch<T, P, kTwo ? 1024 : 512, kTwo ? 2 : 4, 1>(a);
     int64_t grid = a.rows < kMaxGrid ? a.rows : kMaxGrid;
     void* args[] = {&a.x, &a.ldx, &a.w, &a.b, &a.rows, &a.n, &a.eps, &a.out, &a.ldo, &a.mean,
                     &a.rstd};
@@ -606,6 +621,13 @@ static int bwd_launch(LnArgs<T, P>& a)
     return params_launch<P>(a.part, (int)grid, a.n, a.dweight, a.dbias, a.stream);
 }
 
+// As forward; two rows' loads and the next rows' are in flight:
+//   n = 32 to 1024   as below: 76-85              half the group, twice the
+//                    vectors: 76-85; 4 rows: 77-82 (differences within 2 us)
+//   n = 2048         256 x 1, 2 rows: 83          64 x 4: 81, 128 x 2: 97-118
+//   n = 4096         256 x 2, 2 rows: 87          1 row: 86, 512 x 1: 100, 64 x 8: 101
+//   n = 8192         512 x 2, 2 rows: 108         1 row: 112, 256 x 4: 121, 1024 x 1: 125
+//   n = 16384        512 x 4, 1 row: 133          256 x 8: 147, 1024 x 2: 178
 template <typename T, typename P>
 static int bwd_run(LnArgs<T, P>& a)
 {
@@ -629,9 +651,9 @@ static int bwd_run(LnArgs<T, P>& a)
     if (c <= 512)
         return bwd_launch<T, P, 256, 2, 2>(a);
     if (c <= 1024)
-        return bwd_launch<T, P, 256, 4, 1>(a);
+        return bwd_launch<T, P, 512, 2, 2>(a);
     if (c <= 2048)
-        return bwd_launch<T, P, 1024, 2, 1>(a);
+        return bwd_launch<T, P, 512, 4, 1>(a);
     if (a.part) {
         int64_t rowsplit = a.rows < kMaxParts ? a.rows : kMaxParts;
         void* args[] = {&a.x, &a.ldx, &a.dy, &a.lddy, &a.mean, &a.rstd, &a.rows, &a.n, &a.part};
