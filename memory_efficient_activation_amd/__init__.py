@@ -1,7 +1,7 @@
 """memory_efficient_activation_amd -- memory-efficient Swish for MI355X.
 
 The hot path is libmeswish.so (HIP kernels for gfx950 behind a C ABI,
-declared in include/meswish.h and include/dense_bn.h).  This package is a thin binding over it:
+declared in the headers under include/).  This package is a thin binding over it:
 
 * ``swish_fwd``, ``swish_bwd``, ``swish_fwd_grouped``, ``swish_bwd_grouped``
   -- tensor-level calls with the C ABI's names;
@@ -12,6 +12,11 @@ declared in include/meswish.h and include/dense_bn.h).  This package is a thin b
 * ``dense`` -- the shared-buffer DenseNet layer stage (concatenation +
   batch normalization + ReLU written to a shared buffer and recomputed in
   the backward; include/dense_bn.h) and its bottleneck modules;
+* ``norm`` -- layer normalization that keeps its input and two values a row
+  (include/layer_norm.h);
+* ``ffn`` -- the gated feed-forward unit f(x Wg^T) * (x Wu^T), recomputed from
+  its input in the backward, and the pre-normalized block of both
+  (include/gated_ffn.h);
 * ``naive.Swish`` -- the plain module, for comparisons;
 * ``inputs`` -- seeded synthetic workloads; ``accounting`` -- byte counts.
 
