@@ -85,6 +85,25 @@ template <> struct Elem<bf16_t> {
     }
 };
 
+// v without its first s elements (0 < s < kPerVec), zeros behind the rest.
+template <typename T>
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int s)
+{
+    constexpr int kPerWord = 4 / (int)sizeof(T);
+    uint32_t a = v[0], b = v[1], c = v[2], d = v[3];
+    if (s & 2 * kPerWord)
+        a = c, b = d, c = d = 0;
+    if (s & kPerWord)
+        a = b, b = c, c = d, d = 0;
+    if (kPerWord == 2 && s & 1) {
+        a = a >> 16 | b << 16;
+        b = b >> 16 | c << 16;
+        c = c >> 16 | d << 16;
+        d >>= 16;
+    }
+    return u32x4{a, b, c, d};
+}
+
 // The last elements of a row, from e0 (e0 < n < e0 + kPerVec) on, zeros behind
 // them: the row's last whole vector shifted down; a row shorter than a vector
 // element by element.  Few registers: this is inlined wherever rows are read.
@@ -94,19 +113,7 @@ __device__ __forceinline__ u32x4 load_tail(const T* row, int e0, int n)
     constexpr int E = Elem<T>::kPerVec, kPerWord = 4 / (int)sizeof(T);
     uint32_t a = 0, b = 0, c = 0, d = 0;
     if (n >= E) {
-        const u32x4 v = load16(row + n - E);
-        a = v[0], b = v[1], c = v[2], d = v[3];
-        const int s = e0 - (n - E);  // elements to drop, 1 .. E - 1
-        if (s & 2 * kPerWord)
-            a = c, b = d, c = d = 0;
-        if (s & kPerWord)
-            a = b, b = c, c = d, d = 0;
-        if (kPerWord == 2 && s & 1) {
-            a = a >> 16 | b << 16;
-            b = b >> 16 | c << 16;
-            c = c >> 16 | d << 16;
-            d >>= 16;
-        }
+        return shift_down<T>(load16(row + n - E), e0 - (n - E));
     } else {
 #pragma unroll 1
         for (int j = 0; j < n - e0; ++j) {
@@ -131,6 +138,25 @@ __device__ __forceinline__ u32x4 load_chunk(const T* row, int e0, int n)
     if (e0 + Elem<T>::kPerVec <= n)
         return load16(row + e0);
     return e0 < n ? load_tail(row, e0, n) : u32x4{0, 0, 0, 0};
+}
+
+// load_chunk in two steps, for rows of a vector or more: a load that takes no
+// branch, so that several of them are in flight together, and what makes it
+// the chunk, where it is used (n = 0 there: zeros).
+template <typename T>
+__device__ __forceinline__ u32x4 load_near(const T* row, int e0, int n)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    return load16(row + (e0 + E <= n ? e0 : n - E));
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 chunk_of(u32x4 v, int e0, int n)
+{
+    const int s = e0 - (n - Elem<T>::kPerVec);
+    if (s >= Elem<T>::kPerVec)
+        return u32x4{0, 0, 0, 0};
+    return s > 0 ? shift_down<T>(v, s) : v;
 }
 
 template <typename T>

@@ -97,6 +97,28 @@ __device__ __forceinline__ void load_params(const P* p, int e0, int n, float non
     }
 }
 
+// Elements e0 ... of a row for a group of G, zeros past its end and in rows past
+// the last, in two steps (load_near).  Rows shorter than a vector are of the
+// smallest group alone, which loads the chunk at once.
+template <int G, typename T>
+__device__ __forceinline__ u32x4 load_row(const T* x, int64_t row, int64_t rows, int64_t ldx,
+                                          int e0, int n)
+{
+    if constexpr (G == 4)
+        return load_chunk(x + row * ldx, e0, row < rows ? n : 0);
+    else
+        return load_near(x + (row < rows ? row : rows - 1) * ldx, e0, n);
+}
+
+template <typename T, int G>
+__device__ __forceinline__ u32x4 row_chunk(u32x4 v, int e0, int n)
+{
+    if constexpr (G == 4)
+        return v;
+    else
+        return chunk_of<T>(v, e0, n);
+}
+
 // ---------------------------------------------------------------------------
 // Forward.
 // ---------------------------------------------------------------------------
@@ -131,14 +153,16 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_fwd_kernel(
             const int64_t row = base + r * NG + grp;
 #pragma unroll
             for (int v = 0; v < V; ++v)  // a row past the end counts as an empty one
-                raw[r][v] = load_chunk(x + row * ldx, (v * G + g) * E, row < rows ? n : 0);
+                raw[r][v] = load_row<G>(x, row, rows, ldx, (v * G + g) * E, n);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            const int nr = base + r * NG + grp < rows ? n : 0;
             s[r] = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float f[E];
+                raw[r][v] = row_chunk<T, G>(raw[r][v], (v * G + g) * E, nr);
                 Elem<T>::unpack(raw[r][v], f);
 #pragma unroll
                 for (int j = 0; j < E; ++j)
@@ -300,8 +324,8 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 // A row past the end counts as an empty one (zeros).
-                rx[r][v] = load_chunk(x + row * ldx, (v * G + g) * E, in ? n : 0);
-                rd[r][v] = load_chunk(dy + row * lddy, (v * G + g) * E, in ? n : 0);
+                rx[r][v] = load_row<G>(x, row, rows, ldx, (v * G + g) * E, n);
+                rd[r][v] = load_row<G>(dy, row, rows, lddy, (v * G + g) * E, n);
             }
         }
     };
@@ -317,8 +341,9 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
             t[r] = rs[r];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                cx[r][v] = rx[r][v];
-                cd[r][v] = rd[r][v];
+                const int nr = base + r * NG + grp < rows ? n : 0;
+                cx[r][v] = row_chunk<T, G>(rx[r][v], (v * G + g) * E, nr);
+                cd[r][v] = row_chunk<T, G>(rd[r][v], (v * G + g) * E, nr);
             }
         }
         if (base + step < rows)
