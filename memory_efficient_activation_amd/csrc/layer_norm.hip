@@ -2,15 +2,17 @@
 // and backward.  Formulas and contracts: include/layer_norm.h.
 //
 // Bound: HBM bandwidth (8 flops an element forward, 15 backward).  Measured on
-// bf16 16384 x 4096: forward 46 us (5.8 TB/s of the rows read and written),
-// backward 90 us (4.5 TB/s); the framework's plain copy moves 6.3 TB/s.  Both
+// bf16 16384 x 4096: forward 44 us (6.1 TB/s of the rows read and written),
+// backward 86 us (4.7 TB/s); the framework's plain copy moves 6.3 TB/s.  Both
 // directions read each row once and keep it in registers, packed as loaded:
 //   * A group of G threads owns a row, thread g holding the 16-byte vectors
 //     g, G + g, ... (V of them).  G is 4 to 64 lanes of a wave, or a block of
 //     128 to 1024 threads, so the sums of a row cost lane exchanges only, or
 //     one exchange through LDS a batch of R rows.  (bf16 16384 x 4096 forward:
-//     a block a row 46 us; a wave a row, V = 8, 66 us: its registers leave too
-//     few waves.)
+//     a block a row 44 us; a wave a row, V = 8, 66 us: its registers leave too
+//     few waves.)  Rows are loaded without a branch, a row's last vector from
+//     inside the row, and cut to length where they are used: with the branch
+//     at the load the forward took 53 us.
 //   * The variance is the mean of squared differences from the mean, from
 //     the registers: no cancellation of E[x^2] - mean^2.
 //   * Backward: a thread owns the same columns in every row its block takes,
@@ -574,45 +576,41 @@ static int fwd_launch(LnArgs<T, P>& a)
                   Group<G>::kThreads, args, a.stream);
 }
 
-// The smallest group whose vectors hold the row.  Which V and R go with it was
-// measured on bf16 tensors of 2^26 elements, group x vectors, rows at once (us):
-//   n = 128 to 512   8 to 32 x 2, 2 rows: 50-52    16 to 64 x 1, 2 rows: 59
-//                    (4 rows of either: 60-63)
-//   n = 64           8 x 1, 2 rows: 46             4 x 2: 54, 8 x 1, 4 rows: 60
-//   n = 1024         64 x 2, 2 rows: 51            32 x 4: 61, 64 x 2, 4 rows: 64
-//   n = 2048         128 x 2, 2 rows: 52           256 x 1, 64 x 4: 62
-//   n = 4096         256 x 2, 2 rows: 53           256 x 2, 1 row: 55, 512 x 1: 54-56
-//   n = 8192         512 x 2, 1 row: 56            1024 x 1: 58-72, 256 x 4: 78
-//   n = 16384        1024 x 2, 1 row: 69           512 x 4: 78, 256 x 8: 117
-// Binary32, whose vectors hold half as many values, differs where `kTwo` is used:
-//   n = 64 to 256    16 to 64 x 1, 2 rows: 101     8 to 32 x 2: 118
-//   n = 1024         256 x 1, 2 rows: 98           128 x 2: 105
-//   n = 8192         512 x 4, 1 row: 102           1024 x 2: 120
+// The smallest group whose vectors hold the row.  Which vectors and rows go with
+// it was measured on bf16 tensors of 2^26 elements, group x vectors (us):
+//   n = 64           8 x 1, 2 rows: 46             4 x 2, 2 rows: 49
+//   n = 128 to 512   8 to 32 x 2, 2 rows: 43-45    16 to 64 x 1: 47-49; 1 row: 45-48
+//   n = 1024         64 x 2, 2 rows: 43            32 x 4, 1 row: 44
+//   n = 2048         128 x 2, 2 rows: 44           256 x 1, 2 rows: 52, 64 x 4, 1 row: 45
+//   n = 4096         256 x 2, 2 rows: 44           512 x 1, 2 rows: 48
+//   n = 8192         256 x 4, 1 row: 47            512 x 2, 1 row: 49
+//   n = 16384        1024 x 2, 1 row: 65           512 x 4, 1 row: 65
+// Binary32 is within 3 % of its best with the same choices (n = 8192: 1024 x 2
+// 98, 512 x 4 95).
 template <typename T, typename P>
 static int fwd_run(LnArgs<T, P>& a)
 {
-    constexpr bool kTwo = sizeof(T) == 2;
     const int64_t c = chunks<T>(a.n);
     if (c <= 4)
         return fwd_launch<T, P, 4, 1, 2>(a);
     if (c <= 8)
         return fwd_launch<T, P, 8, 1, 2>(a);
     if (c <= 16)
-        return fwd_launch<T, P, kTwo ? 8 : 16, kTwo ? 2 : 1, 2>(a);
+        return fwd_launch<T, P, 8, 2, 2>(a);
     if (c <= 32)
-        return fwd_launch<T, P, kTwo ? 16 : 32, kTwo ? 2 : 1, 2>(a);
+        return fwd_launch<T, P, 16, 2, 2>(a);
     if (c <= 64)
-        return fwd_launch<T, P, kTwo ? 32 : 64, kTwo ? 2 : 1, 2>(a);
+        return fwd_launch<T, P, 32, 2, 2>(a);
     if (c <= 128)
         return fwd_launch<T, P, 64, 2, 2>(a);
     if (c <= 256)
-        return fwd_launch<T, P, kTwo ? 128 : 256, kTwo ? 2 : 1, 2>(a);
+        return fwd_launch<T, P, 128, 2, 2>(a);
     if (c <= 512)
         return fwd_launch<T, P, 256, 2, 2>(a);
     if (c <= 1024)
-        return fwd_launch<T, P, 512, 2, 1>(a);
+        return fwd_launch<T, P, 256, 4, 1>(a);
     if (c <= 2048)
-        return fwd_launch<T, P, kTwo ? 1024 : 512, kTwo ? 2 : 4, 1>(a);
+        return fwd_launch<T, P, 1024, 2, 1>(a);
     int64_t grid = a.rows < kMaxGrid ? a.rows : kMaxGrid;
     void* args[] = {&a.x, &a.ldx, &a.w, &a.b, &a.rows, &a.n, &a.eps, &a.out, &a.ldo, &a.mean,
                     &a.rstd};
@@ -646,13 +644,14 @@ static int bwd_launch(LnArgs<T, P>& a)
     return params_launch<P>(a.part, (int)grid, a.n, a.dweight, a.dbias, a.stream);
 }
 
-// As forward; two rows' loads and the next rows' are in flight:
-//   n = 32 to 1024   as below: 76-85              half the group, twice the
-//                    vectors: 76-85; 4 rows: 77-82 (differences within 2 us)
-//   n = 2048         256 x 1, 2 rows: 83          64 x 4: 81, 128 x 2: 97-118
-//   n = 4096         256 x 2, 2 rows: 87          1 row: 86, 512 x 1: 100, 64 x 8: 101
-//   n = 8192         512 x 2, 2 rows: 108         1 row: 112, 256 x 4: 121, 1024 x 1: 125
-//   n = 16384        512 x 4, 1 row: 133          256 x 8: 147, 1024 x 2: 178
+// As forward; here a thread also has the rows that follow in flight, and two
+// vectors a thread gain nothing where one does (us):
+//   n = 512          64 x 1, 2 rows: 75            32 x 2, 2 rows: 79
+//   n = 1024         64 x 2, 1 row: 75             32 x 4, 1 row: 81
+//   n = 2048         256 x 1, 2 rows: 79           128 x 2, 2 rows: 82
+//   n = 4096         256 x 2, 2 rows: 86           512 x 1, 2 rows: 86
+//   n = 8192         256 x 4, 1 row: 100           512 x 2, 2 rows: 101
+//   n = 16384        1024 x 2, 1 row: 127          512 x 4, 1 row: 129
 template <typename T, typename P>
 static int bwd_run(LnArgs<T, P>& a)
 {
@@ -676,9 +675,9 @@ static int bwd_run(LnArgs<T, P>& a)
     if (c <= 512)
         return bwd_launch<T, P, 256, 2, 2>(a);
     if (c <= 1024)
-        return bwd_launch<T, P, 512, 2, 2>(a);
+        return bwd_launch<T, P, 256, 4, 1>(a);
     if (c <= 2048)
-        return bwd_launch<T, P, 512, 4, 1>(a);
+        return bwd_launch<T, P, 1024, 2, 1>(a);
     if (a.part) {
         int64_t rowsplit = a.rows < kMaxParts ? a.rows : kMaxParts;
         void* args[] = {&a.x, &a.ldx, &a.dy, &a.lddy, &a.mean, &a.rstd, &a.rows, &a.n, &a.part};
