@@ -40,7 +40,10 @@ constexpr int kMaxParts = 512;
 // registers: eight of 256 threads on a CU (bf16 16384 x 4096: 2048 blocks 47 us,
 // 1536 55; one block a row, reading the parameters again, 64).
 constexpr int kFwdBlocks = 2048;
-constexpr int64_t kMaxGrid = 1 << 23;
+// Most blocks of the kernels of 1024 threads, which loop over what is left: a
+// launch has fewer than 2^32 threads.
+constexpr int64_t kMaxGrid = 1 << 21;
+static_assert(kMaxGrid * 1024 <= UINT32_MAX, "threads of a launch");
 
 template <int G>
 struct Group {
@@ -420,38 +423,42 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
     }
 }
 
-// dweight and dbias from the blocks' partial sums: 32 columns a block, 32
-// threads a column.
+// dweight and dbias from the blocks' partial sums: 32 columns a block at a
+// time, 32 threads a column.
 template <typename P>
 __global__ __launch_bounds__(1024) void ln_params_kernel(const float* __restrict__ part, int parts,
                                                          int n, P* dweight, P* dbias)
 {
     __shared__ float lds[32][33];
     const int c = threadIdx.x % 32, k = threadIdx.x / 32;
-    const int64_t col = (int64_t)blockIdx.x * 32 + c;  // of 2 n: dweight's, then dbias's
-    float s = 0.0f;
-    if (col < 2 * (int64_t)n)
-        for (int p = k; p < parts; p += 32 * 8) {
-            float f[8];  // eight loads in flight
+    const int64_t cols = 2 * (int64_t)n;  // dweight's, then dbias's
+    for (int64_t first = (int64_t)blockIdx.x * 32; first < cols; first += (int64_t)gridDim.x * 32) {
+        const int64_t col = first + c;
+        float s = 0.0f;
+        if (col < cols)
+            for (int p = k; p < parts; p += 32 * 8) {
+                float f[8];  // eight loads in flight
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = p + 32 * i < parts ? part[(int64_t)(p + 32 * i) * 2 * n + col] : 0.0f;
+                for (int i = 0; i < 8; ++i)
+                    f[i] = p + 32 * i < parts ? part[(p + 32 * i) * cols + col] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                s += f[i];
+                for (int i = 0; i < 8; ++i)
+                    s += f[i];
+            }
+        lds[k][c] = s;
+        __syncthreads();
+        // Thread (c', k') takes column k', part c': a half wave a column.
+        float t = lds[c][k];
+#pragma unroll
+        for (int m = 16; m; m >>= 1)
+            t += __shfl_xor(t, m);
+        const int64_t out = first + k;
+        if (c == 0 && out < cols) {
+            P* dst = out < n ? dweight : dbias;
+            if (dst)
+                dst[out < n ? out : out - n] = Elem<P>::put(t);
         }
-    lds[k][c] = s;
-    __syncthreads();
-    // Thread (c', k') takes column k', part c': a half wave a column.
-    float t = lds[c][k];
-#pragma unroll
-    for (int m = 16; m; m >>= 1)
-        t += __shfl_xor(t, m);
-    const int64_t out = (int64_t)blockIdx.x * 32 + k;
-    if (c == 0 && out < 2 * (int64_t)n) {
-        P* dst = out < n ? dweight : dbias;
-        if (dst)
-            dst[out < n ? out : out - n] = Elem<P>::put(t);
+        __syncthreads();
     }
 }
 
@@ -623,9 +630,9 @@ static int params_launch(const float* part, int parts, int n, P* dweight, P* dbi
                          hipStream_t stream)
 {
     void* args[] = {&part, &parts, &n, &dweight, &dbias};
-    const int64_t grid = (2 * (int64_t)n + 31) / 32;
-    return launch(reinterpret_cast<const void*>(&ln_params_kernel<P>), dim3((unsigned)grid), 1024,
-                  args, stream);
+    const int64_t blocks = (2 * (int64_t)n + 31) / 32;
+    return launch(reinterpret_cast<const void*>(&ln_params_kernel<P>),
+                  dim3((unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid)), 1024, args, stream);
 }
 
 template <typename T, typename P, int G, int V, int R>
