@@ -131,11 +131,13 @@ __device__ __forceinline__ u32x4 load_tail(const T* row, int e0, int n)
 }
 
 // Elements e0 .. e0 + kPerVec - 1 of a row of n, as one packed vector; those
-// past the end are zero and are not read.
+// past the end are zero and are not read.  (Here and below whole vectors are
+// told by e0 <= n - kPerVec: e0 + kPerVec passes 31 bits where n is nearly
+// 2^31.)
 template <typename T>
 __device__ __forceinline__ u32x4 load_chunk(const T* row, int e0, int n)
 {
-    if (e0 + Elem<T>::kPerVec <= n)
+    if (e0 <= n - Elem<T>::kPerVec)
         return load16(row + e0);
     return e0 < n ? load_tail(row, e0, n) : u32x4{0, 0, 0, 0};
 }
@@ -147,7 +149,7 @@ template <typename T>
 __device__ __forceinline__ u32x4 load_near(const T* row, int e0, int n)
 {
     constexpr int E = Elem<T>::kPerVec;
-    return load16(row + (e0 + E <= n ? e0 : n - E));
+    return load16(row + (e0 <= n - E ? e0 : n - E));
 }
 
 template <typename T>
@@ -163,7 +165,7 @@ template <typename T>
 __device__ __forceinline__ void store_chunk(T* row, int e0, int n, const float* f)
 {
     constexpr int E = Elem<T>::kPerVec;
-    if (e0 + E <= n) {
+    if (e0 <= n - E) {
         store16(row + e0, Elem<T>::pack(f));
         return;
     }

@@ -536,12 +536,12 @@ __global__ __launch_bounds__(256) void ln_cols_kernel(const T* __restrict__ x, i
             ab[j] += fd[j];
         }
     }
-    float* pw = part + (int64_t)blockIdx.y * 2 * n;
+    float* pw = part + (int64_t)blockIdx.y * 2 * n + first;
 #pragma unroll
     for (int j = 0; j < E; ++j)
         if (e0 + j < n) {
-            pw[e0 + j] = aw[j];
-            pw[n + e0 + j] = ab[j];
+            pw[j] = aw[j];
+            pw[(int64_t)n + j] = ab[j];
         }
 }
 

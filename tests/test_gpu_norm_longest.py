@@ -112,3 +112,12 @@ def test_more_long_rows_than_blocks(n, dtype):
     res.append(o.worst(x[some], want[0], bound[0]))
     say(f"errors over bounds {res}")
     assert max(res) <= 1
+
+
+@pytest.mark.parametrize("n,dtype", [((1 << 30) + 5, F32), ((1 << 31) - 8, BF16),
+                                     ((1 << 31) - 1, BF16)], ids=str)
+def test_columns_whose_indexes_pass_31_bits(n, dtype):
+    """Past 2^30 twice a column's index (dbias's partial sums lie behind
+    dweight's), and within a vector of 2^31, the longest row, a column's index
+    plus the vector's length."""
+    one_row(n, dtype)
