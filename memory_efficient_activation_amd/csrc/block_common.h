@@ -144,12 +144,14 @@ __device__ __forceinline__ u32x4 load_chunk(const T* row, int e0, int n)
 
 // load_chunk in two steps, for rows of a vector or more: a load that takes no
 // branch, so that several of them are in flight together, and what makes it
-// the chunk, where it is used (n = 0 there: zeros).
+// the chunk, where it is used (n = 0 there: zeros).  For rows of registers, far
+// from 2^31: with e0 <= n - kPerVec here the backward of 4096 x 16384 bf16 takes
+// 129 us instead of 127.
 template <typename T>
 __device__ __forceinline__ u32x4 load_near(const T* row, int e0, int n)
 {
     constexpr int E = Elem<T>::kPerVec;
-    return load16(row + (e0 <= n - E ? e0 : n - E));
+    return load16(row + (e0 + E <= n ? e0 : n - E));
 }
 
 template <typename T>
