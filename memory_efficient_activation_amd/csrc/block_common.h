@@ -104,6 +104,30 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int s)
     return u32x4{a, b, c, d};
 }
 
+// v without its first s elements (0 < s < kPerVec), those behind the rest.
+template <typename T>
+__device__ __forceinline__ u32x4 rotate_down(u32x4 v, int s)
+{
+    constexpr int kPerWord = 4 / (int)sizeof(T);
+    uint32_t a = v[0], b = v[1], c = v[2], d = v[3];
+    if (s & 2 * kPerWord) {
+        const uint32_t e = a, f = b;
+        a = c, b = d, c = e, d = f;
+    }
+    if (s & kPerWord) {
+        const uint32_t e = a;
+        a = b, b = c, c = d, d = e;
+    }
+    if (kPerWord == 2 && s & 1) {
+        const uint32_t e = a;
+        a = a >> 16 | b << 16;
+        b = b >> 16 | c << 16;
+        c = c >> 16 | d << 16;
+        d = d >> 16 | e << 16;
+    }
+    return u32x4{a, b, c, d};
+}
+
 // The last elements of a row, from e0 (e0 < n < e0 + kPerVec) on, zeros behind
 // them: the row's last whole vector shifted down; a row shorter than a vector
 // element by element.  Few registers: this is inlined wherever rows are read.
@@ -161,6 +185,34 @@ __device__ __forceinline__ u32x4 chunk_of(u32x4 v, int e0, int n)
     if (s >= Elem<T>::kPerVec)
         return u32x4{0, 0, 0, 0};
     return s > 0 ? shift_down<T>(v, s) : v;
+}
+
+// load_chunk with other elements of the row, any of them, in the place of the
+// zeros past its end (zeros where n = 0).
+template <typename T>
+__device__ __forceinline__ u32x4 load_repeat(const T* row, int e0, int n)
+{
+    constexpr int E = Elem<T>::kPerVec, kPerWord = 4 / (int)sizeof(T);
+    if (e0 <= n - E)
+        return load16(row + e0);
+    if (n >= E) {
+        const u32x4 v = load16(row + n - E);
+        const int s = e0 - (n - E);
+        return s < E ? rotate_down<T>(v, s) : v;
+    }
+    uint32_t a = 0, b = 0, c = 0, d = 0;
+#pragma unroll 1
+    for (int j = 0; n && j < E; ++j) {
+        uint32_t bits = 0;
+        __builtin_memcpy(&bits, row + (e0 + j < n ? e0 + j : 0), sizeof(T));
+        bits <<= j % kPerWord * 16;
+        const int w = j / kPerWord;
+        a |= w == 0 ? bits : 0;
+        b |= w == 1 ? bits : 0;
+        c |= w == 2 ? bits : 0;
+        d |= w == 3 ? bits : 0;
+    }
+    return u32x4{a, b, c, d};
 }
 
 template <typename T>

@@ -102,17 +102,20 @@ __device__ __forceinline__ void load_params(const P* p, int e0, int n, float non
     }
 }
 
-// Elements e0 ... of a row for a group of G, zeros past its end and in rows past
-// the last, in two steps (load_near).  Rows shorter than a vector are of the
-// smallest group alone, which loads the chunk at once.
-template <int G, typename T>
+// Elements e0 ... of a row for a group of G, zeros past its end (REPEAT: other
+// elements of the row) and zeros in rows past the last, in two steps (load_near).
+// Rows shorter than a vector are of the smallest group alone, which loads the
+// chunk at once.
+template <int G, bool REPEAT = false, typename T>
 __device__ __forceinline__ u32x4 load_row(const T* x, int64_t row, int64_t rows, int64_t ldx,
                                           int e0, int n)
 {
-    if constexpr (G == 4)
-        return load_chunk(x + row * ldx, e0, row < rows ? n : 0);
-    else
+    if constexpr (G != 4)
         return load_near(x + (row < rows ? row : rows - 1) * ldx, e0, n);
+    else if constexpr (REPEAT)
+        return load_repeat(x + row * ldx, e0, row < rows ? n : 0);
+    else
+        return load_chunk(x + row * ldx, e0, row < rows ? n : 0);
 }
 
 template <typename T, int G>
@@ -122,6 +125,22 @@ __device__ __forceinline__ u32x4 row_chunk(u32x4 v, int e0, int n)
         return v;
     else
         return chunk_of<T>(v, e0, n);
+}
+
+// The chunks of x (REPEAT) and dy at e0; n: the row's length, 0 for a row past
+// the last.
+template <typename T, int G>
+__device__ __forceinline__ void row_chunks(u32x4& x, u32x4& dy, int e0, int n)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    const int s = e0 - (n - E);
+    if (G == 4 || s <= 0)
+        return;
+    dy = s < E ? shift_down<T>(dy, s) : u32x4{0, 0, 0, 0};
+    if (s < E)
+        x = rotate_down<T>(x, s);
+    else if (n == 0)
+        x = dy;
 }
 
 // ---------------------------------------------------------------------------
@@ -296,7 +315,9 @@ __device__ __forceinline__ void store_part(float* pw, int n, int g, const float 
 }
 
 // R rows a group and batch: their sums share one exchange, and the next
-// batch's loads are in flight while this one is worked on.
+// batch's loads are in flight while this one is worked on.  Past a row's end dy
+// is zero and x repeats elements of the row: a zero there would make xhat
+// -mean rstd, and 0 times that is NaN where it leaves binary32.
 template <typename T, typename P, int G, int V, int R>
 __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
     const T* x, int64_t ldx, const T* dy, int64_t lddy, const float* __restrict__ mean,
@@ -329,7 +350,7 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 // A row past the end counts as an empty one (zeros).
-                rx[r][v] = load_row<G>(x, row, rows, ldx, (v * G + g) * E, n);
+                rx[r][v] = load_row<G, true>(x, row, rows, ldx, (v * G + g) * E, n);
                 rd[r][v] = load_row<G>(dy, row, rows, lddy, (v * G + g) * E, n);
             }
         }
@@ -346,9 +367,11 @@ __global__ __launch_bounds__(Group<G>::kThreads) void ln_bwd_kernel(
             t[r] = rs[r];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int nr = base + r * NG + grp < rows ? n : 0;
-                cx[r][v] = row_chunk<T, G>(rx[r][v], (v * G + g) * E, nr);
-                cd[r][v] = row_chunk<T, G>(rd[r][v], (v * G + g) * E, nr);
+                cx[r][v] = rx[r][v];
+                cd[r][v] = rd[r][v];
+                // (A batch of one row is never past the end.)
+                row_chunks<T, G>(cx[r][v], cd[r][v], (v * G + g) * E,
+                                 NG * R == 1 || base + r * NG + grp < rows ? n : 0);
             }
         }
         if (base + step < rows)
