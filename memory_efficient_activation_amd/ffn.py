@@ -16,8 +16,9 @@ computes both projections again.
 
 Weights are [hidden, dim], as ``torch.nn.Linear`` holds them.  float32 or
 bfloat16.  Tensor-level functions only check and marshal arguments; there is
-no CPU path.  The block's last projection is a plain product and PyTorch's:
-it is the model around the operators.
+no CPU path.  Gradients cannot be differentiated again (an attempt raises).
+The block's last projection is a plain product and PyTorch's: it is the model
+around the operators.
 """
 
 from __future__ import annotations
@@ -26,6 +27,7 @@ import torch
 import torch.nn as nn
 
 from . import _lib
+from ._autograd import first_order
 from .dense import EPS, SharedBuffer
 from .functional import _act_code, _dtype_code, _require_device
 from .norm import _out_rows, as_rows, launch, layer_norm_bwd, layer_norm_fwd, library
@@ -152,6 +154,7 @@ class GatedFFNFn(torch.autograd.Function):
         return gated_ffn_fwd(x, w_gate, w_up, kind, param, shared=shared)
 
     @staticmethod
+    @first_order
     def backward(ctx, dh):
         x, w_gate, w_up = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -193,6 +196,7 @@ class PreNormGatedFFNFn(torch.autograd.Function):
                            w_down.t()).view(x.shape)
 
     @staticmethod
+    @first_order
     def backward(ctx, dy):
         x, mean, rstd, weight, bias, w_gate, w_up, w_down = ctx.saved_tensors
         dy = dy.contiguous()

@@ -13,7 +13,8 @@ recomputes the normalized map, from two binary32 values a row.
 x is float32 or bfloat16 and may have any leading shape; rows at a constant
 distance (a column range of a wider matrix) are read in place.  weight and
 bias are float32 or bfloat16, independent of x.  Tensor-level functions only
-check and marshal arguments; there is no CPU path.
+check and marshal arguments; there is no CPU path.  Gradients cannot be
+differentiated again (an attempt raises).
 """
 
 from __future__ import annotations
@@ -22,6 +23,7 @@ import torch
 import torch.nn as nn
 
 from . import _lib
+from ._autograd import first_order
 from .dense import EPS, SharedBuffer
 from .functional import _dtype_code, _require_device, _same
 
@@ -169,6 +171,7 @@ class LayerNormFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @first_order
     def backward(ctx, dy):
         x, mean, rstd, weight = ctx.saved_tensors
         need_w, need_b = ctx.needs_input_grad[1:3]
