@@ -38,6 +38,7 @@ import torch.nn as nn
 import torch.nn.functional as F
 
 from . import _lib
+from ._autograd import first_order
 from .functional import _dtype_code, _require_device, _stream
 
 EPS = float(torch.tensor(1e-5, dtype=torch.float32))  # binary32, as the kernels use it
@@ -270,6 +271,7 @@ class DenseBnReluConvFn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         gamma, beta, weight = ctx.saved_tensors[:3]
         prep, n = ctx.prep, ctx.n_src

@@ -23,6 +23,7 @@ import torch
 import torch.nn as nn
 
 from . import _lib
+from ._autograd import first_order
 from .functional import _require_device, _stream
 from .dense import _current
 
@@ -171,6 +172,7 @@ class FFTConv2dFn(torch.autograd.Function):
         return fprop(x, w, buf)
 
     @staticmethod
+    @first_order
     def backward(ctx, g):
         x, w = ctx.saved_tensors
         g = g.contiguous()

@@ -17,6 +17,7 @@ from __future__ import annotations
 import torch
 from torch import nn
 
+from ._autograd import first_order
 from .functional import act_bwd, act_fwd, swish_bwd, swish_fwd
 
 
@@ -31,6 +32,7 @@ class SwishFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @first_order
     def backward(ctx, dy: torch.Tensor):
         (x,) = ctx.saved_tensors
         return swish_bwd(x, dy, ctx.alpha), None
@@ -66,6 +68,7 @@ class ActFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @first_order
     def backward(ctx, dy: torch.Tensor):
         (x,) = ctx.saved_tensors
         return act_bwd(ctx.kind, x, dy, ctx.param), None, None
