@@ -39,6 +39,7 @@ import torch.nn.functional as F
 
 from . import _lib
 from ._autograd import first_order
+from ._memory import GrowingBlock
 from .functional import _dtype_code, _require_device, _stream
 
 EPS = float(torch.tensor(1e-5, dtype=torch.float32))  # binary32, as the kernels use it
@@ -70,40 +71,25 @@ class SharedBuffer:
     implementation of DenseNets", Motivation): the normalized map z of the
     layer being computed, and the reduction workspace of the kernels.  Both
     grow to the largest request and are never shrunk.  Kernels use them in
-    stream order, so one SharedBuffer serves one stream at a time."""
+    stream order, so one SharedBuffer serves one stream at a time.  What is
+    captured into a graph gets memory of its own (see GrowingBlock)."""
 
     def __init__(self):
-        self._storage: torch.Tensor | None = None
-        self._ws: torch.Tensor | None = None
-
-    @staticmethod
-    def _dev(device) -> torch.device:
-        dev = torch.device(device)
-        if dev.type == "cuda" and dev.index is None:
-            dev = torch.device("cuda", torch.cuda.current_device())
-        return dev
+        self._storage, self._ws = GrowingBlock(), GrowingBlock()
 
     def view(self, shape, dtype, device) -> torch.Tensor:
         numel = 1
         for s in shape:
             numel *= int(s)
         nbytes = numel * torch.empty((), dtype=dtype).element_size()
-        dev = self._dev(device)
-        st = self._storage
-        if st is None or st.numel() < nbytes or st.device != dev:
-            self._storage = st = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        return st[:nbytes].view(dtype).view(shape)
+        return self._storage.take(nbytes, device)[:nbytes].view(dtype).view(shape)
 
     def workspace(self, nbytes: int, device) -> torch.Tensor:
-        dev = self._dev(device)
-        ws = self._ws
-        if ws is None or ws.numel() < nbytes or ws.device != dev:
-            self._ws = ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        return ws
+        return self._ws.take(nbytes, device)
 
     @property
     def nbytes(self) -> int:
-        return sum(0 if t is None else t.numel() for t in (self._storage, self._ws))
+        return self._storage.nbytes + self._ws.nbytes
 
 
 def workspace(n: int, channels: int, hw: int, device, shared: SharedBuffer | None = None

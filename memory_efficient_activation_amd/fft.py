@@ -24,6 +24,7 @@ import torch.nn as nn
 
 from . import _lib
 from ._autograd import first_order
+from ._memory import GrowingBlock
 from .functional import _require_device, _stream
 from .dense import _current
 
@@ -37,23 +38,18 @@ def bins(n: int) -> int:
 class FrequencyBuffer:
     """Device memory for the spectra of one layer at a time; grows to the
     largest layer it serves and is never shrunk.  Kernels use it in stream
-    order, so one buffer serves one stream at a time."""
+    order, so one buffer serves one stream at a time.  What is captured into a
+    graph gets memory of its own (see GrowingBlock)."""
 
     def __init__(self):
-        self._t: torch.Tensor | None = None
+        self._block = GrowingBlock()
 
     def get(self, nbytes: int, device) -> torch.Tensor:
-        dev = torch.device(device)
-        if dev.index is None:
-            dev = torch.device("cuda", torch.cuda.current_device())
-        t = self._t
-        if t is None or t.numel() < nbytes or t.device != dev:
-            self._t = t = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        return t
+        return self._block.take(nbytes, device)
 
     @property
     def nbytes(self) -> int:
-        return 0 if self._t is None else self._t.numel()
+        return self._block.nbytes
 
 
 def _f32(t: torch.Tensor, name: str) -> torch.Tensor:
