@@ -212,7 +212,9 @@ class PreNormGatedFFNFn(torch.autograd.Function):
 
 class PreNormGatedFeedForward(nn.Module):
     """The transformer's feed-forward block x + W_down h(LN(x)), every
-    parameter in ``dtype``.  Blocks may share one SharedBuffer."""
+    parameter in ``dtype``.  Blocks may share one SharedBuffer, if their calls
+    follow each other on one stream (and come from one thread); without one
+    each call has a workspace of its own."""
 
     def __init__(self, dim: int, hidden: int, kind: str = "swish", param: float | None = None,
                  eps: float = EPS, shared: SharedBuffer | None = None,
@@ -224,8 +226,7 @@ class PreNormGatedFeedForward(nn.Module):
         self.w_gate = nn.Parameter(torch.randn(hidden, dim, dtype=dtype) * dim ** -0.5)
         self.w_up = nn.Parameter(torch.randn(hidden, dim, dtype=dtype) * dim ** -0.5)
         self.w_down = nn.Parameter(torch.randn(dim, hidden, dtype=dtype) * hidden ** -0.5)
-        self.kind, self.param, self.eps = kind, param, float(eps)
-        self.shared = shared if shared is not None else SharedBuffer()
+        self.kind, self.param, self.eps, self.shared = kind, param, float(eps), shared
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         return PreNormGatedFFNFn.apply(x, self.weight, self.bias, self.w_gate, self.w_up,

@@ -5,7 +5,7 @@ are)."""
 import pytest
 import torch
 
-from memory_efficient_activation_amd import ffn, norm
+from memory_efficient_activation_amd import dense, ffn, norm
 from oracle import ffn_oracle as o
 
 
@@ -86,3 +86,12 @@ def test_first_derivatives_of_the_block(formulas):
     for a, b in zip(got, torch.autograd.grad(plain, wrt, dy)):
         # Binary32 sums of up to 24 products and some ten roundings on the way.
         assert float((a - b).norm()) <= 34 * 2.0 ** -24 * 10 * float(b.norm())
+
+
+def test_a_block_shares_memory_only_when_asked():
+    """A buffer serves one stream at a time; calls of one module from two
+    streams or threads would race in one that the module made itself."""
+    shared = dense.SharedBuffer()
+    assert ffn.PreNormGatedFeedForward(16, 24).shared is None
+    assert ffn.GatedUnit(16, 24).shared is None and norm.LayerNorm(16).shared is None
+    assert ffn.PreNormGatedFeedForward(16, 24, shared=shared).shared is shared

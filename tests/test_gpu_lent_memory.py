@@ -92,3 +92,33 @@ def test_a_block_waits_for_the_stream_that_uses_it(take):
     other = torch.empty(size, dtype=torch.uint8, device=DEV)
     assert not done.query() and other.data_ptr() != at
     torch.cuda.synchronize()
+
+
+def test_one_block_on_two_streams():
+    """Forward and backward of one module on two streams at once, many times:
+    each gives what it gives alone (to the roundings of the projection's library
+    products, whose order of sums is not ours to know)."""
+    torch.manual_seed(4)
+    m = ffn.PreNormGatedFeedForward(104, 1000, dtype=BF16).to(DEV)
+    xs = [torch.randn(700, 104, device=DEV).to(BF16) for _ in range(2)]
+    dys = [torch.randn(700, 104, device=DEV).to(BF16) for _ in range(2)]
+
+    def step(k):
+        x = xs[k].clone().requires_grad_(True)
+        y = m(x)
+        return (y.detach(), *torch.autograd.grad(y, (x, *m.parameters()), dys[k]))
+
+    want = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(step(k))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for res in got[k]:
+            for a, b in zip(res, want[k]):
+                a, b = a.float(), b.float()
+                assert float((a - b).norm()) <= 2.0 ** -7 * float(b.norm()), k
