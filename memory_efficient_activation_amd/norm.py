@@ -25,7 +25,7 @@ import torch.nn as nn
 from . import _lib
 from ._autograd import first_order
 from .dense import EPS, SharedBuffer
-from .functional import _dtype_code, _require_device, _same
+from .functional import _DTYPES, _dtype_code, _require_device, _same
 
 # The current stream's handle by device index, and the current device,
 # without building objects for every call (0.1 us each against 2 and 0.5 of a
@@ -126,12 +126,13 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None,
 
 def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                    weight: torch.Tensor | None = None, need_params: bool = True,
-                   out: torch.Tensor | None = None, shared: SharedBuffer | None = None
+                   out: torch.Tensor | None = None, shared: SharedBuffer | None = None,
+                   param_dtype: torch.dtype | None = None
                    ) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor | None]:
     """(dx, dweight, dbias) from the input, the upstream gradient and the
     statistics the forward returned.  dweight and dbias have weight's dtype
-    (x's without a weight); None if ``need_params`` is False.  ``shared``
-    lends its workspace."""
+    (without a weight ``param_dtype``, or x's if that is None); None if
+    ``need_params`` is False.  ``shared`` lends its workspace."""
     code = _dtype_code(x)
     x, rows, n, ldx = as_rows(x, "x")
     dy, _, _, lddy = as_rows(dy, "dy")
@@ -143,13 +144,17 @@ def layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: 
             raise ValueError(f"{name} must be a contiguous float32 tensor of shape "
                              f"{tuple(lead)} on {device}")
     wp = _param(weight, n, x, "weight")
-    pcode = _param_code(weight, None, x)
+    if weight is not None and param_dtype not in (None, weight.dtype):
+        raise TypeError(f"weight is {weight.dtype}, param_dtype {param_dtype}")
+    pdtype = weight.dtype if weight is not None else param_dtype or x.dtype
+    if pdtype not in _DTYPES:
+        raise TypeError(f"param_dtype must be float32 or bfloat16, got {pdtype}")
+    pcode = _DTYPES[pdtype]
     dx, lddx = _out_rows(out, x, "out")
     dw = db = wsp = None
     nbytes = 0
     if need_params:
-        dw, db = torch.empty((2, n), dtype=x.dtype if weight is None else weight.dtype,
-                             device=device).unbind(0)
+        dw, db = torch.empty((2, n), dtype=pdtype, device=device).unbind(0)
         ws = (shared or SharedBuffer()).workspace(library().layer_norm_workspace_bytes(rows, n), device)
         wsp, nbytes = ws.data_ptr(), ws.numel()
     launch("layer_norm_bwd", "layer_norm_bwd", device, x.data_ptr(), ldx, dy.data_ptr(), lddy,
@@ -175,9 +180,9 @@ class LayerNormFn(torch.autograd.Function):
     def backward(ctx, dy):
         x, mean, rstd, weight = ctx.saved_tensors
         need_w, need_b = ctx.needs_input_grad[1:3]
-        dx, dw, db = layer_norm_bwd(x, dy, mean, rstd, weight, need_w or need_b,
-                                    shared=ctx.shared)
-        return (dx, dw if need_w else None, db.to(ctx.bias_dtype) if need_b else None, None, None)
+        dx, dw, db = layer_norm_bwd(x, dy, mean, rstd, weight, need_w or need_b, shared=ctx.shared,
+                                    param_dtype=ctx.bias_dtype if weight is None else None)
+        return dx, dw if need_w else None, db if need_b else None, None, None
 
 
 class LayerNorm(nn.Module):

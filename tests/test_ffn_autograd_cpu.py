@@ -14,7 +14,8 @@ def _norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None):
         return tuple(t.to(x.dtype) for t in o.norm_forward(x, weight, bias, eps)[0])
 
 
-def _norm_bwd(x, dy, mean, rstd, weight=None, need_params=True, out=None, shared=None):
+def _norm_bwd(x, dy, mean, rstd, weight=None, need_params=True, out=None, shared=None,
+              param_dtype=None):
     with torch.no_grad():
         dx, dw, db = (t.to(x.dtype) for t in o.norm_backward(x, dy, mean, rstd, weight)[0])
         return (dx, dw, db) if need_params else (dx, None, None)
