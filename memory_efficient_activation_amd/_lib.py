@@ -31,6 +31,7 @@ EXPORTED = ("swish_fwd", "swish_bwd", "swish_fwd_grouped", "swish_bwd_grouped",
 # The transformer feed-forward operators (include/layer_norm.h, include/gated_ffn.h).
 BLOCK_EXPORTED = ("layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
                   "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn_workspace_bytes")
+GATED_FFN_MAX_LD = 2097152
 DENSE_MAX_SOURCES = 64
 DENSE_STATIC_WORKSPACE_BYTES = 4 << 20
 

@@ -33,6 +33,15 @@ from .functional import _act_code, _dtype_code, _require_device
 from .norm import _out_rows, as_rows, launch, layer_norm_bwd, layer_norm_fwd, library
 
 
+def _rows(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
+    """t and the distance of its rows, copied where no one distance serves or
+    the library does not take it (one token of each long sequence, say)."""
+    t, _, n, ld = as_rows(t, name)
+    if ld > _lib.GATED_FFN_MAX_LD and ld > n:
+        t, ld = t.contiguous(), n
+    return t, ld
+
+
 def _weight(x: torch.Tensor, w: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
     """w and its row distance, checked against x."""
     if not w.is_cuda:
@@ -43,8 +52,7 @@ def _weight(x: torch.Tensor, w: torch.Tensor, name: str) -> tuple[torch.Tensor, 
         raise TypeError(f"x and {name} have different dtypes ({x.dtype}, {w.dtype})")
     if w.dim() != 2 or w.shape[1] != x.shape[-1]:
         raise ValueError(f"{name} must be [hidden, {x.shape[-1]}], got {tuple(w.shape)}")
-    w, _, _, ld = as_rows(w, name)
-    return w, ld
+    return _rows(w, name)
 
 
 def _weights(x, w_gate, w_up):
@@ -91,7 +99,8 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, kin
     workspace."""
     act = _act_code(kind)
     code = _dtype_code(x)
-    x, _, dim, ldx = as_rows(x, "x")
+    x, ldx = _rows(x, "x")
+    dim = x.shape[-1]
     (wg, ldg), (wu, ldu) = _weights(x, w_gate, w_up)
     tokens, hidden = _tokens(x), w_gate.shape[0]
     shape = (*x.shape[:-1], hidden)
@@ -101,6 +110,9 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, kin
         if out.shape != shape or out.dtype != x.dtype or out.device != x.device:
             raise ValueError(f"out must be a {x.dtype} tensor of shape {shape} on {x.device}")
         h, ldh = _out_rows(out, out, "out")
+        if ldh > _lib.GATED_FFN_MAX_LD and ldh > hidden:
+            raise ValueError(f"the rows of out are {ldh} elements apart, more than "
+                             f"{_lib.GATED_FFN_MAX_LD}")
     device = x.device
     ws, nbytes = _workspace(tokens, dim, hidden, code, 0,
                             _aligned(x, ldx, wg, ldg, wu, ldu, dim), device, shared)
@@ -121,13 +133,14 @@ def gated_ffn_bwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, dh:
     code = _dtype_code(x)
     if not dh.is_cuda:
         _require_device(dh, "dh")
-    x, _, dim, ldx = as_rows(x, "x")
+    x, ldx = _rows(x, "x")
+    dim = x.shape[-1]
     (wg, ldg), (wu, ldu) = _weights(x, w_gate, w_up)
     tokens, hidden = _tokens(x), w_gate.shape[0]
     if dh.shape != (*x.shape[:-1], hidden) or dh.dtype != x.dtype or dh.device != x.device:
         raise ValueError(f"dh must be a {x.dtype} tensor of shape {(*x.shape[:-1], hidden)} on "
                          f"{x.device}")
-    dh, _, _, lddh = as_rows(dh, "dh")
+    dh, lddh = _rows(dh, "dh")
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_x else None
     dwg = dwu = None
     if need_weights:
