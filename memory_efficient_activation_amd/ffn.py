@@ -212,15 +212,27 @@ class PreNormGatedFFNFn(torch.autograd.Function):
     @first_order
     def backward(ctx, dy):
         x, mean, rstd, weight, bias, w_gate, w_up, w_down = ctx.saved_tensors
+        need = ctx.needs_input_grad  # x, weight, bias, w_gate, w_up, w_down, ...
+        need_norm, need_unit = any(need[:3]), need[3] or need[4]
         dy = dy.contiguous()
         dy2 = dy.view(-1, dy.shape[-1])
         n = layer_norm_fwd(x, weight, bias, ctx.eps)[0]
-        dh = (dy2 @ w_down).view(*x.shape[:-1], w_down.shape[1])
-        dn, dwg, dwu, h = gated_ffn_bwd(n, w_gate, w_up, dh, ctx.kind, ctx.param, need_h=True,
+        dx = dw = db = dwg = dwu = dwd = h = None
+        if need_norm or need_unit:
+            dh = (dy2 @ w_down).view(*x.shape[:-1], w_down.shape[1])
+            dn, dwg, dwu, *rest = gated_ffn_bwd(n, w_gate, w_up, dh, ctx.kind, ctx.param, need_norm,
+                                                need_unit, need[5], shared=ctx.shared)
+            h = rest[0] if need[5] else None
+        elif need[5]:
+            h = gated_ffn_fwd(n, w_gate, w_up, ctx.kind, ctx.param, shared=ctx.shared)
+        if need[5]:
+            dwd = dy2.t() @ h.view(-1, h.shape[-1])
+        if need_norm:
+            dx, dw, db = layer_norm_bwd(x, dn, mean, rstd, weight, need[1] or need[2],
                                         shared=ctx.shared)
-        dwd = dy2.t() @ h.view(-1, h.shape[-1])
-        dx, dw, db = layer_norm_bwd(x, dn, mean, rstd, weight, shared=ctx.shared)
-        return dx.add_(dy), dw, db, dwg, dwu, dwd, None, None, None, None
+            dx = dx.add_(dy) if need[0] else None
+        grads = (dx, dw, db, dwg, dwu, dwd)
+        return (*(g if wanted else None for g, wanted in zip(grads, need)), None, None, None, None)
 
 
 class PreNormGatedFeedForward(nn.Module):

@@ -96,3 +96,42 @@ def test_a_block_shares_memory_only_when_asked():
     assert ffn.PreNormGatedFeedForward(16, 24).shared is None
     assert ffn.GatedUnit(16, 24).shared is None and norm.LayerNorm(16).shared is None
     assert ffn.PreNormGatedFeedForward(16, 24, shared=shared).shared is shared
+
+
+PARTS = ("x", "weight", "bias", "w_gate", "w_up", "w_down")
+
+
+@pytest.mark.parametrize("wanted", [("x",), ("w_down",), ("w_gate",), ("w_up", "w_down"), ("bias",),
+                                    ("weight", "w_up"), ("x", "w_down"), PARTS], ids="-".join)
+def test_the_block_computes_what_is_wanted(formulas, monkeypatch, wanted):
+    """With part of it frozen the block's other gradients are the same, and
+    what only frozen parts need is not computed."""
+    m = modules()["PreNormGatedFeedForward"]
+    x = torch.randn(5, 16)
+    dy = torch.randn(5, 16)
+    tensors = dict(m.named_parameters(), x=x)
+    x.requires_grad_(True)
+    want = dict(zip(PARTS, torch.autograd.grad(m(x), [tensors[k] for k in PARTS], dy)))
+    for k in PARTS:
+        tensors[k].requires_grad_(k in wanted)
+    asked = []
+
+    def unit_bwd(x, wg, wu, dh, kind, param, need_x=True, need_weights=True, need_h=False,
+                 shared=None):
+        asked.append((need_x, need_weights, need_h))
+        return _unit_bwd(x, wg, wu, dh, kind, param, need_x, need_weights, need_h)
+
+    def norm_bwd(x, dy, mean, rstd, weight=None, need_params=True, out=None, shared=None):
+        asked.append(need_params)
+        return _norm_bwd(x, dy, mean, rstd, weight, need_params)
+
+    monkeypatch.setattr(ffn, "gated_ffn_bwd", unit_bwd)
+    monkeypatch.setattr(ffn, "layer_norm_bwd", norm_bwd)
+    got = torch.autograd.grad(m(x), [tensors[k] for k in wanted], dy)
+    for k, g in zip(wanted, got):
+        assert torch.equal(g, want[k]), k
+    wanted = set(wanted)
+    need_norm = bool(wanted & {"x", "weight", "bias"})
+    need_unit = bool(wanted & {"w_gate", "w_up"})
+    expect = [(need_norm, need_unit, "w_down" in wanted)] if need_norm or need_unit else []
+    assert asked == expect + ([bool(wanted & {"weight", "bias"})] if need_norm else [])

@@ -24,3 +24,18 @@ def test_second_derivatives_raise(make):
             assert torch.equal(a, b)
         with pytest.raises(RuntimeError, match="cannot be differentiated again"):
             (graph[0].pow(2).sum() + x.pow(3).sum()).backward()
+
+
+@pytest.mark.parametrize("wanted", [("x",), ("w_down",), ("w_gate", "bias"), ("x", "w_down")],
+                         ids="-".join)
+def test_block_with_frozen_parts(wanted):
+    torch.manual_seed(5)
+    m = ffn.PreNormGatedFeedForward(72, 200, "gelu", dtype=torch.bfloat16).to(DEV)
+    x = torch.randn(3, 50, 72, device=DEV).bfloat16().requires_grad_(True)
+    dy = torch.randn(3, 50, 72, device=DEV).bfloat16()
+    tensors = dict(m.named_parameters(), x=x)
+    want = dict(zip(tensors, torch.autograd.grad(m(x), list(tensors.values()), dy)))
+    for k, t in tensors.items():
+        t.requires_grad_(k in wanted)
+    for k, g in zip(wanted, torch.autograd.grad(m(x), [tensors[k] for k in wanted], dy)):
+        assert torch.equal(g, want[k]), k
