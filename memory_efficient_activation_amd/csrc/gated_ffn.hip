@@ -555,6 +555,22 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t offset, i32x4 
                  : "memory", "m0");
 }
 
+// The scalar registers of a descriptor may come from vector instructions, which
+// a buffer load may read five issue slots later at the earliest; the compiler
+// does not see into the assembly above.  (In the loop a row of products lies
+// between.)
+__device__ __forceinline__ void settle_descriptors()
+{
+    asm volatile("s_nop 4" : : : "memory");
+}
+
+// The block's barrier, over which no access to LDS moves.
+__device__ __forceinline__ void meet()
+{
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void wait_loads()
 {
@@ -808,12 +824,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         next_step();
+        settle_descriptors();
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             issue(s * kStage, i);
     }
     wait_loads<kLoads>();
-    __builtin_amdgcn_s_barrier();
+    meet();
     // Step s: its first fragments are in registers.  Its last reads are issued
     // before its last part; a row of products into that part (BG), the barrier
     // behind which step s + 1 is in LDS and the place of step s is free for
@@ -856,7 +873,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
                         __builtin_amdgcn_sched_barrier(0);
                         wait_loads<0>();
                         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-                        __builtin_amdgcn_s_barrier();
+                        meet();
                         __builtin_amdgcn_sched_barrier(0);
                     }
                     // The next part's fragments: Q's row i behind its products
