@@ -23,6 +23,9 @@
  * launched on an error.
  *   - dtype: MESWISH_F32 or MESWISH_BF16 for every matrix of a call.
  *     Products accumulate in binary32; g and u stay binary32 through f.
+ *     f and f' are evaluated on them to 1e-5 in binary32 calls, and to 2^-14
+ *     in bfloat16 calls (the activations' shorter paths; the rounding of the
+ *     result is 2^-9 to 2^-8 of it).
  *     bfloat16 calls round dg and du to bfloat16 for the products that use
  *     them (the matrix cores' operand type).  Every output is rounded once,
  *     to nearest even.

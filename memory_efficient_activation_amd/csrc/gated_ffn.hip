@@ -70,7 +70,9 @@ struct GemmArgs {
 };
 
 // ---------------------------------------------------------------------------
-// The activation and the product, on binary32 g and u.
+// The activation and the product, on binary32 g and u.  P (precise): binary32
+// calls; bfloat16 calls take the activations' shorter paths (2^-14 of f and f',
+// against 2^-9 and more of the result's rounding).
 // ---------------------------------------------------------------------------
 template <class Op, bool P>
 __device__ __forceinline__ float act_value(float x, const Coef& k)
