@@ -1228,14 +1228,15 @@ static int gemm_launch(GemmArgs<T>& a, const void* fn, int bm, int bn, int block
     const int cols = MODE == kUp ? bn / 2 : bn;
     a.tiles_m = (a.q.rows + bm - 1) / bm;
     a.tiles_n = (a.out_cols + cols - 1) / cols;
-    const int64_t grid = (int64_t)a.tiles_m * a.tiles_n * (MODE == kDw ? 2 : 1);
-    if (grid == 0)
+    // The kernel counts tiles in 31 bits; a launch has fewer than 2^32 threads.
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n * (MODE == kDw ? 2 : 1);
+    if (tiles == 0)
         return MESWISH_OK;
-    if (grid >= ((int64_t)1 << 23))
+    const int64_t grid = resident && tiles > resident ? resident : tiles;
+    if (tiles > ((int64_t)1 << 30) || grid >= ((int64_t)1 << 23))
         return MESWISH_EINVAL;
     void* args[] = {&a};
-    int rc = launch(fn, dim3((unsigned)(resident && grid > resident ? resident : grid), a.splits),
-                    block, args, stream);
+    int rc = launch(fn, dim3((unsigned)grid, a.splits), block, args, stream);
     if (rc != MESWISH_OK || a.splits == 1)
         return rc;
     if constexpr (MODE == kUp)
