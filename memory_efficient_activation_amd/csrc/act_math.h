@@ -63,7 +63,7 @@ enum ActKind {
     kSwishUnit = 8
 };
 
-// Coefficients prepared on the host (make_coef below).
+// Coefficients prepared on the host (make_coef in meswish.hip).
 struct Coef {
     float p;       // alpha (Swish) or negative slope (LeakyReLU); unused otherwise
     float c_hi;    // binary32 nearest to the exponent coefficient C (per activation)
@@ -72,55 +72,6 @@ struct Coef {
     float aux_lo;  // GELU_tanh: 0.044715 - aux_hi
 };
 
-// ---------------------------------------------------------------------------
-// Host.
-// ---------------------------------------------------------------------------
-// Per-activation coefficients, in binary64 and split.
-inline Coef make_coef(int act, float p)
-{
-    const double log2e = 1.44269504088896340735992468100189214;
-    const double sqrt_2_over_pi = 0.797884560802865355879892119868763737;
-    double c = 0.0;
-    switch (act) {
-    case kSwish:
-        c = -(double)p * log2e;  // e^-(p x)
-        break;
-    case kSigmoid:
-        c = -log2e;  // e^-x
-        break;
-    case kTanh:
-        c = -2.0 * log2e;  // e^-2|x|
-        break;
-    case kGeluErf:
-        c = -0.5 * log2e;  // e^-(x^2 / 2)
-        break;
-    case kGeluTanh:
-        c = -2.0 * sqrt_2_over_pi * log2e;  // e^-2u over x (1 + 0.044715 x^2)
-        break;
-    default:
-        break;
-    }
-    const double cubic = 0.044715;
-    Coef k;
-    k.p = p;
-    k.c_hi = (float)c;
-    k.c_lo = (float)(c - (double)k.c_hi);
-    k.aux_hi = (float)cubic;
-    k.aux_lo = (float)(cubic - (double)k.aux_hi);
-    return k;
-}
-
-// Swish's exponent coefficient -alpha log2 e must be a finite binary32
-// value (|alpha| <= about 2.36e38); beyond that the kernels' e^-t = 2^(x C)
-// would take C = -inf.
-inline bool swish_alpha_ok(float alpha)
-{
-    return isfinite(make_coef(kSwish, alpha).c_hi);
-}
-
-// ---------------------------------------------------------------------------
-// Device.
-// ---------------------------------------------------------------------------
 constexpr float kLn2f = 0.693147180559945309f;
 // |base-2 exponent| beyond which 2^v leaves [2^-125, 2^125].
 constexpr float kMaxExp = 125.0f;

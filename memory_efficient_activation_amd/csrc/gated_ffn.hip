@@ -1109,11 +1109,47 @@ __global__ __launch_bounds__(256) void gate_parts_kernel(const GemmArgs<T> a)
 // Host.
 // ---------------------------------------------------------------------------
 
+// Coefficients of the activation, in binary64 and split (see Coef).
+static Coef make_coef(int act, float p)
+{
+    const double log2e = 1.44269504088896340735992468100189214;
+    const double sqrt_2_over_pi = 0.797884560802865355879892119868763737;
+    double c = 0.0;
+    switch (act) {
+    case MESWISH_ACT_SWISH:
+        c = -(double)p * log2e;
+        break;
+    case MESWISH_ACT_SIGMOID:
+        c = -log2e;
+        break;
+    case MESWISH_ACT_TANH:
+        c = -2.0 * log2e;
+        break;
+    case MESWISH_ACT_GELU_ERF:
+        c = -0.5 * log2e;
+        break;
+    case MESWISH_ACT_GELU_TANH:
+        c = -2.0 * sqrt_2_over_pi * log2e;
+        break;
+    default:
+        break;
+    }
+    const double cubic = 0.044715;
+    Coef k;
+    k.p = p;
+    k.c_hi = (float)c;
+    k.c_lo = (float)(c - (double)k.c_hi);
+    k.aux_hi = (float)cubic;
+    k.aux_lo = (float)(cubic - (double)k.aux_hi);
+    return k;
+}
+
 static bool act_ok(int act, float param)
 {
     if (act < MESWISH_ACT_SWISH || act > MESWISH_ACT_GELU_TANH || !isfinite(param))
         return false;
-    return act != MESWISH_ACT_SWISH || meswish::swish_alpha_ok(param);
+    // Swish's exponent coefficient must be a finite binary32 value.
+    return act != MESWISH_ACT_SWISH || isfinite(make_coef(act, param).c_hi);
 }
 
 constexpr size_t kMaxTokens = (size_t)1 << 30;
@@ -1416,7 +1452,7 @@ static int run(const Call& c)
     a.q = operand<T>(up.x, up.ldx, up.x, up.ldx, c.tokens);
     a.k = up.dim;
     a.act = c.act;
-    a.coef = meswish::make_coef(c.act, c.param);
+    a.coef = make_coef(c.act, c.param);
     if constexpr (!BWD) {
         a.out[0] = static_cast<T*>(c.h);
         a.ldo[0] = c.ldh;

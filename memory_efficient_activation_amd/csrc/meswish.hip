@@ -588,6 +588,41 @@ static int64_t head_elems(const void* p, size_t esize)
     return mis ? (int64_t)((16u - mis) / esize) : 0;
 }
 
+// Per-activation coefficients (see Coef in act_math.h).
+static Coef make_coef(int act, float p)
+{
+    const double log2e = 1.44269504088896340735992468100189214;
+    const double sqrt_2_over_pi = 0.797884560802865355879892119868763737;
+    double c = 0.0;
+    switch (act) {
+    case kSwish:
+        c = -(double)p * log2e;  // e^-(p x)
+        break;
+    case kSigmoid:
+        c = -log2e;  // e^-x
+        break;
+    case kTanh:
+        c = -2.0 * log2e;  // e^-2|x|
+        break;
+    case kGeluErf:
+        c = -0.5 * log2e;  // e^-(x^2 / 2)
+        break;
+    case kGeluTanh:
+        c = -2.0 * sqrt_2_over_pi * log2e;  // e^-2u over x (1 + 0.044715 x^2)
+        break;
+    default:
+        break;
+    }
+    const double cubic = 0.044715;
+    Coef k;
+    k.p = p;
+    k.c_hi = (float)c;
+    k.c_lo = (float)(c - (double)k.c_hi);
+    k.aux_hi = (float)cubic;
+    k.aux_lo = (float)(cubic - (double)k.aux_hi);
+    return k;
+}
+
 // How one tensor is split between the kernels' paths (see meswish_plan_t).
 template <typename IO, bool kBwd, typename SH = Shape<IO, kBwd>>
 static meswish_plan_t make_plan(const void* x, const void* dy, const void* out, size_t n)
@@ -750,9 +785,13 @@ static int check_common(float alpha, int dtype)
     return MESWISH_OK;
 }
 
+// Swish's exponent coefficient -alpha log2 e must be a finite binary32
+// value (|alpha| <= about 2.36e38); beyond that the kernels' e^-t = 2^(x C)
+// would take C = -inf.
 static int check_swish_alpha(float alpha)
 {
-    return swish_alpha_ok(alpha) ? MESWISH_OK : MESWISH_EINVAL;
+    const double c = -(double)alpha * 1.44269504088896340735992468100189214;
+    return isfinite((float)c) ? MESWISH_OK : MESWISH_EINVAL;
 }
 
 static int check_tensor(const void* p, size_t n, size_t esize)
