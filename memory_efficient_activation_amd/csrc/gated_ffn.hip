@@ -1109,7 +1109,9 @@ __global__ __launch_bounds__(256) void gate_parts_kernel(const GemmArgs<T> a)
 // Host.
 // ---------------------------------------------------------------------------
 
-// Coefficients of the activation, in binary64 and split (see Coef).
+// Coefficients of the activation, in binary64 and split (see Coef): the table of
+// meswish.hip, whose counter summaries hold for its exact text (a test compares the
+// two).
 static Coef make_coef(int act, float p)
 {
     const double log2e = 1.44269504088896340735992468100189214;
