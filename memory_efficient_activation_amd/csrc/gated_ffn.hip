@@ -13,6 +13,11 @@
 //   kDw  dWg, dWu:  P = x (n contiguous), Q = dg, du (m contiguous),
 //        k = tokens.
 //
+// dg and du are written in the tensors' type, also where that is bfloat16: they
+// are the next products' operands, which the matrix cores take in that type
+// (errors of the bf16 gradients against binary64 0.0023 to 0.0024 of their norm,
+// 0.0017 from the results' own rounding alone).
+//
 // The matrix cores (v_mfma_f32_16x16x32_bf16, v_mfma_f32_16x16x4_f32) take
 // P as the operand whose rows index the four consecutive results a lane
 // holds, so a lane's results are consecutive along n.
@@ -408,6 +413,13 @@ struct Gate {
     }
 };
 
+// The whole wave again, four results of a lane at a time and element by element:
+// for the activations' rare arguments (GELU below -6, tanh-GELU past |g| = 4.5 in
+// binary32 and 10 in bf16; Swish and sigmoid past 86).  What it costs: with g ~ N(0, 1) next to nothing; with
+// g ~ N(0, 3^2) nearly every wave comes here (bf16 16384 x 4096 -> 16384, GELU:
+// forward 3.18 to 3.97 ms, recomputation 3.66 to 6.66; tanh-GELU 3.17 to 3.98, 3.49
+// to 6.82; binary32 8192 x 2048 -> 4096 tanh-GELU 1.91 to 2.01 and 2.03 to 2.44).
+// Swish takes no more there than at N(0, 1).
 template <class Op, typename T, bool BWD, int MT, int NT>
 __device__ __forceinline__ void gate_slow(const GemmArgs<T>& a, int64_t m0, int n0,
                                           const f32x4 (&acc)[MT][NT])
@@ -517,7 +529,7 @@ __device__ __forceinline__ void part_of_sum(int splits, int& first, int& total)
 // one arrives.
 //
 // What bounds it, and why this shape (bf16, 16384 x 4096 -> 16384: forward
-// 1400 TFLOP/s, recomputation 1290, dx 1310, dWg and dWu 1270; binary32 8192 x
+// 1400 TFLOP/s, recomputation 1250, dx 1320, dWg and dWu 1270; binary32 8192 x
 // 2048 -> 4096: 147 of the 157 its matrix instructions have).  The matrix
 // cores are busy 71 % of the cycles and the card lowers its clock (1.75 GHz)
 // under the load: on zeros, which cost little power, the forward reaches 1580.
@@ -529,6 +541,10 @@ __device__ __forceinline__ void part_of_sum(int splits, int& first, int& total)
 // tiles in LDS, 1210 (twice the barriers, half lines fetched twice); loads
 // spread over the next step, 1305 against 1346; lines of later steps touched
 // into the L2 beforehand, 1490 to 1650 on zeros but 1217 to 1185 on numbers.
+//
+// The recomputation's 256 x 256 kernels have no register left (256 of 256): the
+// binary32 one spills 60 (52 bytes of scratch), the bf16 one 2, all outside the
+// products' loop, around the epilogue.
 //
 // A load writes 1 KiB of LDS in lane order, so the layouts that avoid bank
 // conflicts are made by choosing which 16 bytes each lane fetches:
@@ -918,7 +934,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void gemm_fast_kernel(const GemmAr
 // straight into registers (16 bytes a lane at element alignment, U steps in
 // flight) with x's fragments beside them (from the caches), and add their
 // parts through LDS in the order of the wave.  bf16 4096 -> 16384 (268 MB of
-// weights): 1 token 43 us, 24 tokens 50 (6.2 and 5.4 TB/s).
+// weights): 1 token 49 us, 24 tokens 56 (5.5 and 4.8 TB/s) where the weights come
+// from memory; 43 and 51 called again on the same weights, of which the 256 MB
+// Infinity Cache then holds most.
 // ---------------------------------------------------------------------------
 template <typename T, bool BWD, int PT, int QT, int NW>
 __global__ __launch_bounds__(NW * 64) void few_tokens_kernel(const GemmArgs<T> a)
@@ -1235,7 +1253,7 @@ static size_t part_bytes(int mode, int64_t rows, int64_t cols, int64_t k, size_t
 }
 
 // Most tokens of the kernel that reads the weights once.  bf16 4096 -> 16384,
-// against 128 x 128 tiles: 1 token 43 us and 53, 24 tokens 50 and 57, 48 tokens
+// called again on the same weights, against 128 x 128 tiles: 1 token 43 us and 53, 24 tokens 50 and 57, 48 tokens
 // 58.4 and 58.0, 64 tokens 63.5 and 58.5.  Up to 16 tokens a block has 16 hidden
 // units; for more it has 32, so that x's fragments serve twice (24 tokens: 50 us
 // against 56 with 16).

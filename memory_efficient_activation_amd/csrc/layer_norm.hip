@@ -32,9 +32,13 @@
 
 namespace meblock {
 
-// Most blocks of the backward, each with its own partial sums
-// (512: two of 256 threads on a CU.  Measured, bf16 16384 x 4096 backward: 384
-// blocks 102 us, 512 92, 768 95, 1024 115: more of them write more parts.)
+// Most blocks of the backward, each with its own partial sums.  Chosen at width
+// 4096 (bf16 16384 x 4096: 384 blocks 102 us, 512 92, 768 95, 1024 115: more of
+// them write more parts), where a CU holds two blocks of 256 threads.  Wider rows
+// have the same number: in bf16 the registers leave one block a CU there (up to
+// 8192 values all 256 of them and 10 more as spill space; up to 16384 values 128 in
+// blocks of 1024 threads, with 40 to 44 bytes of scratch), so that 512 blocks run
+// in two rounds, and the partial sums are 34 and 67 MB.
 constexpr int kMaxParts = 512;
 // Most blocks of the forward, each keeping its columns of the parameters in
 // registers: eight of 256 threads on a CU (bf16 16384 x 4096: 2048 blocks 47 us,
@@ -680,7 +684,7 @@ static int bwd_launch(LnArgs<T, P>& a)
 //   n = 1024         64 x 2, 1 row: 75             32 x 4, 1 row: 81
 //   n = 2048         256 x 1, 2 rows: 79           128 x 2, 2 rows: 82
 //   n = 4096         256 x 2, 2 rows: 86           512 x 1, 2 rows: 86
-//   n = 8192         256 x 4, 1 row: 100           512 x 2, 2 rows: 101
+//   n = 8192         256 x 4, 1 row: 97            512 x 2, 2 rows: 101
 //   n = 16384        1024 x 2, 1 row: 127          512 x 4, 1 row: 129
 template <typename T, typename P>
 static int bwd_run(LnArgs<T, P>& a)
