@@ -1,6 +1,6 @@
 """ctypes loader for libmeswish.so (the C ABI declared in include/meswish.h,
-include/dense_bn.h, include/fft_conv.h, include/layer_norm.h and
-include/gated_ffn.h).
+include/dense_bn.h, include/fft_conv.h, include/layer_norm.h,
+include/gated_ffn.h and include/linear.h).
 
 Argument marshalling only: every element of every pass is computed by the
 HIP kernels inside the library.  There is no CPU fallback -- if the library
@@ -32,6 +32,11 @@ EXPORTED = ("swish_fwd", "swish_bwd", "swish_fwd_grouped", "swish_bwd_grouped",
 BLOCK_EXPORTED = ("layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
                   "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn_workspace_bytes")
 GATED_FFN_MAX_LD = 2097152
+# What finishes a transformer block (include/linear.h).
+FINISH_EXPORTED = ("linear_fwd", "linear_bwd", "linear_workspace_bytes")
+LINEAR_MAX_LD = 2097152
+LINEAR_IDENTITY = -1
+LINEAR_ALIGNED_XW, LINEAR_ALIGNED_DY = 1, 2
 DENSE_MAX_SOURCES = 64
 DENSE_STATIC_WORKSPACE_BYTES = 4 << 20
 
@@ -118,10 +123,21 @@ def _block_signatures() -> dict:
     }
 
 
+def _finish_signatures() -> dict:
+    """Argument and result types of the operators that finish a block."""
+    vp, sz, f, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float, ctypes.c_int
+    return {
+        "linear_workspace_bytes": ([sz, sz, sz, i, i, i, i], sz),
+        "linear_fwd": ([i, f, vp, sz, vp, sz, vp, vp, sz, sz, sz, sz, vp, sz, vp, sz, i, vp], i),
+        "linear_bwd": ([i, f, vp, sz, vp, sz, vp, vp, sz, sz, sz, sz, vp, sz, vp, sz, vp, vp, sz,
+                        i, vp], i),
+    }
+
+
 def _declare(lib: ctypes.CDLL, names=None) -> ctypes.CDLL:
     """Set argtypes/restype of ``names`` (every exported function by default);
     a missing symbol raises AttributeError."""
-    sig = {**_signatures(), **_block_signatures()}
+    sig = {**_signatures(), **_block_signatures(), **_finish_signatures()}
     for name in (sig if names is None else names):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = sig[name]

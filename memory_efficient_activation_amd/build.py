@@ -4,11 +4,14 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("meswish.hip", "dense_bn.hip", "fft_conv.hip",
-                                                "layer_norm.hip", "gated_ffn.hip")]
+                                                "layer_norm.hip", "gated_ffn.hip",
+                                                "linear.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libmeswish.so")
 
@@ -42,11 +45,21 @@ SPLIT_TEST_NAMES = ("swish_fwd", "swish_bwd", "swish_fwd_grouped", "swish_bwd_gr
 
 def build(output: str = LIBRARY, extra_flags: list[str] | None = None,
           sources: list[str] | None = None) -> str:
-    """Compile libmeswish.so (always recompiles) and return its path."""
+    """Compile libmeswish.so (always recompiles, the sources side by side) and
+    return its path."""
+    sources = sources or SOURCES
     tmp = output + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *(extra_flags or []), f"-I{INCLUDE}", *(sources or SOURCES),
-           "-o", tmp]
-    subprocess.run(cmd, check=True)
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"] + (extra_flags or [])
+    with tempfile.TemporaryDirectory() as scratch:
+        objects = [os.path.join(scratch, f"{i}.o") for i in range(len(sources))]
+
+        def compile_one(job):
+            source, out = job
+            subprocess.run([hipcc(), *flags, f"-I{INCLUDE}", "-c", source, "-o", out], check=True)
+
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(compile_one, zip(sources, objects)))
+        subprocess.run([hipcc(), *HIPCC_FLAGS, *objects, "-o", tmp], check=True)
     os.replace(tmp, output)
     return output
 

@@ -273,6 +273,20 @@ inline bool same_or_apart(const Span& out, const Span& in)
            !overlaps(out, in);
 }
 
+// No output touches an input or another output.
+inline int apart(const Span* out, int nout, const Span* in, int nin)
+{
+    for (int o = 0; o < nout; ++o) {
+        for (int i = 0; i < nin; ++i)
+            if (overlaps(out[o], in[i]))
+                return MESWISH_EALIAS;
+        for (int i = 0; i < o; ++i)
+            if (overlaps(out[o], out[i]))
+                return MESWISH_EALIAS;
+    }
+    return MESWISH_OK;
+}
+
 inline int launch(const void* fn, dim3 grid, int block, void** args, hipStream_t stream)
 {
     return hipLaunchKernel(fn, grid, dim3(block), args, 0, stream) == hipSuccess ? MESWISH_OK

@@ -1,0 +1,744 @@
+// linear.hip -- the matrix product with bias, activation and residual in its
+// epilogue, for gfx950, forward and backward.  Formulas and contracts:
+// include/linear.h.
+//
+// The products (products.h), out[m][n] = sum_k Q(m, k) P(n, k):
+//
+//   kLin    z:   P = W (k contiguous), Q = x (k contiguous), k = dim.  The
+//        epilogue works on z in the accumulators: y, or dz, is all that is
+//        written.
+//   kLinDx  dx:  P = W (n contiguous), Q = dz (k contiguous), k = units.
+//   kLinDw  dW:  P = x (n contiguous), Q = dz (m contiguous), k = tokens.
+//
+// dz is written in the tensors' type, also where that is bfloat16: it is the
+// next products' operand, which the matrix cores take in that type.  Without an
+// activation dz is dy, read where it is.
+
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+#include <utility>
+
+#include "act_coef.h"
+#include "linear.h"
+#include "products.h"
+
+namespace meblock {
+
+namespace {
+
+template <typename T>
+struct LinArgs : Product<T> {  // out: y, or dz (columns padded, zeros past p.rows); dx; dW
+    const T* bias;  // kLin: or NULL
+    const T* r;     // kLin: the residual or NULL; backward: dy
+    int64_t ldr;
+    int act;
+    Coef coef;
+};
+
+struct IdentityOp {
+    static constexpr bool kHasRare = false;
+    template <bool P>
+    __device__ static constexpr float rare_thr() { return 1.0f; }
+    template <bool BWD, bool P>
+    __device__ static bool is_rare(float, const Coef&) { return false; }
+    template <bool P>
+    __device__ static float fwd(float x, const Coef&, float&) { return x; }
+    template <bool P>
+    __device__ static float bwd(float, float dy, const Coef&, float&) { return dy; }
+    __device__ static float fwd_rare(float x, const Coef&) { return x; }
+    __device__ static float bwd_rare(float, float dy, const Coef&) { return dy; }
+};
+
+// Calls f with the call's activation.
+template <class F>
+__device__ __forceinline__ void with_act(int act, const F& f)
+{
+    using namespace meswish;
+    switch (act) {
+    case kSwish:
+        return f(ActOp<kSwish>());
+    case kRelu:
+        return f(ActOp<kRelu>());
+    case kLeakyRelu:
+        return f(ActOp<kLeakyRelu>());
+    case kSigmoid:
+        return f(ActOp<kSigmoid>());
+    case kTanh:
+        return f(ActOp<kTanh>());
+    case kGeluErf:
+        return f(ActOp<kGeluErf>());
+    case kGeluTanh:
+        return f(ActOp<kGeluTanh>());
+    default:
+        return f(IdentityOp());
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Epilogue of kLin.
+// ---------------------------------------------------------------------------
+
+// One element of y or dz, written where it belongs: exactly (with the rare
+// branches).  c is below a.out_cols.
+template <typename T, bool BWD>
+__device__ __forceinline__ void lin_one(const LinArgs<T>& a, int64_t m, int c, float z)
+{
+    constexpr bool P = sizeof(T) == 4;
+    T* out = a.out[0] + m * a.ldo[0] + c;
+    if (c >= a.p.rows) {
+        if constexpr (BWD)  // the workspace's rows are padded: zeros past the last unit
+            *out = Elem<T>::put(0.0f);
+        return;
+    }
+    if (a.bias)
+        z += Elem<T>::get(a.bias[c]);
+    const float r = BWD || a.r ? Elem<T>::get(a.r[m * a.ldr + c]) : 0.0f;
+    with_act(a.act, [&](auto op) {
+        using Op = decltype(op);
+        z = BWD ? act_slope<Op, P>(z, r, a.coef) : act_value<Op, P>(z, a.coef);
+    });
+    *out = Elem<T>::put(BWD ? z : z + r);
+}
+
+// Eight values of the bias, zeros past its end and where there is none.
+template <typename T>
+__device__ __forceinline__ void load_bias(const T* bias, int c, int n, float* f)
+{
+    Eight<T> v;
+#pragma unroll
+    for (int k = 0; k < Eight<T>::V; ++k)
+        v.v[k] = u32x4{0, 0, 0, 0};
+    if (bias && c + 8 <= n)
+        v.load(bias + c);
+    v.values(f);
+    if (bias && c + 8 > n)
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (c + e < n)
+                f[e] = Elem<T>::get(bias[c + e]);
+}
+
+// f(0), f(1), ... f(N - 1), the numbers known to the compiler: a loop that it
+// unrolls however long its body is (accumulators in a loop that it does not
+// unroll go to scratch memory).
+template <class F, int... I>
+__device__ __forceinline__ void each(const F& f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// A wave's results on vectors of eight, without the activations' rare branches.
+// True in a lane that met one: the wave is then done again by lin_slow, to the
+// same places (which is why y may not be the residual).  The activation is chosen
+// anew for every vector: eight copies of what loads and stores around it took
+// more registers than there are.
+template <typename T, bool BWD, int MT, int NT>
+__device__ __forceinline__ bool lin_fast(const LinArgs<T>& a, int64_t m0, int n0,
+                                         const f32x4 (&acc)[MT][NT])
+{
+    constexpr bool P = sizeof(T) == 4;
+    constexpr int MH = MT < 16 / (int)sizeof(T) ? MT : 16 / (int)sizeof(T);  // rows of dy or r in flight
+    const int l = late_lane();
+    bool rare = false;
+    each([&](auto group) {
+        constexpr int b = decltype(group)::value;
+        const int c = n0 + 32 * b + 8 * (l / 16), left = a.p.rows - c;
+        int64_t row = m0 + l % 16;
+        T* out = a.out[0] + row * a.ldo[0] + c;
+        float bias[8];
+        load_bias(a.bias, c, a.p.rows, bias);
+each([&](auto part) {
+            constexpr int i0 = decltype(part)::value * MH;
+            Beside<T, MH, 1> d;
+            if (BWD || a.r)
+                d.load(a.r, a.ldr, a.q.rows, a.p.rows, m0 + 16 * i0, n0 + 32 * b);
+#pragma unroll
+            for (int t = 0; t < MH; ++t) {
+                float o[8], up[8];
+                if (BWD || a.r) {
+                    d.v[t].values(up);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        up[e] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    o[e] = acc[i0 + t][2 * b + e / 4][e % 4] + bias[e];
+                with_act(a.act, [&](auto op) {
+                    using Op = decltype(op);
+                    float key = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[e] = BWD ? Op::template bwd<P>(o[e], up[e], a.coef, key)
+                                   : Op::template fwd<P>(o[e], a.coef, key);
+                    if (Op::kHasRare)
+                        rare |= key > Op::template rare_thr<P>();
+                });
+                if constexpr (!BWD)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[e] += up[e];
+                if (row < a.q.rows && c < a.out_cols) {
+                    if constexpr (BWD) {
+                        // The workspace's rows are padded: zeros past the last unit.
+                        if (left < 8)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = e < left ? o[e] : 0.0f;
+                        Eight<T>::store(out, o);
+                    } else {
+                        store_some8(out, o, left);
+                    }
+                }
+                row += 16;
+                out += 16 * a.ldo[0];
+                __builtin_amdgcn_sched_barrier(0);  // few results at a time
+            }
+        }, std::make_integer_sequence<int, MT / MH>());
+    }, std::make_integer_sequence<int, NT / 2>());
+    return rare;
+}
+
+// The whole wave again, element by element, for the activations' rare arguments.
+template <typename T, bool BWD, int MT, int NT>
+__device__ __forceinline__ void lin_slow(const LinArgs<T>& a, int64_t m0, int n0,
+                                         const f32x4 (&acc)[MT][NT])
+{
+    const int l = late_lane();
+#pragma unroll 1
+    for (int t = 0; t < MT * NT; ++t) {
+        const int i = t / NT, j = t % NT;
+        f32x4 z = f32x4{};
+#pragma unroll
+        for (int k = 0; k < MT * NT; ++k)  // a uniform choice of registers
+            if (k == t)
+                z = acc[k / NT][k % NT];
+        const int64_t m = m0 + l % 16 + 16 * i;
+        const int n = n0 + 32 * (j / 2) + 8 * (l / 16) + 4 * (j % 2);
+        if (m >= a.q.rows)
+            continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.out_cols)
+                lin_one<T, BWD>(a, m, n + e, z[e]);
+    }
+}
+
+template <typename T, int MODE, bool BWD, bool PARTS, int MT, int NT>
+__device__ __forceinline__ void lin_epilogue(const LinArgs<T>& a, int64_t m0, int n0,
+                                             const f32x4 (&acc)[MT][NT])
+{
+    if constexpr (PARTS) {
+        store_results<MODE == kLin>(a.part + (int64_t)blockIdx.y * a.q.rows * a.part_ld, a.part_ld,
+                                    a.q.rows, a.part_ld, m0, n0, acc);
+    } else if constexpr (MODE != kLin) {
+        store_results<false>(a.out[0], a.ldo[0], a.q.rows, a.out_cols, m0, n0, acc);
+    } else {
+        if (__any(lin_fast<T, BWD>(a, m0, n0, acc)))
+            lin_slow<T, BWD>(a, m0, n0, acc);
+    }
+}
+
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, bool PARTS>
+__global__ __launch_bounds__(WM * WN * 64, 2) void lin_tiles_kernel(const LinArgs<T> a)
+{
+    product_tiles<T, MODE, WM, WN, MT, NT, PARTS>(
+        a, [&](int64_t m0, int n0, int, const f32x4 (&acc)[MT][NT]) {
+            lin_epilogue<T, MODE, BWD, PARTS>(a, m0, n0, acc);
+        });
+}
+
+template <typename T, bool BWD, int PT, int QT, int NW>
+__global__ __launch_bounds__(NW * 64) void lin_few_kernel(const LinArgs<T> a)
+{
+    few_tokens<T, 1, PT, QT, NW>(a, [&](int m, int n, const float (&r)[1]) {
+        if (n < a.out_cols)
+            lin_one<T, BWD>(a, m, n, r[0]);
+    });
+}
+
+// The parts of a split sum: z, one element a thread.
+template <typename T, bool BWD>
+__global__ __launch_bounds__(256) void lin_parts_kernel(const LinArgs<T> a)
+{
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = at / a.out_cols;
+    if (m >= a.q.rows)
+        return;
+    const int c = (int)(at % a.out_cols);
+    float z = 0.0f;
+    if (c < a.p.rows) {
+        const float* p = a.part + m * a.part_ld + c;
+        for (int s = 0; s < a.splits; ++s) {
+            z += *p;
+            p += (int64_t)a.q.rows * a.part_ld;
+        }
+    }
+    lin_one<T, BWD>(a, m, c, z);
+}
+
+// The parts of a split sum: dx, dW.
+template <typename T, int MODE>
+__global__ __launch_bounds__(256) void lin_sum_kernel(const LinArgs<T> a)
+{
+    sum_parts<T, MODE>(a);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void lin_pack_kernel(const PackArgs<T> a)
+{
+    pack_rows(a);
+}
+
+// ---------------------------------------------------------------------------
+// db: column sums of dz.  A block takes 64 vectors of columns and a share of the
+// rows, one row a wave; its waves' sums meet in LDS.  A second kernel adds the
+// shares in order.
+// ---------------------------------------------------------------------------
+template <typename T>
+struct ColArgs {
+    const T* d;
+    int64_t ld, rows;
+    int cols;
+    float* part;  // [shares][cols]
+    int shares;
+    T* out;
+};
+
+constexpr int kColUnroll = 8;  // rows of a wave in flight
+
+template <typename T>
+__global__ __launch_bounds__(256) void lin_cols_kernel(const ColArgs<T> a)
+{
+    constexpr int E = Elem<T>::kPerVec, U = kColUnroll;
+    __shared__ float lds[4][64 * E];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int e0 = (blockIdx.x * 64 + lane) * E;
+    const int64_t first = a.rows * blockIdx.y / a.shares, end = a.rows * (blockIdx.y + 1) / a.shares;
+    float s[E] = {};
+    if (e0 < a.cols) {
+        int64_t row = first + wave;
+        for (; row + 4 * (U - 1) < end; row += 4 * U) {
+            u32x4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                v[u] = load_chunk(a.d + (row + 4 * u) * a.ld, e0, a.cols);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[E];
+                Elem<T>::unpack(v[u], f);
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    s[j] += f[j];
+            }
+        }
+        for (; row < end; row += 4) {
+            float f[E];
+            Elem<T>::unpack(load_chunk(a.d + row * a.ld, e0, a.cols), f);
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                s[j] += f[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        lds[wave][lane * E + j] = s[j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 64 * E; c += 256) {
+        const int col = blockIdx.x * (64 * E) + c;
+        if (col < a.cols)
+            a.part[(int64_t)blockIdx.y * a.cols + col] =
+                (lds[0][c] + lds[1][c]) + (lds[2][c] + lds[3][c]);
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void lin_col_sum_kernel(const ColArgs<T> a)
+{
+    __shared__ float lds[8][32];
+    const int c = threadIdx.x % 32, k = threadIdx.x / 32;
+    const int col = blockIdx.x * 32 + c;
+    float s = 0.0f;
+    if (col < a.cols)
+        for (int p = k; p < a.shares; p += 8)
+            s += a.part[(int64_t)p * a.cols + col];
+    lds[k][c] = s;
+    __syncthreads();
+    if (k == 0 && col < a.cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t += lds[i][c];
+        a.out[col] = Elem<T>::put(t);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host.
+// ---------------------------------------------------------------------------
+
+constexpr size_t kMaxTokens = (size_t)1 << 30;
+
+bool sizes_ok(size_t tokens, size_t dim, size_t units)
+{
+    return tokens < kMaxTokens && dim <= LINEAR_MAX_LD && units <= LINEAR_MAX_LD;
+}
+
+bool call_ok(int act, float param)
+{
+    return act == LINEAR_IDENTITY ? isfinite(param) : act_ok(act, param);
+}
+
+bool matrix_ok(const void* p, size_t rows, size_t cols, size_t ld, size_t es)
+{
+    if (ld < cols || ld > LINEAR_MAX_LD)
+        return false;
+    return rows == 0 || cols == 0 || (p && aligned(p, es));
+}
+
+bool rows_aligned(const void* p, size_t ld, size_t cols, size_t es)
+{
+    return aligned(p, 16) && ld * es % 16 == 0 && cols * es % 16 == 0;
+}
+
+// Most tokens of the kernel that reads the weight once.
+constexpr int kFewTokens = 32;
+
+// Shares of the rows in db's sums: about four blocks a CU, 32 rows a share at
+// the least.
+int col_shares(int64_t rows, int64_t cols, size_t es)
+{
+    const int64_t blocks = (cols * (int64_t)es + 1023) / 1024;
+    int64_t s = (4 * kCus + blocks - 1) / (blocks ? blocks : 1);
+    const int64_t most = (rows + 31) / 32;
+    s = s < most ? s : most;
+    return (int)(s < 1 ? 1 : s);
+}
+
+// The workspace: dz in padded rows (backward with an activation), the packed
+// operands, the parts of one split sum at a time (or of db's).  Each is whole
+// 128-byte lines long.
+struct Space {
+    size_t dz, xw, dy, part;
+    size_t bytes() const { return dz + xw + dy + part; }
+};
+
+Space space(size_t tokens, size_t dim, size_t units, bool act, size_t es, bool backward, int align)
+{
+    const int64_t m = (int64_t)tokens, d = (int64_t)dim, f = (int64_t)units;
+    const bool few = tokens <= (size_t)kFewTokens;
+    Space s{};
+    // The kernel for few tokens takes any rows.
+    if (!(align & LINEAR_ALIGNED_XW) && (backward || !few))
+        s.xw = (tokens + units) * packed_ld(dim, es) * es;
+    if ((!backward || act) && !few)
+        s.part = part_bytes(kLin, m, f, d, es);
+    if (backward) {
+        if (act)
+            s.dz = lines(tokens * padded(units) * es);
+        else if (!(align & LINEAR_ALIGNED_DY))
+            s.dy = tokens * packed_ld(units, es) * es;
+        const size_t more[] = {part_bytes(kLinDx, m, d, f, es), part_bytes(kLinDw, f, d, m, es),
+                               (size_t)col_shares(m, f, es) * units * sizeof(float)};
+        for (size_t v : more)
+            s.part = s.part > v ? s.part : v;
+    }
+    s.part = lines(s.part);
+    return s;
+}
+
+template <typename T, bool BWD, int PT, int QT>
+int lin_few(LinArgs<T>& a, hipStream_t stream)
+{
+    void* args[] = {&a};
+    return launch(reinterpret_cast<const void*>(&lin_few_kernel<T, BWD, PT, QT, 8>),
+                  dim3((unsigned)((a.out_cols + 16 * PT - 1) / (16 * PT))), 512, args, stream);
+}
+
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, bool PARTS>
+int lin_tiles(LinArgs<T>& a, hipStream_t stream)
+{
+    constexpr int kLds = 2 * (WM * MT + WN * NT) * 16 * 128;
+    int rc = launch_tiles(
+        a,
+        reinterpret_cast<const void*>(
+            &lin_tiles_kernel<T, MODE, BWD && !PARTS, WM, WN, MT, NT, PARTS>),
+        WM * MT * 16, WN * NT * 16, 1, WM * WN * 64,
+        MODE == kLin && !PARTS ? resident_blocks(kLds) : 0, stream);
+    if (rc != MESWISH_OK || !PARTS)
+        return rc;
+    void* args[] = {&a};
+    if constexpr (MODE == kLin)
+        return launch_over(reinterpret_cast<const void*>(&lin_parts_kernel<T, BWD>),
+                           (int64_t)a.q.rows * a.out_cols, args, stream);
+    else
+        return launch_over(reinterpret_cast<const void*>(&lin_sum_kernel<T, MODE>),
+                           (int64_t)a.q.rows * (a.part_ld / 4), args, stream);
+}
+
+// part: memory for the parts of a split sum; k, cols: the length and the columns
+// that the plan (and the size of that memory) goes by.
+template <typename T, int MODE, bool BWD>
+int lin_product(LinArgs<T>& a, int64_t cols, int64_t k, float* part, hipStream_t stream)
+{
+    a.splits = 1;
+    if (a.q.rows == 0 || a.out_cols == 0)
+        return MESWISH_OK;
+    if constexpr (MODE == kLin) {
+        if (a.q.rows <= kFewTokens)
+            return a.q.rows <= 16 ? lin_few<T, BWD, 1, 1>(a, stream)
+                                  : lin_few<T, BWD, 2, 2>(a, stream);
+    }
+    const Plan p = make_plan(a.q.rows, cols, k, 1, 1, sizeof(T));
+    a.splits = p.splits;
+    a.part = part;
+    a.part_ld = (int)part_ld(MODE, cols);
+    if (p.big)
+        return p.splits > 1 ? lin_tiles<T, MODE, BWD, 2, 4, 8, 4, true>(a, stream)
+                            : lin_tiles<T, MODE, BWD, 2, 4, 8, 4, false>(a, stream);
+    return p.splits > 1 ? lin_tiles<T, MODE, BWD, 2, 2, 4, 4, true>(a, stream)
+                        : lin_tiles<T, MODE, BWD, 2, 2, 4, 4, false>(a, stream);
+}
+
+// Rows of a matrix as the products take them.
+template <typename T>
+struct Rows {
+    const T* p;
+    int64_t ld;
+    int cols;  // in whole vectors, zeros behind the caller's (packed)
+};
+
+// Packs up to two matrices of the same row length, after each other.
+template <typename T>
+int pack(Rows<T>& a, size_t arows, Rows<T>* b, size_t brows, T* to, hipStream_t stream)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    const int64_t ld = (int64_t)packed_ld((size_t)a.cols, sizeof(T));
+    PackArgs<T> args{{a.p, b ? b->p : a.p, a.p},
+                     {a.ld, b ? b->ld : a.ld, a.ld},
+                     {(int64_t)arows, (int64_t)brows, 0},
+                     to,
+                     a.cols,
+                     (int)ld,
+                     0};
+    while (args.row_bits < 8 && (E << args.row_bits) < ld)
+        ++args.row_bits;
+    const int cols = (a.cols + E - 1) / E * E;
+    a = Rows<T>{to, ld, cols};
+    if (b)
+        *b = Rows<T>{to + (int64_t)arows * ld, ld, cols};
+    const int64_t rows = (int64_t)(arows + brows);
+    if (rows == 0 || ld == 0)
+        return MESWISH_OK;
+    const int64_t blocks = ((rows << args.row_bits) + 255) / 256;
+    void* p[] = {&args};
+    return launch(reinterpret_cast<const void*>(&lin_pack_kernel<T>),
+                  dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), 256, p, stream);
+}
+
+template <typename T>
+int col_sums(const Rows<T>& d, size_t rows, size_t cols, float* part, T* out, hipStream_t stream)
+{
+    if (cols == 0)
+        return MESWISH_OK;
+    ColArgs<T> a{d.p, d.ld, (int64_t)rows, (int)cols, part,
+                 col_shares((int64_t)rows, (int64_t)cols, sizeof(T)), out};
+    void* args[] = {&a};
+    constexpr int kCols = 64 * Elem<T>::kPerVec;
+    int rc = launch(reinterpret_cast<const void*>(&lin_cols_kernel<T>),
+                    dim3((unsigned)((cols + kCols - 1) / kCols), (unsigned)a.shares), 256, args,
+                    stream);
+    if (rc != MESWISH_OK)
+        return rc;
+    return launch(reinterpret_cast<const void*>(&lin_col_sum_kernel<T>),
+                  dim3((unsigned)((cols + 31) / 32)), 256, args, stream);
+}
+
+// What a call was given, checked.
+struct Call {
+    int act;
+    float param;
+    const void *x, *w, *bias, *r;  // r: the residual, or dy
+    int64_t ldx, ldw, ldr;
+    size_t tokens, dim, units;
+    void *y, *dx, *dw, *dbias;
+    int64_t ldy, lddx, lddw;
+    char* workspace;
+    Space space;
+    hipStream_t stream;
+};
+
+template <typename T, bool BWD>
+int run(const Call& c)
+{
+    Rows<T> x{static_cast<const T*>(c.x), c.ldx, (int)c.dim};
+    Rows<T> w{static_cast<const T*>(c.w), c.ldw, (int)c.dim};
+    const Rows<T> x_given = x, w_given = w;
+    const bool few = c.tokens <= (size_t)kFewTokens, act = c.act != LINEAR_IDENTITY;
+    char* at = c.workspace;
+    T* dz = reinterpret_cast<T*>(at);
+    T* xw = reinterpret_cast<T*>(at += c.space.dz);
+    T* dy = reinterpret_cast<T*>(at += c.space.xw);
+    float* part = reinterpret_cast<float*>(at += c.space.dy);
+    int rc = MESWISH_OK;
+    // In the backward without an activation x serves dW alone and w dx.
+    const bool need_x = !BWD || act || c.dw, need_w = !BWD || act || c.dx;
+    if (c.space.xw)
+        rc = pack(x, need_x ? c.tokens : 0, &w, need_w ? c.units : 0, xw, c.stream);
+    Rows<T> d{static_cast<const T*>(c.r), c.ldr, (int)c.units};
+    if (rc == MESWISH_OK && (!BWD || act)) {
+        LinArgs<T> a{};
+        const Rows<T>&p = few ? w_given : w, &q = few ? x_given : x;
+        a.p = operand<T>(p.p, p.ld, p.p, p.ld, c.units);
+        a.q = operand<T>(q.p, q.ld, q.p, q.ld, c.tokens);
+        a.k = q.cols;
+        a.bias = static_cast<const T*>(c.bias);
+        a.r = d.p;
+        a.ldr = d.ld;
+        a.act = c.act;
+        if (act)
+            a.coef = unit_coef(c.act, c.param);
+        const int64_t fp = (int64_t)padded(c.units);
+        a.out[0] = BWD ? dz : static_cast<T*>(c.y);
+        a.ldo[0] = BWD ? fp : c.ldy;
+        a.out_cols = BWD ? (int)fp : (int)c.units;
+        rc = lin_product<T, kLin, BWD>(a, (int64_t)c.units, (int64_t)c.dim, part, c.stream);
+        if (BWD)
+            d = Rows<T>{dz, fp, (int)fp};
+    } else if (rc == MESWISH_OK && c.space.dy && (c.dx || c.dw)) {
+        rc = pack<T>(d, c.tokens, nullptr, 0, dy, c.stream);
+    }
+    if constexpr (BWD) {
+        if (rc == MESWISH_OK && c.dx) {
+            LinArgs<T> a{};
+            a.p = operand<T>(w.p, w.ld, w.p, w.ld, (size_t)w.cols);
+            a.q = operand<T>(d.p, d.ld, d.p, d.ld, c.tokens);
+            a.k = (int)c.units;
+            a.out[0] = static_cast<T*>(c.dx);
+            a.ldo[0] = c.lddx;
+            a.out_cols = (int)c.dim;
+            rc = lin_product<T, kLinDx, false>(a, (int64_t)c.dim, (int64_t)c.units, part, c.stream);
+        }
+        if (rc == MESWISH_OK && c.dw) {
+            LinArgs<T> a{};
+            a.p = operand<T>(x.p, x.ld, x.p, x.ld, (size_t)x.cols);
+            a.q = operand<T>(d.p, d.ld, d.p, d.ld, c.units);
+            a.k = (int)c.tokens;
+            a.q_cols = d.cols;
+            a.out[0] = static_cast<T*>(c.dw);
+            a.ldo[0] = c.lddw;
+            a.out_cols = (int)c.dim;
+            rc = lin_product<T, kLinDw, false>(a, (int64_t)c.dim, (int64_t)c.tokens, part, c.stream);
+        }
+        if (rc == MESWISH_OK && c.dbias)
+            rc = col_sums<T>(d, c.tokens, c.units, part, static_cast<T*>(c.dbias), c.stream);
+    }
+    return rc;
+}
+
+template <bool BWD>
+int run_dtype(int dtype, const Call& c)
+{
+    return dtype == MESWISH_F32 ? run<float, BWD>(c) : run<bf16_t, BWD>(c);
+}
+
+}  // namespace
+
+}  // namespace meblock
+
+using namespace meblock;
+
+extern "C" size_t linear_workspace_bytes(size_t tokens, size_t dim, size_t units, int act, int dtype,
+                                         int backward, int align)
+{
+    if (!dtype_ok(dtype) || !sizes_ok(tokens, dim, units) ||
+        (act != LINEAR_IDENTITY && !act_ok(act, 1.0f)))
+        return 0;
+    const size_t es = elem_size(dtype);
+    if (dim * es % 16)
+        align &= ~LINEAR_ALIGNED_XW;
+    if (units * es % 16)
+        align &= ~LINEAR_ALIGNED_DY;
+    return space(tokens, dim, units, act != LINEAR_IDENTITY, es, backward != 0, align).bytes();
+}
+
+extern "C" int linear_fwd(int act, float param, const void* x, size_t ldx, const void* w, size_t ldw,
+                          const void* bias, const void* residual, size_t ldr, size_t tokens,
+                          size_t dim, size_t units, void* y, size_t ldy, void* workspace,
+                          size_t workspace_bytes, int dtype, void* stream)
+{
+    if (!dtype_ok(dtype) || !call_ok(act, param) || !sizes_ok(tokens, dim, units))
+        return MESWISH_EINVAL;
+    const size_t es = elem_size(dtype);
+    if (!matrix_ok(x, tokens, dim, ldx, es) || !matrix_ok(w, units, dim, ldw, es) ||
+        !aligned(bias, es) || (residual && !matrix_ok(residual, tokens, units, ldr, es)) ||
+        !matrix_ok(y, tokens, units, ldy, es))
+        return MESWISH_EINVAL;
+    const int align = rows_aligned(x, ldx, dim, es) && rows_aligned(w, ldw, dim, es)
+                          ? LINEAR_ALIGNED_XW : 0;
+    const Space sp = space(tokens, dim, units, act != LINEAR_IDENTITY, es, false, align);
+    const size_t need = sp.bytes();
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return MESWISH_EINVAL;
+    const Span in[] = {span(x, tokens, dim, ldx, es), span(w, units, dim, ldw, es),
+                       span(bias, bias ? 1 : 0, units, units, es),
+                       span(residual, residual ? tokens : 0, units, ldr, es)};
+    const Span out[] = {span(y, tokens, units, ldy, es), span(workspace, need ? 1 : 0, need, need, 1)};
+    const int rc = apart(out, 2, in, 4);
+    if (rc != MESWISH_OK || tokens == 0 || units == 0)
+        return rc;
+    Call c{};
+    c.act = act, c.param = param;
+    c.x = x, c.w = w, c.bias = bias, c.r = residual, c.y = y;
+    c.ldx = (int64_t)ldx, c.ldw = (int64_t)ldw, c.ldr = (int64_t)ldr, c.ldy = (int64_t)ldy;
+    c.tokens = tokens, c.dim = dim, c.units = units;
+    c.workspace = static_cast<char*>(workspace);
+    c.space = sp;
+    c.stream = static_cast<hipStream_t>(stream);
+    return run_dtype<false>(dtype, c);
+}
+
+extern "C" int linear_bwd(int act, float param, const void* x, size_t ldx, const void* w, size_t ldw,
+                          const void* bias, const void* dy, size_t lddy, size_t tokens, size_t dim,
+                          size_t units, void* dx, size_t lddx, void* dw, size_t lddw, void* dbias,
+                          void* workspace, size_t workspace_bytes, int dtype, void* stream)
+{
+    if (!dtype_ok(dtype) || !call_ok(act, param) || !sizes_ok(tokens, dim, units))
+        return MESWISH_EINVAL;
+    const size_t es = elem_size(dtype);
+    if (!matrix_ok(x, tokens, dim, ldx, es) || !matrix_ok(w, units, dim, ldw, es) ||
+        !aligned(bias, es) || !matrix_ok(dy, tokens, units, lddy, es) ||
+        (dx && !matrix_ok(dx, tokens, dim, lddx, es)) ||
+        (dw && !matrix_ok(dw, units, dim, lddw, es)) || !aligned(dbias, es))
+        return MESWISH_EINVAL;
+    const int align = (rows_aligned(x, ldx, dim, es) && rows_aligned(w, ldw, dim, es)
+                           ? LINEAR_ALIGNED_XW : 0) |
+                      (rows_aligned(dy, lddy, units, es) ? LINEAR_ALIGNED_DY : 0);
+    const Space sp = space(tokens, dim, units, act != LINEAR_IDENTITY, es, true, align);
+    const size_t need = sp.bytes();
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+        return MESWISH_EINVAL;
+    const Span in[] = {span(x, tokens, dim, ldx, es), span(w, units, dim, ldw, es),
+                       span(bias, bias ? 1 : 0, units, units, es), span(dy, tokens, units, lddy, es)};
+    const Span out[] = {span(dx, dx ? tokens : 0, dim, lddx, es), span(dw, dw ? units : 0, dim, lddw, es),
+                        span(dbias, dbias ? 1 : 0, units, units, es),
+                        span(workspace, need ? 1 : 0, need, need, 1)};
+    const int rc = apart(out, 4, in, 4);
+    if (rc != MESWISH_OK || (!dx && !dw && !dbias))
+        return rc;
+    Call c{};
+    c.act = act, c.param = param;
+    c.x = x, c.w = w, c.bias = bias, c.r = dy, c.dx = dx, c.dw = dw, c.dbias = dbias;
+    c.ldx = (int64_t)ldx, c.ldw = (int64_t)ldw, c.ldr = (int64_t)lddy, c.lddx = (int64_t)lddx;
+    c.lddw = (int64_t)lddw;
+    c.tokens = tokens, c.dim = dim, c.units = units;
+    c.workspace = static_cast<char*>(workspace);
+    c.space = sp;
+    c.stream = static_cast<hipStream_t>(stream);
+    return run_dtype<true>(dtype, c);
+}
