@@ -1,6 +1,6 @@
 """ctypes loader for libmeswish.so (the C ABI declared in include/meswish.h,
 include/dense_bn.h, include/fft_conv.h, include/layer_norm.h,
-include/gated_ffn.h and include/linear.h).
+include/gated_ffn.h, include/linear.h and include/residual_norm.h).
 
 Argument marshalling only: every element of every pass is computed by the
 HIP kernels inside the library.  There is no CPU fallback -- if the library
@@ -32,8 +32,9 @@ EXPORTED = ("swish_fwd", "swish_bwd", "swish_fwd_grouped", "swish_bwd_grouped",
 BLOCK_EXPORTED = ("layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
                   "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn_workspace_bytes")
 GATED_FFN_MAX_LD = 2097152
-# What finishes a transformer block (include/linear.h).
-FINISH_EXPORTED = ("linear_fwd", "linear_bwd", "linear_workspace_bytes")
+# What finishes a transformer block (include/linear.h, include/residual_norm.h).
+FINISH_EXPORTED = ("linear_fwd", "linear_bwd", "linear_workspace_bytes", "residual_norm_fwd",
+                   "residual_norm_bwd", "residual_norm_workspace_bytes")
 LINEAR_MAX_LD = 2097152
 LINEAR_IDENTITY = -1
 LINEAR_ALIGNED_XW, LINEAR_ALIGNED_DY = 1, 2
@@ -68,6 +69,17 @@ class DenseSource(ctypes.Structure):
     """dense_bn_source of include/dense_bn.h."""
     _fields_ = [("x", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("stats", ctypes.c_void_p),
                 ("channels", ctypes.c_int), ("offset", ctypes.c_int)]
+
+
+class ResidualNormOp(ctypes.Structure):
+    """residual_norm_op of include/residual_norm.h."""
+    _fields_ = [("rows", ctypes.c_size_t), ("n", ctypes.c_size_t), ("gates", ctypes.c_size_t),
+                ("gate", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("post_bias", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("pre_bias", ctypes.c_void_p), ("skip", ctypes.c_float), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("post", ctypes.c_int), ("pre", ctypes.c_int),
+                ("center", ctypes.c_int), ("stream_dtype", ctypes.c_int),
+                ("branch_dtype", ctypes.c_int), ("param_dtype", ctypes.c_int)]
 
 
 class MeswishError(RuntimeError):
@@ -126,11 +138,16 @@ def _block_signatures() -> dict:
 def _finish_signatures() -> dict:
     """Argument and result types of the operators that finish a block."""
     vp, sz, f, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float, ctypes.c_int
+    op = ctypes.POINTER(ResidualNormOp)
     return {
         "linear_workspace_bytes": ([sz, sz, sz, i, i, i, i], sz),
         "linear_fwd": ([i, f, vp, sz, vp, sz, vp, vp, sz, sz, sz, sz, vp, sz, vp, sz, i, vp], i),
         "linear_bwd": ([i, f, vp, sz, vp, sz, vp, vp, sz, sz, sz, sz, vp, sz, vp, sz, vp, vp, sz,
                         i, vp], i),
+        "residual_norm_fwd": ([op] + [vp, sz] * 4 + [vp] * 5, i),
+        "residual_norm_workspace_bytes": ([sz, sz, sz], sz),
+        "residual_norm_bwd": ([op] + [vp, sz] * 4 + [vp] * 4 + [vp, sz] * 2 + [vp] * 6 + [sz, vp],
+                              i),
     }
 
 

@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("meswish.hip", "dense_bn.hip", "fft_conv.hip",
                                                 "layer_norm.hip", "gated_ffn.hip",
-                                                "linear.hip")]
+                                                "linear.hip", "residual_norm.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libmeswish.so")
 
