@@ -81,7 +81,7 @@ int residual_norm_fwd(const residual_norm_op *op, const void *x, size_t ldx, con
 size_t residual_norm_workspace_bytes(size_t rows, size_t n, size_t gates);
 
 /* Backward.  y, dout (= do) and the statistics of pre only with pre, those of
- * post only with post; z only with post or a gate.  dy may be NULL: zeros.  The
+ * post only with post; z only with post or dgate.  dy may be NULL with pre: zeros.  The
  * gradients of the parameters and of the gate may be NULL, each by itself: what
  * is NULL is not written.  workspace: 16-byte aligned, as large as
  * residual_norm_workspace_bytes(rows, n, gates) says. */

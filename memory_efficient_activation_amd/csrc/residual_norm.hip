@@ -32,40 +32,108 @@ namespace meblock {
 namespace {
 
 constexpr int C = 8;  // columns of a thread and chunk
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
 // Rows.
 // ---------------------------------------------------------------------------
 
-// Eight columns of a row, as loaded.  SMALL: rows may be shorter than a vector.
-template <typename T, bool SMALL>
+// An offset that the compiler adds where it is used: a row's address stays in
+// scalar registers then, where else it would keep 64 bits a lane for every
+// matrix through the loop over rows.
+__device__ __forceinline__ uint32_t late_offset(int v)
+{
+    uint32_t u = (uint32_t)v;
+    asm volatile("" : "+v"(u));
+    return u;
+}
+
+// Eight columns of a row, as loaded.
+template <typename T>
 struct Chunk {
     static constexpr int E = Elem<T>::kPerVec, K = C / E;
     u32x4 v[K];
-    // Without a branch (load_near); what lies past the row's end is some other
-    // value of it.
-    __device__ __forceinline__ void load(const T* row, int e0, int n)
+    __device__ __forceinline__ void load(const T* row, int col)
     {
+        const char* p = reinterpret_cast<const char*>(row);
+        const uint32_t at = late_offset(col * (int)sizeof(T));
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            v[k] = SMALL ? load_chunk(row, e0 + k * E, n) : load_near(row, e0 + k * E, n);
+            v[k] = load16(p + at + 16 * k);
     }
-    // The values, zeros past the row's end.
-    __device__ __forceinline__ void values(float* f, int e0, int n) const
+    // Zeros past the row's end (for rows of any length).
+    __device__ __forceinline__ void load_cut(const T* row, int e0, int n)
     {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            Elem<T>::unpack(SMALL ? v[k] : chunk_of<T>(v[k], e0 + k * E, n), f + k * E);
+            v[k] = load_chunk(row, e0 + k * E, n);
+    }
+    // mask: 0 (zeros in the place of the values) or all ones.
+    __device__ __forceinline__ void keep(uint32_t mask)
+    {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            v[k] &= mask;
+    }
+    __device__ __forceinline__ void values(float* f) const
+    {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            Elem<T>::unpack(v[k], f + k * E);
     }
 };
 
 template <typename T>
-__device__ __forceinline__ void store_row(T* row, int e0, int n, const float* f)
+__device__ __forceinline__ void store8(T* row, int col, const float* f)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    char* p = reinterpret_cast<char*>(row);
+    const uint32_t at = late_offset(col * (int)sizeof(T));
+#pragma unroll
+    for (int k = 0; k < C / E; ++k)
+        store16(p + at + 16 * k, Elem<T>::pack(f + k * E));
+}
+
+template <typename T>
+__device__ __forceinline__ void store_cut(T* row, int e0, int n, const float* f)
 {
     constexpr int E = Elem<T>::kPerVec;
 #pragma unroll
     for (int k = 0; k < C / E; ++k)
         store_chunk(row, e0 + k * E, n, f + k * E);
+}
+
+// The columns of a thread's chunk.  A chunk that would pass the row's end is moved
+// back to end with it: it shares its first `shared` columns with the chunk before
+// (or all eight), and both compute the same values there.  Sums over the row
+// count them once.  So no load, store or value needs a mask.
+struct Place {
+    int col, shared;
+    Place() = default;
+    __device__ __forceinline__ Place(int e0, int n)
+    {
+        col = e0 <= n - C ? e0 : n - C;
+        shared = e0 - col < C ? e0 - col : C;
+    }
+    __device__ __forceinline__ bool none() const { return shared == C; }
+};
+
+// Sum of f(j) over a chunk's columns, added to s.
+template <class F>
+__device__ __forceinline__ float chunk_sum(const Place& p, const F& f)
+{
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+        s = f(j, s);
+    if (p.shared) {
+        s = 0.0f;
+#pragma unroll
+        for (int j = 1; j < C; ++j)
+            if (j >= p.shared)
+                s = f(j, s);
+    }
+    return s;
 }
 
 // Eight parameters of n, `none` past the end and where there are none.
@@ -91,6 +159,18 @@ __device__ __forceinline__ void load_params(const void* p, int wide, int e0, int
             if (e0 + j < n)
                 f[j] = wide ? static_cast<const float*>(p)[e0 + j]
                             : Elem<bf16_t>::get(static_cast<const bf16_t*>(p)[e0 + j]);
+    }
+}
+
+// Eight parameters, whole.
+__device__ __forceinline__ void put_params(void* p, int wide, int64_t at, const float* f)
+{
+    if (wide) {
+        float* q = static_cast<float*>(p) + at;
+        store16(q, Elem<float>::pack(f));
+        store16(q + 4, Elem<float>::pack(f + 4));
+    } else {
+        store16(static_cast<bf16_t*>(p) + at, Elem<bf16_t>::pack(f));
     }
 }
 
@@ -120,6 +200,53 @@ struct Block {
     static constexpr int kLds = G > 64 ? kThreads / 64 : 1;  // floats of one sum
 };
 
+// Which of the block's groups this thread is in, as a scalar where a group is whole
+// waves: a row's address is one then, and its lanes need offsets alone.
+template <int G>
+__device__ __forceinline__ int group_of_thread()
+{
+    if constexpr (Block<G>::kGroups == 1)
+        return 0;
+    else if constexpr (G >= 64)
+        return __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+    else
+        return threadIdx.x / G;
+}
+
+// v plus its value in another lane: DPP within rows of 16 lanes, the lane swaps
+// across them.  (Through LDS permutes an exchange held six address registers and
+// waited for LDS six times.)
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v)
+{
+    const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true);
+    return v + __builtin_bit_cast(float, o);
+}
+
+// Sum over each G lanes (8 to 64, at most a wave), the result in every lane.
+template <int G>
+__device__ __forceinline__ float lane_sum(float v)
+{
+    v = add_dpp<0xb1>(v);   // quad_perm 1 0 3 2
+    v = add_dpp<0x4e>(v);   // quad_perm 2 3 0 1
+    v = add_dpp<0x141>(v);  // row_half_mirror: the other four of eight
+    if constexpr (G >= 16)
+        v = add_dpp<0x140>(v);  // row_mirror: the other eight of 16
+    if constexpr (G >= 32) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, v);
+        const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+        const uint32_t lo = r[0], hi = r[1];
+        v = __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+    }
+    if constexpr (G >= 64) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, v);
+        const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+        const uint32_t lo = r[0], hi = r[1];
+        v = __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+    }
+    return v;
+}
+
 // Sum of K values over each group of G threads, the result in every thread.
 // Waves combine through `lds` (2 K Block::kLds floats); calls alternate between
 // its halves (`turn`), so that one barrier a call is enough: a half is written
@@ -128,10 +255,8 @@ template <int G, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* lds, int& turn)
 {
 #pragma unroll
-    for (int m = 1; m < (G < 64 ? G : 64); m <<= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            v[k] += __shfl_xor(v[k], m);
+    for (int k = 0; k < K; ++k)
+        v[k] = lane_sum<(G < 64 ? G : 64)>(v[k]);
     if constexpr (G > 64) {
         constexpr int W = Block<G>::kWaves;
         lds += turn * (K * Block<G>::kLds);
@@ -164,7 +289,8 @@ struct RnArgs {
     int center, wide;  // wide: binary32 parameters
     int64_t gates, gate_rows;  // gate_rows: rows that share a gate row
     const void *gate, *post_weight, *post_bias, *pre_weight, *pre_bias;
-    const void *x, *z, *dy, *dout;  // backward: x is y
+    const void *x, *z, *dy, *dout;  // backward: x is y; where there is no dy, it is y
+    uint32_t dy_mask;               // under a mask of 0 (a load without a branch)
     int64_t ldx, ldz, lddy, lddout;
     void *y, *o;  // backward: dx, dz
     int64_t ldy, ldo;
@@ -189,132 +315,174 @@ __device__ __forceinline__ const char* gate_of(const RnArgs& a, int64_t g)
 // Forward.
 // ---------------------------------------------------------------------------
 
-// Mean and 1 / sqrt(variance + eps) of a row; f becomes f - mean (zeros past its
-// end).
-template <int G, int V>
-__device__ __forceinline__ void row_stats(const RnArgs& a, float (&f)[V][C], int g, float* lds,
-                                          int& turn, float& mean, float& rstd)
+// Means and 1 / sqrt(variance + eps) of R rows; f becomes f - mean.
+template <int G, int V, int R>
+__device__ __forceinline__ void row_stats(const RnArgs& a, float (&f)[R][V][C], const Place (&at)[V],
+                                          float* lds, int& turn, float (&mean)[R], float (&rstd)[R])
 {
-    mean = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        mean[r] = 0.0f;
     if (a.center) {
-        float s[1] = {0.0f};
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                s[0] += f[v][j];
-        row_sum<G>(s, lds, turn);
-        mean = s[0] * a.inv_n;
+            for (int v = 0; v < V; ++v)
+                mean[r] += chunk_sum(at[v], [&](int j, float t) { return t + f[r][v][j]; });
+        row_sum<G>(mean, lds, turn);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
+        for (int r = 0; r < R; ++r) {
+            mean[r] *= a.inv_n;
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                f[v][j] -= mean;
-            cut(f[v], (v * G + g) * C, a.n);
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    f[r][v][j] -= mean[r];
         }
     }
-    float q[1] = {0.0f};
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int r = 0; r < R; ++r) {
+        rstd[r] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            q[0] = fmaf(f[v][j], f[v][j], q[0]);
-    row_sum<G>(q, lds, turn);
-    rstd = 1.0f / sqrtf(fmaf(q[0], a.inv_n, a.eps));
+        for (int v = 0; v < V; ++v)
+            rstd[r] += chunk_sum(at[v], [&](int j, float t) { return fmaf(f[r][v][j], f[r][v][j], t); });
+    }
+    row_sum<G>(rstd, lds, turn);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        rstd[r] = 1.0f / sqrtf(fmaf(rstd[r], a.inv_n, a.eps));
 }
 
-// TS, TB: the stream's type and the branches'.
-template <typename TS, typename TB, bool POST, bool PRE, int G, int V>
-__global__ __launch_bounds__(Block<G>::kThreads) void rn_fwd_kernel(const RnArgs a)
+// TS, TB: the stream's type and the branches'.  R rows of a group at a time: their
+// loads in flight together, their sums in one exchange.
+template <typename TS, typename TB, bool POST, bool PRE, int G, int V, int R>
+__global__ __launch_bounds__(Block<G>::kThreads, 4) void rn_fwd_kernel(const RnArgs a)
 {
     constexpr int NG = Block<G>::kGroups;
-    constexpr bool SMALL = G == 8;
-    __shared__ float lds[2 * Block<G>::kLds];
+    __shared__ float lds[2 * R * Block<G>::kLds];
     int turn = 0;
-    const int g = threadIdx.x % G, grp = threadIdx.x / G, n = a.n;
-    float qw[V][C], qb[V][C], gate[V][C], nw[V][C], nb[V][C];
+    const int g = threadIdx.x % G, grp = group_of_thread<G>(), n = a.n;
+    Place at[V];
+    // scale w_post and scale b_post, with the gate where it is one for all rows.
+    float qw[V][C], qb[V][C], nw[V][C], nb[V][C];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e0 = (v * G + g) * C;
-        load_params(a.gate, a.wide, e0, n, 1.0f, gate[v]);
-        if constexpr (POST) {
-            load_params(a.post_weight, a.wide, e0, n, 1.0f, qw[v]);
-            load_params(a.post_bias, a.wide, e0, n, 0.0f, qb[v]);
+        at[v] = Place((v * G + g) * C, n);
+        const int col = at[v].col;
+        float gate[C];
+        load_params(a.gates > 1 ? nullptr : a.gate, a.wide, col, n, 1.0f, gate);
+        load_params(POST ? a.post_weight : nullptr, a.wide, col, n, 1.0f, qw[v]);
+        load_params(POST ? a.post_bias : nullptr, a.wide, col, n, 0.0f, qb[v]);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            qw[v][j] *= a.scale * gate[j];
+            qb[v][j] *= a.scale * gate[j];
         }
         if constexpr (PRE) {
-            load_params(a.pre_weight, a.wide, e0, n, 1.0f, nw[v]);
-            load_params(a.pre_bias, a.wide, e0, n, 0.0f, nb[v]);
+            load_params(a.pre_weight, a.wide, col, n, 1.0f, nw[v]);
+            load_params(a.pre_bias, a.wide, col, n, 0.0f, nb[v]);
         }
     }
+    // z's rows are loaded while the rows before are worked on, x's at the start of
+    // their own turn.
+    Chunk<TB> rz[R][V];
+    auto row_of = [&](int64_t base, int r) {
+        const int64_t row = base + r * NG + grp;
+        return row < a.rows ? row : a.rows - 1;
+    };
+    auto load_z = [&](int64_t base) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                rz[r][v].load(static_cast<const TB*>(a.z) + row_of(base, r) * a.ldz, at[v].col);
+    };
     // Threads of one block agree on the trips and meet every barrier together.
-    for (int64_t base = (int64_t)blockIdx.x * NG; base < a.rows; base += (int64_t)gridDim.x * NG) {
-        const bool in = base + grp < a.rows;
-        const int64_t row = in ? base + grp : a.rows - 1;
-        Chunk<TB, SMALL> rz[V];
-        Chunk<TS, SMALL> rx[V];
-        const TB* z = static_cast<const TB*>(a.z) + row * a.ldz;
-        const TS* x = static_cast<const TS*>(a.x) + row * a.ldx;
+    const int64_t all = (int64_t)gridDim.x * (NG * R);
+    int64_t base = (int64_t)blockIdx.x * (NG * R);
+    load_z(base);
+    for (; base < a.rows; base += all) {
+        bool in[R];
+        int64_t row[R];
+        Chunk<TS> rx[R][V];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            rz[v].load(z, (v * G + g) * C, n);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            rx[v].load(x, (v * G + g) * C, n);
-        if (a.gates > 1) {
-            const char* p = gate_of(a, row / a.gate_rows);
+        for (int r = 0; r < R; ++r) {
+            row[r] = row_of(base, r);
+            in[r] = base + r * NG + grp < a.rows;
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                load_params(p, a.wide, (v * G + g) * C, n, 1.0f, gate[v]);
+                rx[r][v].load(static_cast<const TS*>(a.x) + row[r] * a.ldx, at[v].col);
         }
-        float f[V][C];
+        __builtin_amdgcn_sched_barrier(0);
+        float f[R][V][C], mean[R], rstd[R];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            rz[v].values(f[v], (v * G + g) * C, n);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                rz[r][v].values(f[r][v]);
+        load_z(base + all);
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (POST) {
-            float mean, rstd;
-            row_stats<G>(a, f, g, lds, turn, mean, rstd);
+            row_stats<G>(a, f, at, lds, turn, mean, rstd);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+            for (int r = 0; r < R; ++r) {
 #pragma unroll
-                for (int j = 0; j < C; ++j)
-                    f[v][j] = fmaf(f[v][j] * rstd, qw[v][j], qb[v][j]);
-            if (in && g == 0) {
-                if (a.post_mean && a.center)
-                    a.post_mean[row] = mean;
-                if (a.post_rstd)
-                    a.post_rstd[row] = rstd;
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        f[r][v][j] *= rstd[r];
+                if (in[r] && g == 0) {
+                    if (a.post_mean && a.center)
+                        a.post_mean[row[r]] = mean[r];
+                    if (a.post_rstd)
+                        a.post_rstd[row[r]] = rstd[r];
+                }
             }
         }
-        TS* y = static_cast<TS*>(a.y) + row * a.ldy;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float fx[C];
-            const int e0 = (v * G + g) * C;
-            rx[v].values(fx, e0, n);
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-                f[v][j] = fmaf(a.scale, f[v][j] * gate[v][j], a.skip * fx[j]);
-            if (in)
-                store_row(y, e0, n, f[v]);
-        }
-        if constexpr (PRE) {
-            // (Past the row's end f is 0: x, z and the post bias are.)
-            float mean, rstd;
-            row_stats<G>(a, f, g, lds, turn, mean, rstd);
-            if (in && g == 0) {
-                if (a.pre_mean && a.center)
-                    a.pre_mean[row] = mean;
-                if (a.pre_rstd)
-                    a.pre_rstd[row] = rstd;
-            }
-            TB* o = static_cast<TB*>(a.o) + row * a.ldo;
+        for (int r = 0; r < R; ++r) {
+            TS* y = static_cast<TS*>(a.y) + row[r] * a.ldy;
+            const char* p = a.gates > 1 ? gate_of(a, row[r] / a.gate_rows) : nullptr;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                float fx[C];
+                rx[r][v].values(fx);
 #pragma unroll
                 for (int j = 0; j < C; ++j)
-                    f[v][j] = fmaf(f[v][j] * rstd, nw[v][j], nb[v][j]);
-                if (in)
-                    store_row(o, (v * G + g) * C, n, f[v]);
+                    f[r][v][j] = POST ? fmaf(f[r][v][j], qw[v][j], qb[v][j]) : f[r][v][j] * qw[v][j];
+                if (a.gates > 1) {
+                    float gate[C];
+                    load_params(p, a.wide, at[v].col, n, 1.0f, gate);
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        f[r][v][j] *= gate[j];
+                }
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    f[r][v][j] = fmaf(a.skip, fx[j], f[r][v][j]);
+                if (in[r] && !at[v].none())
+                    store8(y, at[v].col, f[r][v]);
+            }
+        }
+        if constexpr (PRE) {
+            row_stats<G>(a, f, at, lds, turn, mean, rstd);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (in[r] && g == 0) {
+                    if (a.pre_mean && a.center)
+                        a.pre_mean[row[r]] = mean[r];
+                    if (a.pre_rstd)
+                        a.pre_rstd[row[r]] = rstd[r];
+                }
+                TB* o = static_cast<TB*>(a.o) + row[r] * a.ldo;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        f[r][v][j] = fmaf(f[r][v][j] * rstd[r], nw[v][j], nb[v][j]);
+                    if (in[r] && !at[v].none())
+                        store8(o, at[v].col, f[r][v]);
+                }
             }
         }
     }
@@ -339,9 +507,9 @@ __global__ __launch_bounds__(1024) void rn_fwd_long_kernel(const RnArgs a)
                 f((int)e);
         };
         auto of_z = [&](int e0, float* f) {
-            Chunk<TB, true> c;
-            c.load(z, e0, n);
-            c.values(f, e0, n);
+            Chunk<TB> c;
+            c.load_cut(z, e0, n);
+            c.values(f);
         };
         // Sum of the values, or of their squared differences from `mean`.
         auto sum = [&](auto of, float mean, bool square) {
@@ -382,9 +550,9 @@ __global__ __launch_bounds__(1024) void rn_fwd_long_kernel(const RnArgs a)
                     f[j] = fmaf((f[j] - zm) * zr, p[j], b[j]);
             }
             load_params(gp, a.wide, e0, n, 1.0f, p);
-            Chunk<TS, true> c;
-            c.load(x, e0, n);
-            c.values(fx, e0, n);
+            Chunk<TS> c;
+            c.load_cut(x, e0, n);
+            c.values(fx);
 #pragma unroll
             for (int j = 0; j < C; ++j)
                 f[j] = fmaf(a.scale, f[j] * p[j], a.skip * fx[j]);
@@ -404,14 +572,14 @@ __global__ __launch_bounds__(1024) void rn_fwd_long_kernel(const RnArgs a)
         over([&](int e0) {
             float f[C], w[C], b[C];
             of_y(e0, f);
-            store_row(static_cast<TS*>(a.y) + row * a.ldy, e0, n, f);
+            store_cut(static_cast<TS*>(a.y) + row * a.ldy, e0, n, f);
             if constexpr (PRE) {
                 load_params(a.pre_weight, a.wide, e0, n, 1.0f, w);
                 load_params(a.pre_bias, a.wide, e0, n, 0.0f, b);
 #pragma unroll
                 for (int j = 0; j < C; ++j)
                     f[j] = fmaf((f[j] - ym) * yr, w[j], b[j]);
-                store_row(static_cast<TB*>(a.o) + row * a.ldo, e0, n, f);
+                store_cut(static_cast<TB*>(a.o) + row * a.ldo, e0, n, f);
             }
         });
     }
@@ -442,108 +610,199 @@ __device__ __forceinline__ Item item_of(const RnArgs& a, int64_t item)
     return Item{g, r + a.gate_rows * s / a.shares, r + a.gate_rows * (s + 1) / a.shares};
 }
 
-// SUMS: with the sums over rows (n <= 8192).
-template <typename TS, typename TB, bool POST, bool PRE, int G, int V, bool SUMS>
-__global__ __launch_bounds__(Block<G>::kThreads) void rn_bwd_kernel(const RnArgs a)
-{
-    constexpr int NG = Block<G>::kGroups, T = Block<G>::kThreads;
-    constexpr bool SMALL = G == 8;
-    __shared__ float lds[4 * Block<G>::kLds];
-    __shared__ float sums[SUMS && NG > 1 ? T * V * C : 1];
-    int turn = 0;
-    const int g = threadIdx.x % G, grp = threadIdx.x / G, n = a.n;
-    float qw[V][C], qb[V][C], gate[V][C], nw[V][C];
-    float ag[V][C], aqw[V][C], aqb[V][C], anw[V][C], anb[V][C];
+// Parameters in LDS, for a group's threads: in registers they would take those of
+// a second block on the CU.
+template <int G, int V>
+struct Params {
+    f32x4_t f[V][2][G];
+    __device__ __forceinline__ void put(const void* p, int wide, int v, int g, int col, int n,
+                                        float none)
+    {
+        float t[C];
+        load_params(p, wide, col, n, none, t);
+        f[v][0][g] = f32x4_t{t[0], t[1], t[2], t[3]};
+        f[v][1][g] = f32x4_t{t[4], t[5], t[6], t[7]};
+    }
+    __device__ __forceinline__ void get(int v, int g, float* t) const
+    {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e0 = (v * G + g) * C;
-        if constexpr (POST) {
-            load_params(a.post_weight, a.wide, e0, n, 1.0f, qw[v]);
-            load_params(a.post_bias, a.wide, e0, n, 0.0f, qb[v]);
-        }
-        if constexpr (PRE)
-            load_params(a.pre_weight, a.wide, e0, n, 1.0f, nw[v]);
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                t[4 * k + j] = f[v][k][g][j];
+    }
+};
+
+// The sums of a block's groups: to LDS, chunk by chunk, and a column's total, added
+// in order of the group.
+template <int G, int V>
+__device__ __forceinline__ int own_slot(int v)
+{
+    return threadIdx.x / G * (G * V * C) + (v * G + (int)threadIdx.x % G) * C;
+}
+
+template <int G, int V>
+__device__ __forceinline__ void to_lds(float* lds, const float (&f)[V][C])
+{
+#pragma unroll
+    for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int j = 0; j < C; ++j)
-            ag[v][j] = aqw[v][j] = aqb[v][j] = anw[v][j] = anb[v][j] = 0.0f;
+            lds[own_slot<G, V>(v) + j] = f[v][j];
+}
+
+template <int G, int V>
+__device__ __forceinline__ float from_lds(const float* lds, int col, int n)
+{
+    // A last chunk that was moved back ends with the row.
+    const int chunk = col / C, at = chunk * C <= n - C ? col : chunk * C + (col - (n - C));
+    float t = 0.0f;
+    for (int k = 0; k < Block<G>::kGroups; ++k)
+        t += lds[k * (G * V * C) + at];
+    return t;
+}
+
+// Keeps a branch one: the sums under it would be computed twice and selected, in as
+// many registers again.
+__device__ __forceinline__ void stay_branch() { asm volatile(""); }
+
+// A row in two steps: the upper (PRE: y and do, e) and the lower (POST: z; dx and dz).
+// What the first of them reads is loaded while the row before is in its second,
+// the rest while the first is worked on.
+//
+// Three of the five sums over rows follow from two, as the gate is one for all
+// rows of an item: with T0 = sum e and T1 = sum e zhat (or e z),
+//     dw_post = scale gate T1,  db_post = scale gate T0,
+//     dgate = scale (w_post T1 + b_post T0)  (scale T1 without post).
+//
+// SUMS: with the sums over rows (n <= 8192).  Z: z is read (POST, or for the
+// gate's gradient).
+template <typename TS, typename TB, bool POST, bool PRE, bool Z, int G, int V, bool SUMS>
+__global__ __launch_bounds__(Block<G>::kThreads, 4) void rn_bwd_kernel(const RnArgs a)
+{
+    constexpr int NG = Block<G>::kGroups, T = Block<G>::kThreads;
+    __shared__ float lds[4 * Block<G>::kLds];
+    __shared__ Params<PRE ? G : 1, V> nw;
+    // Groups' sums of one vector; of the post norm's parameters over the items.
+    __shared__ float sums[SUMS && NG > 1 ? T * V * C : 1];
+    __shared__ float post_sums[SUMS && POST && NG > 1 ? 2 : 1][SUMS && POST && NG > 1 ? T * V * C : 1];
+    int turn = 0;
+    const int g = threadIdx.x % G, grp = group_of_thread<G>(), n = a.n;
+    Place at[V];
+    float gw[V][C];  // scale gate w_post
+    float t0[V][C], t1[V][C], anw[V][C], anb[V][C];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        at[v] = Place((v * G + g) * C, n);
+        if constexpr (PRE)
+            if (grp == 0)
+                nw.put(a.pre_weight, a.wide, v, g, at[v].col, n, 1.0f);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            t0[v][j] = t1[v][j] = anw[v][j] = anb[v][j] = 0.0f;
+            if constexpr (SUMS && POST && NG > 1)
+                post_sums[0][own_slot<G, V>(v) + j] = post_sums[1][own_slot<G, V>(v) + j] = 0.0f;
+        }
     }
-    const bool use_z = POST || a.dgate;
+    __syncthreads();
+    float* part = a.part ? a.part + (int64_t)blockIdx.x * 4 * n : nullptr;
     const int64_t items = a.gates * a.shares;
-    const int64_t unit = a.by_group ? (int64_t)blockIdx.x * NG + grp : blockIdx.x;
-    const int64_t units = a.by_group ? (int64_t)gridDim.x * NG : gridDim.x;
+    const int64_t own = a.by_group ? grp : 0, units = (int64_t)gridDim.x * (a.by_group ? NG : 1);
     const int step = a.by_group ? 1 : NG, off = a.by_group ? 0 : grp;
     const int64_t trips = ((a.gate_rows + a.shares - 1) / a.shares + step - 1) / step;
+    bool begun = false;
     // Every thread of a block makes the same trips and meets every barrier; an
     // item or a row past the last counts as one whose results are not written.
-    for (int64_t first = a.by_group ? (int64_t)blockIdx.x * NG : blockIdx.x; first < items;
-         first += units) {
-        const int64_t index = first + (unit - (a.by_group ? (int64_t)blockIdx.x * NG : blockIdx.x));
+    for (int64_t first = (int64_t)blockIdx.x * (a.by_group ? NG : 1); first < items; first += units) {
+        const int64_t index = first + own;
         const bool live = index < items;
         const Item it = item_of(a, live ? index : items - 1);
+        const char* gate = a.gate ? gate_of(a, it.gate) : nullptr;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            load_params(a.gate ? gate_of(a, it.gate) : nullptr, a.wide, (v * G + g) * C, n, 1.0f,
-                        gate[v]);
-        for (int64_t t = 0; t < trips; ++t) {
-            int64_t row = it.first + off + t * step;
-            const bool in = live && row < it.end;
-            row = in ? row : it.first;
-            Chunk<TS, SMALL> ry[V], rdy[V];
-            Chunk<TB, SMALL> rz[V], rdo[V];
+        for (int v = 0; v < V; ++v) {
+            load_params(gate, a.wide, at[v].col, n, 1.0f, gw[v]);
+            float w[C];
+            load_params(POST ? a.post_weight : nullptr, a.wide, at[v].col, n, 1.0f, w);
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                gw[v][j] *= a.scale * w[j];
+        }
+        Chunk<TS> ry[V], rdy[V];
+        Chunk<TB> rz[V], rdo[V];
+        float ym = 0.0f, yr = 0.0f, zm = 0.0f, zr = 0.0f;
+        auto row_of = [&](int64_t t) {
+            const int64_t row = it.first + off + t * step;
+            return live && row < it.end ? row : it.first;
+        };
+        auto load_upper = [&](int64_t row) {
             const TS* y = static_cast<const TS*>(a.x) + row * a.ldx;
+            const TB* dout = static_cast<const TB*>(a.dout) + row * a.lddout;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                ry[v].load(y, at[v].col);
+                rdo[v].load(dout, at[v].col);
+            }
+            ym = a.pre_mean[row];
+            yr = a.pre_rstd[row];
+        };
+        auto load_lower = [&](int64_t row) {
             const TS* dy = static_cast<const TS*>(a.dy) + row * a.lddy;
             const TB* z = static_cast<const TB*>(a.z) + row * a.ldz;
-            const TB* dout = static_cast<const TB*>(a.dout) + row * a.lddout;
-            float ym = 0.0f, yr = 0.0f, zm = 0.0f, zr = 0.0f;
-            if constexpr (PRE) {
-                ym = a.center ? a.pre_mean[row] : 0.0f;
-                yr = a.pre_rstd[row];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                rdy[v].load(dy, at[v].col);
+                if constexpr (Z)
+                    rz[v].load(z, at[v].col);
             }
             if constexpr (POST) {
-                zm = a.center ? a.post_mean[row] : 0.0f;
+                zm = a.post_mean[row];
                 zr = a.post_rstd[row];
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e0 = (v * G + g) * C;
-                if constexpr (PRE) {
-                    ry[v].load(y, e0, n);
-                    rdo[v].load(dout, e0, n);
-                }
-                if (a.dy)
-                    rdy[v].load(dy, e0, n);
-                if (use_z)
-                    rz[v].load(z, e0, n);
-            }
+        };
+        if constexpr (PRE)
+            load_upper(row_of(0));
+        else
+            load_lower(row_of(0));
+        for (int64_t t = 0; t < trips; ++t) {
+            const int64_t row = row_of(t), next = row_of(t + 1 < trips ? t + 1 : t);
+            const bool in = live && it.first + off + t * step < it.end;
             float e[V][C];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (a.dy)
-                    rdy[v].values(e[v], (v * G + g) * C, n);
-                else
-#pragma unroll
-                    for (int j = 0; j < C; ++j)
-                        e[v][j] = 0.0f;
-            }
-            if constexpr (PRE) {
-                float s[2] = {0.0f, 0.0f};
-                float h[V][C], c[V][C];
+            auto unpack_dy = [&]() {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const int e0 = (v * G + g) * C;
-                    ry[v].values(h[v], e0, n);
-                    normalize(h[v], ym, yr, e0, n);
-                    rdo[v].values(c[v], e0, n);
+                    rdy[v].keep(a.dy_mask);
+                    rdy[v].values(e[v]);
+                }
+            };
+            if constexpr (PRE) {
+                load_lower(row);
+                __builtin_amdgcn_sched_barrier(0);
+                float s[2] = {0.0f, 0.0f};
+                float h[V][C], c[V][C];
+                // (Without center the mean's place holds something else.)
+                const float mean = a.center ? ym : 0.0f, rstd = yr;
 #pragma unroll
-                    for (int j = 0; j < C; ++j) {
-                        if (SUMS && in) {
+                for (int v = 0; v < V; ++v) {
+                    ry[v].values(h[v]);
+                    rdo[v].values(c[v]);
+                    float w[C];
+                    nw.get(v, g, w);
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        h[v][j] = (h[v][j] - mean) * rstd;
+                    if (SUMS && in) {
+                        stay_branch();
+#pragma unroll
+                        for (int j = 0; j < C; ++j) {
                             anw[v][j] = fmaf(c[v][j], h[v][j], anw[v][j]);
                             anb[v][j] += c[v][j];
                         }
-                        c[v][j] *= nw[v][j];
-                        s[0] += c[v][j];
-                        s[1] = fmaf(c[v][j], h[v][j], s[1]);
                     }
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        c[v][j] *= w[j];
+                    s[0] += chunk_sum(at[v], [&](int j, float f) { return f + c[v][j]; });
+                    s[1] += chunk_sum(at[v], [&](int j, float f) { return fmaf(c[v][j], h[v][j], f); });
                 }
                 row_sum<G>(s, lds, turn);
                 const float m1 = a.center ? s[0] * a.inv_n : 0.0f, m2 = s[1] * a.inv_n;
@@ -551,51 +810,56 @@ __global__ __launch_bounds__(Block<G>::kThreads) void rn_bwd_kernel(const RnArgs
                     a.means[2 * row] = m1;
                     a.means[2 * row + 1] = m2;
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                unpack_dy();
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
+                for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int j = 0; j < C; ++j)
-                        e[v][j] = fmaf(yr, (c[v][j] - m1) - h[v][j] * m2, e[v][j]);
-                    cut(e[v], (v * G + g) * C, n);
-                }
+                        e[v][j] = fmaf(rstd, (c[v][j] - m1) - h[v][j] * m2, e[v][j]);
+                load_upper(next);
+            } else {
+                unpack_dy();
             }
             TS* dx = static_cast<TS*>(a.y) + row * a.ldy;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float f[C];
 #pragma unroll
-                for (int j = 0; j < C; ++j) {
+                for (int j = 0; j < C; ++j)
                     f[j] = a.skip * e[v][j];
-                    e[v][j] *= a.scale;
-                }
-                if (in)
-                    store_row(dx, (v * G + g) * C, n, f);
+                if (in && !at[v].none())
+                    store8(dx, at[v].col, f);
             }
+            __builtin_amdgcn_sched_barrier(0);
             float h[V][C], s[2] = {0.0f, 0.0f};
+            const float mean = a.center ? zm : 0.0f, rstd = zr;
+            if constexpr (Z)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    rz[v].values(h[v]);
+            if constexpr (!PRE)
+                load_lower(next);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int e0 = (v * G + g) * C;
-                if (use_z)
-                    rz[v].values(h[v], e0, n);
                 if constexpr (POST)
-                    normalize(h[v], zm, zr, e0, n);
 #pragma unroll
-                for (int j = 0; j < C; ++j) {
-                    // e: t, then q, then (POST) q w_post.
-                    if (SUMS && in && a.dgate)
-                        ag[v][j] = fmaf(e[v][j],
-                                        POST ? fmaf(h[v][j], qw[v][j], qb[v][j]) : h[v][j],
-                                        ag[v][j]);
-                    e[v][j] *= gate[v][j];
-                    if constexpr (POST) {
-                        if (SUMS && in) {
-                            aqw[v][j] = fmaf(e[v][j], h[v][j], aqw[v][j]);
-                            aqb[v][j] += e[v][j];
-                        }
-                        e[v][j] *= qw[v][j];
-                        s[0] += e[v][j];
-                        s[1] = fmaf(e[v][j], h[v][j], s[1]);
+                    for (int j = 0; j < C; ++j)
+                        h[v][j] = (h[v][j] - mean) * rstd;
+                if (SUMS && Z && in) {
+                    stay_branch();
+#pragma unroll
+                    for (int j = 0; j < C; ++j) {
+                        t0[v][j] += e[v][j];
+                        t1[v][j] = fmaf(e[v][j], h[v][j], t1[v][j]);
                     }
+                }
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    e[v][j] *= gw[v][j];
+                if constexpr (POST) {
+                    s[0] += chunk_sum(at[v], [&](int j, float f) { return f + e[v][j]; });
+                    s[1] += chunk_sum(at[v], [&](int j, float f) { return fmaf(e[v][j], h[v][j], f); });
                 }
             }
             if constexpr (POST) {
@@ -605,90 +869,108 @@ __global__ __launch_bounds__(Block<G>::kThreads) void rn_bwd_kernel(const RnArgs
                 for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int j = 0; j < C; ++j)
-                        e[v][j] = zr * ((e[v][j] - m1) - h[v][j] * m2);
+                        e[v][j] = rstd * ((e[v][j] - m1) - h[v][j] * m2);
             }
             TB* dz = static_cast<TB*>(a.o) + row * a.ldo;
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (in)
-                    store_row(dz, (v * G + g) * C, n, e[v]);
+                if (in && !at[v].none())
+                    store8(dz, at[v].col, e[v]);
         }
-        if (SUMS && a.dgate) {
-            // The gate's gradient of this item.
-            auto put = [&](int col, float f) {
-                if (a.gate_part)
-                    a.gate_part[index * n + col] = f;
-                else
-                    put_param(a.dgate, a.wide, it.gate * n + col, f);
-            };
-            if constexpr (NG > 1)
-                if (!a.by_group) {
-                    __syncthreads();  // of the item before
+        if constexpr (!(SUMS && Z))
+            continue;
+        // What the item's two sums give.  The item's last row may have been the
+        // last row of other groups, not of this one: no barrier is needed, the
+        // sums are the thread's own.
+        float f[V][C], b[C];
+        if (a.dgate) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v) {
+                load_params(POST ? a.post_weight : nullptr, a.wide, at[v].col, n, 1.0f, f[v]);
+                load_params(POST ? a.post_bias : nullptr, a.wide, at[v].col, n, 0.0f, b);
 #pragma unroll
-                        for (int j = 0; j < C; ++j)
-                            sums[grp * (G * V * C) + (v * G + g) * C + j] = ag[v][j];
-                    __syncthreads();
-                    for (int col = threadIdx.x; col < n; col += T) {
-                        float f = 0.0f;
-                        for (int k = 0; k < NG; ++k)
-                            f += sums[k * (G * V * C) + col];
-                        put(col, f);
-                    }
-                }
-            if (NG == 1 || a.by_group) {
+                for (int j = 0; j < C; ++j)
+                    f[v][j] = a.scale * (POST ? fmaf(f[v][j], t1[v][j], b[j] * t0[v][j]) : t1[v][j]);
+            }
+            void* to = a.gate_part ? static_cast<void*>(a.gate_part) : a.dgate;
+            const int wide = a.gate_part ? 1 : a.wide;
+            const int64_t at0 = (a.gate_part ? index : it.gate) * n;
+            if (NG > 1 && !a.by_group) {
+                __syncthreads();  // of the item before
+                to_lds<G, V>(sums, f);
+                __syncthreads();
+                for (int col = threadIdx.x; col < n; col += T)
+                    put_param(to, wide, at0 + col, from_lds<G, V>(sums, col, n));
+            } else if (live) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
+                    if (!at[v].none())
+                        put_params(to, wide, at0 + at[v].col, f[v]);
+            }
+        }
+        if (POST && part) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    load_params(gate, a.wide, at[v].col, n, 1.0f, f[v]);
 #pragma unroll
                     for (int j = 0; j < C; ++j)
-                        if (live && (v * G + g) * C + j < n)
-                            put((v * G + g) * C + j, ag[v][j]);
+                        f[v][j] = a.scale * f[v][j] * (k == 0 ? t1[v][j] : t0[v][j]);
+                    if constexpr (NG > 1) {
+#pragma unroll
+                        for (int j = 0; j < C; ++j)
+                            post_sums[k][own_slot<G, V>(v) + j] += f[v][j];
+                    } else if (a.dparam[k] && !at[v].none()) {
+                        // The thread's own columns of the block's partial sums.
+                        float* p = part + (int64_t)k * n;
+                        if (begun) {
+                            load_params(p, 1, at[v].col, n, 0.0f, b);
+#pragma unroll
+                            for (int j = 0; j < C; ++j)
+                                f[v][j] += b[j];
+                        }
+                        store8(p, at[v].col, f[v]);
+                    }
+                }
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int j = 0; j < C; ++j)
-                    ag[v][j] = 0.0f;
+            begun = true;
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                t0[v][j] = t1[v][j] = 0.0f;
     }
-    if (!SUMS || !a.part)
+    if (!SUMS || !part)
         return;
-    float* part = a.part + (int64_t)blockIdx.x * 4 * n;
-    auto flush = [&](int which, const float (&f)[V][C]) {
-        if (!a.dparam[which])
-            return;
-        float* to = part + (int64_t)which * n;
-        if constexpr (NG > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int j = 0; j < C; ++j)
-                    sums[grp * (G * V * C) + (v * G + g) * C + j] = f[v][j];
-            __syncthreads();
-            for (int col = threadIdx.x; col < n; col += T) {
-                float s = 0.0f;
-                for (int k = 0; k < NG; ++k)
-                    s += sums[k * (G * V * C) + col];
-                to[col] = s;
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int j = 0; j < C; ++j)
-                    if ((v * G + g) * C + j < n)
-                        to[(v * G + g) * C + j] = f[v][j];
-        }
-    };
-    if constexpr (POST) {
-        flush(0, aqw);
-        flush(1, aqb);
-    }
     if constexpr (PRE) {
-        flush(2, anw);
-        flush(3, anb);
+#pragma unroll
+        for (int k = 2; k < 4; ++k) {
+            const float(&f)[V][C] = k == 2 ? anw : anb;
+            if (!a.dparam[k])
+                continue;
+            float* to = part + (int64_t)k * n;
+            if constexpr (NG > 1) {
+                __syncthreads();
+                to_lds<G, V>(sums, f);
+                __syncthreads();
+                for (int col = threadIdx.x; col < n; col += T)
+                    to[col] = from_lds<G, V>(sums, col, n);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (!at[v].none())
+                        store8(to, at[v].col, f[v]);
+            }
+        }
+    }
+    if constexpr (POST && NG > 1) {
+        __syncthreads();
+        for (int k = 0; k < 2; ++k)
+            if (a.dparam[k])
+                for (int col = threadIdx.x; col < n; col += T)
+                    part[(int64_t)k * n + col] = from_lds<G, V>(post_sums[k], col, n);
     }
 }
 
@@ -723,28 +1005,28 @@ __global__ __launch_bounds__(1024) void rn_bwd_long_kernel(const RnArgs a)
         };
         // do w_pre and yhat; q w_post and zhat.
         auto of_pre = [&](int e0, float* c, float* h) {
-            Chunk<TS, true> y;
-            Chunk<TB, true> d;
-            y.load(static_cast<const TS*>(a.x) + row * a.ldx, e0, n);
-            d.load(static_cast<const TB*>(a.dout) + row * a.lddout, e0, n);
+            Chunk<TS> y;
+            Chunk<TB> d;
+            y.load_cut(static_cast<const TS*>(a.x) + row * a.ldx, e0, n);
+            d.load_cut(static_cast<const TB*>(a.dout) + row * a.lddout, e0, n);
             float w[C];
             load_params(a.pre_weight, a.wide, e0, n, 1.0f, w);
-            y.values(h, e0, n);
+            y.values(h);
             normalize(h, ym, yr, e0, n);
-            d.values(c, e0, n);
+            d.values(c);
 #pragma unroll
             for (int j = 0; j < C; ++j)
                 c[j] *= w[j];
         };
         float sy[2] = {0.0f, 0.0f}, sz[2] = {0.0f, 0.0f};
         auto of_e = [&](int e0, float* e) {
-            Chunk<TS, true> d;
+            Chunk<TS> d;
 #pragma unroll
             for (int j = 0; j < C; ++j)
                 e[j] = 0.0f;
-            if (a.dy) {
-                d.load(static_cast<const TS*>(a.dy) + row * a.lddy, e0, n);
-                d.values(e, e0, n);
+            if (a.dy_mask) {
+                d.load_cut(static_cast<const TS*>(a.dy) + row * a.lddy, e0, n);
+                d.values(e);
             }
             if constexpr (PRE) {
                 float c[C], h[C];
@@ -755,11 +1037,11 @@ __global__ __launch_bounds__(1024) void rn_bwd_long_kernel(const RnArgs a)
             }
         };
         auto of_post = [&](int e0, float* e, float* h) {
-            Chunk<TB, true> z;
-            z.load(static_cast<const TB*>(a.z) + row * a.ldz, e0, n);
+            Chunk<TB> z;
+            z.load_cut(static_cast<const TB*>(a.z) + row * a.ldz, e0, n);
             float w[C];
             load_params(a.post_weight, a.wide, e0, n, 1.0f, w);
-            z.values(h, e0, n);
+            z.values(h);
             normalize(h, zm, zr, e0, n);
 #pragma unroll
             for (int j = 0; j < C; ++j)
@@ -812,7 +1094,7 @@ __global__ __launch_bounds__(1024) void rn_bwd_long_kernel(const RnArgs a)
 #pragma unroll
             for (int j = 0; j < C; ++j)
                 f[j] = a.skip * e[j];
-            store_row(static_cast<TS*>(a.y) + row * a.ldy, e0, n, f);
+            store_cut(static_cast<TS*>(a.y) + row * a.ldy, e0, n, f);
             of_q(e0, e);
             if constexpr (POST) {
                 of_post(e0, e, h);
@@ -820,7 +1102,7 @@ __global__ __launch_bounds__(1024) void rn_bwd_long_kernel(const RnArgs a)
                 for (int j = 0; j < C; ++j)
                     e[j] = zr * ((e[j] - sz[0]) - h[j] * sz[1]);
             }
-            store_row(static_cast<TB*>(a.o) + row * a.ldo, e0, n, e);
+            store_cut(static_cast<TB*>(a.o) + row * a.ldo, e0, n, e);
         });
     }
 }
@@ -849,29 +1131,29 @@ __global__ __launch_bounds__(256) void rn_cols_kernel(const RnArgs a)
         const Item it = item_of(a, index);
         load_params(a.gate ? gate_of(a, it.gate) : nullptr, a.wide, e0, n, 1.0f, gate);
         for (int64_t row = it.first; row < it.end; ++row) {
-            Chunk<TS, true> ry, rdy;
-            Chunk<TB, true> rz, rdo;
+            Chunk<TS> ry, rdy;
+            Chunk<TB> rz, rdo;
             if constexpr (PRE) {
-                ry.load(static_cast<const TS*>(a.x) + row * a.ldx, e0, n);
-                rdo.load(static_cast<const TB*>(a.dout) + row * a.lddout, e0, n);
+                ry.load_cut(static_cast<const TS*>(a.x) + row * a.ldx, e0, n);
+                rdo.load_cut(static_cast<const TB*>(a.dout) + row * a.lddout, e0, n);
             }
             if (use_z) {
-                if (a.dy)
-                    rdy.load(static_cast<const TS*>(a.dy) + row * a.lddy, e0, n);
-                rz.load(static_cast<const TB*>(a.z) + row * a.ldz, e0, n);
+                if (a.dy_mask)
+                    rdy.load_cut(static_cast<const TS*>(a.dy) + row * a.lddy, e0, n);
+                rz.load_cut(static_cast<const TB*>(a.z) + row * a.ldz, e0, n);
             }
             float e[C], h[C];
 #pragma unroll
             for (int j = 0; j < C; ++j)
                 e[j] = 0.0f;
-            if (use_z && a.dy)
-                rdy.values(e, e0, n);
+            if (use_z && a.dy_mask)
+                rdy.values(e);
             if constexpr (PRE) {
                 float c[C];
                 const float yr = a.pre_rstd[row], m1 = a.means[2 * row], m2 = a.means[2 * row + 1];
-                ry.values(h, e0, n);
+                ry.values(h);
                 normalize(h, a.center ? a.pre_mean[row] : 0.0f, yr, e0, n);
-                rdo.values(c, e0, n);
+                rdo.values(c);
 #pragma unroll
                 for (int j = 0; j < C; ++j) {
                     acc[2][j] = fmaf(c[j], h[j], acc[2][j]);
@@ -881,7 +1163,7 @@ __global__ __launch_bounds__(256) void rn_cols_kernel(const RnArgs a)
             }
             if (!use_z)
                 continue;
-            rz.values(h, e0, n);
+            rz.values(h);
             if constexpr (POST)
                 normalize(h, a.center ? a.post_mean[row] : 0.0f, a.post_rstd[row], e0, n);
 #pragma unroll
@@ -978,48 +1260,58 @@ __global__ __launch_bounds__(512) void rn_sums_kernel(const RnArgs a)
 // threads on a CU.
 constexpr int kMaxParts = 512;
 // Most blocks of the forward, each keeping its columns of the parameters.
-constexpr int kFwdBlocks = 1024;
+constexpr int kFwdBlocks = 512;
 // Most blocks of the kernels of 1024 threads that loop over what is left: a
 // launch has fewer than 2^32 threads.
 constexpr int64_t kMaxGrid = 1 << 21;
 constexpr int kSumsWidth = 8192;   // widest rows whose sums stay in registers
 constexpr int kRowWidth = 16384;   // widest rows that do
 
-template <typename TS, typename TB, bool POST, bool PRE, int G, int V>
+template <typename TS, typename TB, bool POST, bool PRE, int G, int V, int R>
 int fwd_launch(RnArgs& a, hipStream_t stream)
 {
-    int64_t grid = (a.rows + Block<G>::kGroups - 1) / Block<G>::kGroups;
+    constexpr int NG = Block<G>::kGroups;
+    int64_t grid = (a.rows + NG * R - 1) / (NG * R);
     if (grid > kFwdBlocks)
         grid = kFwdBlocks;
     void* args[] = {&a};
-    return launch(reinterpret_cast<const void*>(&rn_fwd_kernel<TS, TB, POST, PRE, G, V>),
+    return launch(reinterpret_cast<const void*>(&rn_fwd_kernel<TS, TB, POST, PRE, G, V, R>),
                   dim3((unsigned)grid), Block<G>::kThreads, args, stream);
 }
 
-// The smallest group whose chunks hold the row.
+template <typename TS, typename TB, bool POST, bool PRE>
+int fwd_long(RnArgs& a, hipStream_t stream)
+{
+    void* args[] = {&a};
+    return launch(reinterpret_cast<const void*>(&rn_fwd_long_kernel<TS, TB, POST, PRE>),
+                  dim3((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)), 1024, args, stream);
+}
+
+// The smallest group whose chunks hold the row (rows shorter than a chunk as
+// long ones).
 template <typename TS, typename TB, bool POST, bool PRE>
 int fwd_run(RnArgs& a, hipStream_t stream)
 {
     const int n = a.n;
+    if (n < C)
+        return fwd_long<TS, TB, POST, PRE>(a, stream);
     if (n <= 64)
-        return fwd_launch<TS, TB, POST, PRE, 8, 1>(a, stream);
+        return fwd_launch<TS, TB, POST, PRE, 8, 1, 2>(a, stream);
     if (n <= 256)
-        return fwd_launch<TS, TB, POST, PRE, 32, 1>(a, stream);
+        return fwd_launch<TS, TB, POST, PRE, 32, 1, 2>(a, stream);
     if (n <= 512)
-        return fwd_launch<TS, TB, POST, PRE, 64, 1>(a, stream);
+        return fwd_launch<TS, TB, POST, PRE, 64, 1, 2>(a, stream);
     if (n <= 1024)
-        return fwd_launch<TS, TB, POST, PRE, 128, 1>(a, stream);
+        return fwd_launch<TS, TB, POST, PRE, 128, 1, 2>(a, stream);
     if (n <= 2048)
-        return fwd_launch<TS, TB, POST, PRE, 256, 1>(a, stream);
+        return fwd_launch<TS, TB, POST, PRE, 256, 1, 2>(a, stream);
     if (n <= 4096)
-        return fwd_launch<TS, TB, POST, PRE, 512, 1>(a, stream);
+        return fwd_launch<TS, TB, POST, PRE, 512, 1, 2>(a, stream);
     if (n <= 8192)
-        return fwd_launch<TS, TB, POST, PRE, 1024, 1>(a, stream);
+        return fwd_launch<TS, TB, POST, PRE, 1024, 1, 2>(a, stream);
     if (n <= kRowWidth)
-        return fwd_launch<TS, TB, POST, PRE, 1024, 2>(a, stream);
-    void* args[] = {&a};
-    return launch(reinterpret_cast<const void*>(&rn_fwd_long_kernel<TS, TB, POST, PRE>),
-                  dim3((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)), 1024, args, stream);
+        return fwd_launch<TS, TB, POST, PRE, 1024, 2, 1>(a, stream);
+    return fwd_long<TS, TB, POST, PRE>(a, stream);
 }
 
 int sums_launch(RnArgs& a, hipStream_t stream)
@@ -1061,73 +1353,81 @@ void plan_items(RnArgs& a, int64_t groups, int64_t& blocks)
     a.parts = (int)blocks;
 }
 
-template <typename TS, typename TB, bool POST, bool PRE, int G, int V, bool SUMS>
+template <typename TS, typename TB, bool POST, bool PRE, bool Z, int G, int V, bool SUMS>
 int bwd_launch(RnArgs& a, hipStream_t stream)
 {
     int64_t blocks;
     RnArgs b = a;
     plan_items(b, Block<G>::kGroups, blocks);
     void* args[] = {&b};
-    if (!SUMS) {  // a block a row; items are the other kernel's
-        b.shares = b.gate_rows;
-        b.by_group = 0;
-        const int64_t rows = a.rows < kMaxGrid ? a.rows : kMaxGrid;
-        blocks = rows;
-    }
-    int rc = launch(reinterpret_cast<const void*>(&rn_bwd_kernel<TS, TB, POST, PRE, G, V, SUMS>),
+    int rc = launch(reinterpret_cast<const void*>(&rn_bwd_kernel<TS, TB, POST, PRE, Z, G, V, SUMS>),
                     dim3((unsigned)blocks), Block<G>::kThreads, args, stream);
     if (rc != MESWISH_OK || !SUMS || !(wants_params(b) || (b.dgate && b.gate_part)))
         return rc;
     return sums_launch(b, stream);
 }
 
+// The sums over rows by themselves.
 template <typename TS, typename TB, bool POST, bool PRE>
-int bwd_run(RnArgs& a, hipStream_t stream)
+int cols_launch(RnArgs& a, hipStream_t stream)
 {
-    const int n = a.n;
-    if (n <= 64)
-        return bwd_launch<TS, TB, POST, PRE, 8, 1, true>(a, stream);
-    if (n <= 256)
-        return bwd_launch<TS, TB, POST, PRE, 32, 1, true>(a, stream);
-    if (n <= 512)
-        return bwd_launch<TS, TB, POST, PRE, 64, 1, true>(a, stream);
-    if (n <= 1024)
-        return bwd_launch<TS, TB, POST, PRE, 128, 1, true>(a, stream);
-    if (n <= 2048)
-        return bwd_launch<TS, TB, POST, PRE, 256, 1, true>(a, stream);
-    if (n <= 4096)
-        return bwd_launch<TS, TB, POST, PRE, 512, 1, true>(a, stream);
-    if (n <= kSumsWidth)
-        return bwd_launch<TS, TB, POST, PRE, 1024, 1, true>(a, stream);
-    int rc;
-    if (n <= kRowWidth) {
-        rc = bwd_launch<TS, TB, POST, PRE, 1024, 2, false>(a, stream);
-    } else {
-        void* args[] = {&a};
-        rc = launch(reinterpret_cast<const void*>(&rn_bwd_long_kernel<TS, TB, POST, PRE>),
-                    dim3((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)), 1024, args, stream);
-    }
-    if (rc != MESWISH_OK || !(a.dgate || wants_params(a)))
-        return rc;
+    if (!a.dgate && !wants_params(a))
+        return MESWISH_OK;
     int64_t blocks;
     plan_items(a, 1, blocks);
     void* args[] = {&a};
-    const int64_t cols = ((int64_t)n + 256 * C - 1) / (256 * C);
-    rc = launch(reinterpret_cast<const void*>(&rn_cols_kernel<TS, TB, POST, PRE>),
-                dim3((unsigned)cols, (unsigned)blocks), 256, args, stream);
+    const int64_t cols = ((int64_t)a.n + 256 * C - 1) / (256 * C);
+    const int rc = launch(reinterpret_cast<const void*>(&rn_cols_kernel<TS, TB, POST, PRE>),
+                          dim3((unsigned)cols, (unsigned)blocks), 256, args, stream);
     if (rc != MESWISH_OK || !(wants_params(a) || (a.dgate && a.gate_part)))
         return rc;
     return sums_launch(a, stream);
+}
+
+template <typename TS, typename TB, bool POST, bool PRE>
+int bwd_long(RnArgs& a, hipStream_t stream)
+{
+    void* args[] = {&a};
+    const int rc = launch(reinterpret_cast<const void*>(&rn_bwd_long_kernel<TS, TB, POST, PRE>),
+                          dim3((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)), 1024, args, stream);
+    return rc == MESWISH_OK ? cols_launch<TS, TB, POST, PRE>(a, stream) : rc;
+}
+
+template <typename TS, typename TB, bool POST, bool PRE, bool Z>
+int bwd_run(RnArgs& a, hipStream_t stream)
+{
+    const int n = a.n;
+    if (n < C)
+        return bwd_long<TS, TB, POST, PRE>(a, stream);
+    if (n <= 64)
+        return bwd_launch<TS, TB, POST, PRE, Z, 8, 1, true>(a, stream);
+    if (n <= 256)
+        return bwd_launch<TS, TB, POST, PRE, Z, 32, 1, true>(a, stream);
+    if (n <= 512)
+        return bwd_launch<TS, TB, POST, PRE, Z, 64, 1, true>(a, stream);
+    if (n <= 1024)
+        return bwd_launch<TS, TB, POST, PRE, Z, 128, 1, true>(a, stream);
+    if (n <= 2048)
+        return bwd_launch<TS, TB, POST, PRE, Z, 256, 1, true>(a, stream);
+    if (n <= 4096)
+        return bwd_launch<TS, TB, POST, PRE, Z, 512, 1, true>(a, stream);
+    if (n <= kSumsWidth)
+        return bwd_launch<TS, TB, POST, PRE, Z, 1024, 1, true>(a, stream);
+    if (n > kRowWidth)
+        return bwd_long<TS, TB, POST, PRE>(a, stream);
+    const int rc = bwd_launch<TS, TB, POST, PRE, Z, 1024, 2, false>(a, stream);
+    return rc == MESWISH_OK ? cols_launch<TS, TB, POST, PRE>(a, stream) : rc;
 }
 
 template <typename TS, typename TB, bool BWD>
 int run_norms(RnArgs& a, bool post, bool pre, hipStream_t stream)
 {
     if constexpr (BWD) {
-        if (post && pre)
-            return bwd_run<TS, TB, true, true>(a, stream);
-        return post ? bwd_run<TS, TB, true, false>(a, stream)
-                    : bwd_run<TS, TB, false, true>(a, stream);
+        if (post)
+            return pre ? bwd_run<TS, TB, true, true, true>(a, stream)
+                       : bwd_run<TS, TB, true, false, true>(a, stream);
+        return a.dgate ? bwd_run<TS, TB, false, true, true>(a, stream)
+                       : bwd_run<TS, TB, false, true, false>(a, stream);
     } else {
         if (post && pre)
             return fwd_run<TS, TB, true, true>(a, stream);
@@ -1230,7 +1530,7 @@ RnSpace rn_space(size_t rows, size_t n, size_t gates)
     s.part = line_up(parts * 4 * n * sizeof(float));
     // Shares of a gate's rows are kept only if there are more than one, or one gate.
     s.gate = gates > 1 && gates > (size_t)kMaxParts / 2 ? 0 : line_up(parts * n * sizeof(float));
-    s.means = n > (size_t)kSumsWidth ? line_up(2 * rows * sizeof(float)) : 0;
+    s.means = n > (size_t)kSumsWidth || n < (size_t)C ? line_up(2 * rows * sizeof(float)) : 0;
     return s;
 }
 
@@ -1315,7 +1615,7 @@ extern "C" int residual_norm_bwd(const residual_norm_op* op, const void* y, size
             return MESWISH_EINVAL;
     if (rows > 0) {
         if ((pre && !matrix_ok(y, rows, n, ldy, ss)) || (use_z && !matrix_ok(z, rows, n, ldz, bs)) ||
-            (dy && !matrix_ok(dy, rows, n, lddy, ss)) ||
+            ((dy || !pre) && !matrix_ok(dy, rows, n, lddy, ss)) ||
             (pre && !matrix_ok(dout, rows, n, lddout, bs)) || !matrix_ok(dx, rows, n, lddx, ss) ||
             !matrix_ok(dz, rows, n, lddz, bs))
             return MESWISH_EINVAL;
@@ -1353,6 +1653,11 @@ extern "C" int residual_norm_bwd(const residual_norm_op* op, const void* y, size
     a.gate_part = sp.gate ? reinterpret_cast<float*>(at + sp.part) : nullptr;
     a.means = sp.means ? reinterpret_cast<float*>(at + sp.part + sp.gate) : nullptr;
     const hipStream_t s = static_cast<hipStream_t>(stream);
+    a.dy_mask = dy ? 0xffffffffu : 0;
+    if (!dy)
+        a.dy = y, a.lddy = a.ldx;
+    if (!center)
+        a.pre_mean = a.pre_rstd, a.post_mean = a.post_rstd;
     if (rows == 0) {  // sums over nothing: zeros
         if (!a.dgate && !wants_params(a))
             return MESWISH_OK;
