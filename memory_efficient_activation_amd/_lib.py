@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -82,6 +83,10 @@ class ResidualNormOp(ctypes.Structure):
                 ("branch_dtype", ctypes.c_int), ("param_dtype", ctypes.c_int)]
 
 
+# The same as packed bytes (building a Structure of it takes 2.5 us, this 0.8).
+RESIDUAL_NORM_OP = struct.Struct("@3N5P3f6i4x")
+
+
 class MeswishError(RuntimeError):
     """A non-zero status returned by libmeswish."""
 
@@ -138,7 +143,7 @@ def _block_signatures() -> dict:
 def _finish_signatures() -> dict:
     """Argument and result types of the operators that finish a block."""
     vp, sz, f, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float, ctypes.c_int
-    op = ctypes.POINTER(ResidualNormOp)
+    op = ctypes.c_char_p  # the description: packed bytes
     return {
         "linear_workspace_bytes": ([sz, sz, sz, i, i, i, i], sz),
         "linear_fwd": ([i, f, vp, sz, vp, sz, vp, vp, sz, sz, sz, sz, vp, sz, vp, sz, i, vp], i),

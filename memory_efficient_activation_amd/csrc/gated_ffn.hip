@@ -263,7 +263,7 @@ template <typename T, bool BWD, int PT, int QT, int NW>
 __global__ __launch_bounds__(NW * 64) void few_tokens_kernel(const GemmArgs<T> a)
 {
     const Gate<T, BWD> gate{a};
-    few_tokens<T, 2, PT, QT, NW>(a, [&](int m, int n, const float (&r)[2]) {
+    few_tokens<T, 2, PT, QT, NW, 4>(a, [&](int m, int n, const float (&r)[2]) {
         gate(m, n, r[0], r[1]);
     });
 }

@@ -131,19 +131,34 @@ __device__ __forceinline__ void each(const F& f, std::integer_sequence<int, I...
     (f(std::integral_constant<int, I>()), ...);
 }
 
-// A wave's results on vectors of eight, without the activations' rare branches.
-// True in a lane that met one: the wave is then done again by lin_slow, to the
-// same places (which is why y may not be the residual).  The activation is chosen
-// anew for every vector: eight copies of what loads and stores around it took
-// more registers than there are.
+// z becomes f(z), or up f'(z), without the activations' rare branches.  True in a
+// lane that met an argument of theirs (GELU below -6, Swish past 86, ...).
+template <class Op, bool BWD, bool P>
+__device__ __forceinline__ bool act8(float* z, const float* up, const Coef& k)
+{
+    float key = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        z[e] = BWD ? Op::template bwd<P>(z[e], up[e], k, key) : Op::template fwd<P>(z[e], k, key);
+    return Op::kHasRare && key > Op::template rare_thr<P>();
+}
+
+// A wave's results, in vectors of eight.  The activation is chosen anew for every
+// vector: eight copies of what loads and stores around it took more registers
+// than there are.  The result has a bit for each vector, (i, b) at i NT / 2 + b, in
+// which a lane met a rare argument: lin_rare does those again, to the same places
+// (which is why y may not be the residual).  (bf16 16384 x 4096 -> 16384, GELU
+// forward: z of standard deviation 1, where it is never needed, 1.68 ms; 1.4, where one
+// vector in ten thousand is, 1.72 against 2.12 with whole waves done again.)
 template <typename T, bool BWD, int MT, int NT>
-__device__ __forceinline__ bool lin_fast(const LinArgs<T>& a, int64_t m0, int n0,
+__device__ __forceinline__ uint32_t lin_results(const LinArgs<T>& a, int64_t m0, int n0,
                                          const f32x4 (&acc)[MT][NT])
 {
     constexpr bool P = sizeof(T) == 4;
     constexpr int MH = MT < 16 / (int)sizeof(T) ? MT : 16 / (int)sizeof(T);  // rows of dy or r in flight
     const int l = late_lane();
-    bool rare = false;
+    uint32_t rare = 0;
+    static_assert(MT * NT / 2 <= 32, "a bit a vector");
     each([&](auto group) {
         constexpr int b = decltype(group)::value;
         const int c = n0 + 32 * b + 8 * (l / 16), left = a.p.rows - c;
@@ -169,16 +184,9 @@ each([&](auto part) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     o[e] = acc[i0 + t][2 * b + e / 4][e % 4] + bias[e];
-                with_act(a.act, [&](auto op) {
-                    using Op = decltype(op);
-                    float key = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        o[e] = BWD ? Op::template bwd<P>(o[e], up[e], a.coef, key)
-                                   : Op::template fwd<P>(o[e], a.coef, key);
-                    if (Op::kHasRare)
-                        rare |= key > Op::template rare_thr<P>();
-                });
+                bool met = false;
+                with_act(a.act, [&](auto op) { met = act8<decltype(op), BWD, P>(o, up, a.coef); });
+                rare |= __any(met) ? 1u << ((i0 + t) * (NT / 2) + b) : 0u;
                 if constexpr (!BWD)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -204,14 +212,16 @@ each([&](auto part) {
     return rare;
 }
 
-// The whole wave again, element by element, for the activations' rare arguments.
+// The vectors named by `rare` again, element by element.
 template <typename T, bool BWD, int MT, int NT>
-__device__ __forceinline__ void lin_slow(const LinArgs<T>& a, int64_t m0, int n0,
-                                         const f32x4 (&acc)[MT][NT])
+__device__ __forceinline__ void lin_rare(const LinArgs<T>& a, int64_t m0, int n0,
+                                         const f32x4 (&acc)[MT][NT], uint32_t rare)
 {
     const int l = late_lane();
 #pragma unroll 1
     for (int t = 0; t < MT * NT; ++t) {
+        if (!(rare >> (t / 2) & 1))
+            continue;
         const int i = t / NT, j = t % NT;
         f32x4 z = f32x4{};
 #pragma unroll
@@ -239,8 +249,9 @@ __device__ __forceinline__ void lin_epilogue(const LinArgs<T>& a, int64_t m0, in
     } else if constexpr (MODE != kLin) {
         store_results<false>(a.out[0], a.ldo[0], a.q.rows, a.out_cols, m0, n0, acc);
     } else {
-        if (__any(lin_fast<T, BWD>(a, m0, n0, acc)))
-            lin_slow<T, BWD>(a, m0, n0, acc);
+        const uint32_t rare = lin_results<T, BWD>(a, m0, n0, acc);
+        if (rare)
+            lin_rare<T, BWD>(a, m0, n0, acc, rare);
     }
 }
 
@@ -253,10 +264,15 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void lin_tiles_kernel(const LinArg
         });
 }
 
-template <typename T, bool BWD, int PT, int QT, int NW>
-__global__ __launch_bounds__(NW * 64) void lin_few_kernel(const LinArgs<T> a)
+// 16 units a block, 16 waves with a share of the sum each.  (bf16 1 x 16384 -> 4096,
+// waves and steps in flight: 16 and 2 27 us, 16 and 4 31, 8 and 4 34, 16 and 1 31, 8 and
+// 2 33; 32 units a block 41.  5.0 TB/s; 1 x 4096 -> 16384 24 us, 5.6 TB/s.)
+constexpr int kFewWaves = 16;
+
+template <typename T, bool BWD, int QT>
+__global__ __launch_bounds__(kFewWaves * 64) void lin_few_kernel(const LinArgs<T> a)
 {
-    few_tokens<T, 1, PT, QT, NW>(a, [&](int m, int n, const float (&r)[1]) {
+    few_tokens<T, 1, 1, QT, kFewWaves, 2>(a, [&](int m, int n, const float (&r)[1]) {
         if (n < a.out_cols)
             lin_one<T, BWD>(a, m, n, r[0]);
     });
@@ -406,8 +422,20 @@ bool rows_aligned(const void* p, size_t ld, size_t cols, size_t es)
     return aligned(p, 16) && ld * es % 16 == 0 && cols * es % 16 == 0;
 }
 
-// Most tokens of the kernel that reads the weight once.
-constexpr int kFewTokens = 32;
+// Whether z is computed by the kernel that reads the weight once, which takes any
+// rows.  Each of its blocks reads all of x, from the caches; tiles read x less
+// often, but split the sum and add its parts by a second kernel.  bf16, tokens x dim
+// -> units, with x times blocks:
+//   1 x 16384 -> 4096 (8 MB) 27 us against 35; 8 x 16384 -> 4096 (67 MB) 29 against
+//   35; 32 x 4096 -> 4096 (67 MB) 14.0 against 15.6; 16 x 16384 -> 4096 (134 MB) 36
+//   against 35.5; 24 x 4096 -> 16384 (201 MB) 44 against 31.5; 32 x 16384 -> 4096
+//   (268 MB) 53 against 37.
+// Rows that are not aligned would have to be copied for the tiles, the weight's too.
+bool few_tokens_call(size_t tokens, size_t dim, size_t units, size_t es, bool aligned)
+{
+    return tokens <= 32 &&
+           (!aligned || tokens * dim * es * ((units + 15) / 16) <= ((size_t)80 << 20));
+}
 
 // Shares of the rows in db's sums: about four blocks a CU, 32 rows a share at
 // the least.
@@ -420,44 +448,12 @@ int col_shares(int64_t rows, int64_t cols, size_t es)
     return (int)(s < 1 ? 1 : s);
 }
 
-// The workspace: dz in padded rows (backward with an activation), the packed
-// operands, the parts of one split sum at a time (or of db's).  Each is whole
-// 128-byte lines long.
-struct Space {
-    size_t dz, xw, dy, part;
-    size_t bytes() const { return dz + xw + dy + part; }
-};
-
-Space space(size_t tokens, size_t dim, size_t units, bool act, size_t es, bool backward, int align)
-{
-    const int64_t m = (int64_t)tokens, d = (int64_t)dim, f = (int64_t)units;
-    const bool few = tokens <= (size_t)kFewTokens;
-    Space s{};
-    // The kernel for few tokens takes any rows.
-    if (!(align & LINEAR_ALIGNED_XW) && (backward || !few))
-        s.xw = (tokens + units) * packed_ld(dim, es) * es;
-    if ((!backward || act) && !few)
-        s.part = part_bytes(kLin, m, f, d, es);
-    if (backward) {
-        if (act)
-            s.dz = lines(tokens * padded(units) * es);
-        else if (!(align & LINEAR_ALIGNED_DY))
-            s.dy = tokens * packed_ld(units, es) * es;
-        const size_t more[] = {part_bytes(kLinDx, m, d, f, es), part_bytes(kLinDw, f, d, m, es),
-                               (size_t)col_shares(m, f, es) * units * sizeof(float)};
-        for (size_t v : more)
-            s.part = s.part > v ? s.part : v;
-    }
-    s.part = lines(s.part);
-    return s;
-}
-
-template <typename T, bool BWD, int PT, int QT>
+template <typename T, bool BWD, int QT>
 int lin_few(LinArgs<T>& a, hipStream_t stream)
 {
     void* args[] = {&a};
-    return launch(reinterpret_cast<const void*>(&lin_few_kernel<T, BWD, PT, QT, 8>),
-                  dim3((unsigned)((a.out_cols + 16 * PT - 1) / (16 * PT))), 512, args, stream);
+    return launch(reinterpret_cast<const void*>(&lin_few_kernel<T, BWD, QT>),
+                  dim3((unsigned)((a.out_cols + 15) / 16)), kFewWaves * 64, args, stream);
 }
 
 template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, bool PARTS>
@@ -481,18 +477,18 @@ int lin_tiles(LinArgs<T>& a, hipStream_t stream)
                            (int64_t)a.q.rows * (a.part_ld / 4), args, stream);
 }
 
-// part: memory for the parts of a split sum; k, cols: the length and the columns
-// that the plan (and the size of that memory) goes by.
+// few: by the kernel that reads the weight once.  part: memory for the parts of a
+// split sum; k, cols: the length and the columns that the plan (and the size of
+// that memory) goes by.
 template <typename T, int MODE, bool BWD>
-int lin_product(LinArgs<T>& a, int64_t cols, int64_t k, float* part, hipStream_t stream)
+int lin_product(LinArgs<T>& a, bool few, int64_t cols, int64_t k, float* part, hipStream_t stream)
 {
     a.splits = 1;
     if (a.q.rows == 0 || a.out_cols == 0)
         return MESWISH_OK;
     if constexpr (MODE == kLin) {
-        if (a.q.rows <= kFewTokens)
-            return a.q.rows <= 16 ? lin_few<T, BWD, 1, 1>(a, stream)
-                                  : lin_few<T, BWD, 2, 2>(a, stream);
+        if (few)
+            return a.q.rows <= 16 ? lin_few<T, BWD, 1>(a, stream) : lin_few<T, BWD, 2>(a, stream);
     }
     const Plan p = make_plan(a.q.rows, cols, k, 1, 1, sizeof(T));
     a.splits = p.splits;
@@ -503,6 +499,37 @@ int lin_product(LinArgs<T>& a, int64_t cols, int64_t k, float* part, hipStream_t
                             : lin_tiles<T, MODE, BWD, 2, 4, 8, 4, false>(a, stream);
     return p.splits > 1 ? lin_tiles<T, MODE, BWD, 2, 2, 4, 4, true>(a, stream)
                         : lin_tiles<T, MODE, BWD, 2, 2, 4, 4, false>(a, stream);
+}
+
+// The workspace: dz in padded rows (backward with an activation), the packed
+// operands, the parts of one split sum at a time (or of db's).  Each is whole
+// 128-byte lines long.
+struct Space {
+    size_t dz, xw, dy, part;
+    size_t bytes() const { return dz + xw + dy + part; }
+};
+
+Space space(size_t tokens, size_t dim, size_t units, bool act, size_t es, bool backward, int align)
+{
+    const int64_t m = (int64_t)tokens, d = (int64_t)dim, f = (int64_t)units;
+    const bool few = few_tokens_call(tokens, dim, units, es, align & LINEAR_ALIGNED_XW);
+    Space s{};
+    if (!(align & LINEAR_ALIGNED_XW) && (backward || !few))
+        s.xw = (tokens + units) * packed_ld(dim, es) * es;
+    if ((!backward || act) && !few)
+        s.part = part_bytes(kLin, m, f, d, es);
+    if (backward) {
+        if (act)
+            s.dz = lines(tokens * padded(units) * es);
+        else if (!(align & LINEAR_ALIGNED_DY))
+            s.dy = tokens * packed_ld(units, es) * es;
+        const size_t more[] = {part_bytes(kLinDx, m, d, f, es), part_bytes(kLinDw, f, d, m, es),
+                               (size_t)col_shares(m, f, es) * units * sizeof(float)};
+        for (size_t v : more)
+            s.part = s.part > v ? s.part : v;
+    }
+    s.part = lines(s.part);
+    return s;
 }
 
 // Rows of a matrix as the products take them.
@@ -568,6 +595,7 @@ struct Call {
     size_t tokens, dim, units;
     void *y, *dx, *dw, *dbias;
     int64_t ldy, lddx, lddw;
+    bool few;  // tokens, for the kernel that reads the weight once
     char* workspace;
     Space space;
     hipStream_t stream;
@@ -579,7 +607,7 @@ int run(const Call& c)
     Rows<T> x{static_cast<const T*>(c.x), c.ldx, (int)c.dim};
     Rows<T> w{static_cast<const T*>(c.w), c.ldw, (int)c.dim};
     const Rows<T> x_given = x, w_given = w;
-    const bool few = c.tokens <= (size_t)kFewTokens, act = c.act != LINEAR_IDENTITY;
+    const bool few = c.few, act = c.act != LINEAR_IDENTITY;
     char* at = c.workspace;
     T* dz = reinterpret_cast<T*>(at);
     T* xw = reinterpret_cast<T*>(at += c.space.dz);
@@ -607,7 +635,7 @@ int run(const Call& c)
         a.out[0] = BWD ? dz : static_cast<T*>(c.y);
         a.ldo[0] = BWD ? fp : c.ldy;
         a.out_cols = BWD ? (int)fp : (int)c.units;
-        rc = lin_product<T, kLin, BWD>(a, (int64_t)c.units, (int64_t)c.dim, part, c.stream);
+        rc = lin_product<T, kLin, BWD>(a, few, (int64_t)c.units, (int64_t)c.dim, part, c.stream);
         if (BWD)
             d = Rows<T>{dz, fp, (int)fp};
     } else if (rc == MESWISH_OK && c.space.dy && (c.dx || c.dw)) {
@@ -622,7 +650,7 @@ int run(const Call& c)
             a.out[0] = static_cast<T*>(c.dx);
             a.ldo[0] = c.lddx;
             a.out_cols = (int)c.dim;
-            rc = lin_product<T, kLinDx, false>(a, (int64_t)c.dim, (int64_t)c.units, part, c.stream);
+            rc = lin_product<T, kLinDx, false>(a, false, (int64_t)c.dim, (int64_t)c.units, part, c.stream);
         }
         if (rc == MESWISH_OK && c.dw) {
             LinArgs<T> a{};
@@ -633,7 +661,7 @@ int run(const Call& c)
             a.out[0] = static_cast<T*>(c.dw);
             a.ldo[0] = c.lddw;
             a.out_cols = (int)c.dim;
-            rc = lin_product<T, kLinDw, false>(a, (int64_t)c.dim, (int64_t)c.tokens, part, c.stream);
+            rc = lin_product<T, kLinDw, false>(a, false, (int64_t)c.dim, (int64_t)c.tokens, part, c.stream);
         }
         if (rc == MESWISH_OK && c.dbias)
             rc = col_sums<T>(d, c.tokens, c.units, part, static_cast<T*>(c.dbias), c.stream);
@@ -699,6 +727,7 @@ extern "C" int linear_fwd(int act, float param, const void* x, size_t ldx, const
     c.tokens = tokens, c.dim = dim, c.units = units;
     c.workspace = static_cast<char*>(workspace);
     c.space = sp;
+    c.few = few_tokens_call(tokens, dim, units, es, align & LINEAR_ALIGNED_XW);
     c.stream = static_cast<hipStream_t>(stream);
     return run_dtype<false>(dtype, c);
 }
@@ -739,6 +768,7 @@ extern "C" int linear_bwd(int act, float param, const void* x, size_t ldx, const
     c.tokens = tokens, c.dim = dim, c.units = units;
     c.workspace = static_cast<char*>(workspace);
     c.space = sp;
+    c.few = few_tokens_call(tokens, dim, units, es, align & LINEAR_ALIGNED_XW);
     c.stream = static_cast<hipStream_t>(stream);
     return run_dtype<true>(dtype, c);
 }

@@ -702,7 +702,7 @@ __device__ __forceinline__ void product_tiles(const Args& a, const Finish& finis
                             for (int k = 0; k < lead; ++k)
                                 read_q(from, part, k);
                         read_q(from, part, i);
-                        constexpr int kP = MT > NT ? 1 : 2;  // P's fragments a row
+                        constexpr int kP = (NT + MT - BG - 1) / (MT - BG);  // P's fragments a row
 #pragma unroll
                         for (int j = (i - lead) * kP; j < (i - lead + 1) * kP && j < NT; ++j)
                             read_p(~t & 1, from, part, j);
@@ -737,12 +737,11 @@ __device__ __forceinline__ void product_tiles(const Args& a, const Finish& finis
 // Infinity Cache then holds most.
 // ---------------------------------------------------------------------------
 // H weights; finish(m, n, results of the weights) ends an element.
-template <typename T, int H, int PT, int QT, int NW, class Args, class Finish>
+template <typename T, int H, int PT, int QT, int NW, int U, class Args, class Finish>
 __device__ __forceinline__ void few_tokens(const Args& a, const Finish& finish)
 {
     typedef typename Step<T>::Frag Frag;
     constexpr int E = Elem<T>::kPerVec, kK = 64 / sizeof(T), kTiles = H * PT * QT;
-    constexpr int U = H * PT * QT > 8 ? 2 : 4;
     __shared__ float part[NW][kTiles][256];
     const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int n0 = blockIdx.x * (16 * PT);

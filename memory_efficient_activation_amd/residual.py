@@ -26,7 +26,6 @@ differentiated again (an attempt raises).
 
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple
 
 import torch
@@ -83,41 +82,65 @@ def _branch(t: torch.Tensor, x: torch.Tensor, name: str) -> int:
 
 def _gates(gate: torch.Tensor, x: torch.Tensor) -> int:
     """Rows of the gate: its shape is x's first dimensions and the last."""
-    lead = gate.dim() - 1
+    shape, lead = gate.shape, gate.dim() - 1
     if gate.dtype not in _DTYPES:
         raise TypeError(f"gate must be float32 or bfloat16, got {gate.dtype}")
-    if not 0 <= lead < x.dim() or gate.shape != (*x.shape[:lead], x.shape[-1]):
+    if not 0 <= lead < x.dim() or shape[lead] != x.shape[-1] or shape[:lead] != x.shape[:lead]:
         raise ValueError(f"gate must have the stream's first dimensions and its last "
-                         f"({tuple(x.shape)}), got {tuple(gate.shape)}")
+                         f"({tuple(x.shape)}), got {tuple(shape)}")
     if not gate.is_contiguous() or gate.get_device() != x.get_device():
         raise ValueError(f"gate must be contiguous and on {x.device}")
     gates = 1
-    for s in gate.shape[:-1]:
+    for s in shape[:lead]:
         gates *= s
     return gates
 
 
+def _same_dtype(dtype: torch.dtype | None, p: torch.Tensor) -> torch.dtype:
+    if dtype is not None and p.dtype is not dtype:
+        raise TypeError(f"weights, biases and gate have different dtypes ({dtype}, {p.dtype})")
+    return p.dtype
+
+
+def _norm_ptrs(norm, dtype, n, x, name):
+    """(weight's address, bias's, the parameters' dtype so far); 0: none."""
+    w, b = norm
+    wp = bp = 0
+    if w is not None:
+        dtype = _same_dtype(dtype, w)
+        wp = _param(w, n, x, name + "'s weight")
+    if b is not None:
+        dtype = _same_dtype(dtype, b)
+        bp = _param(b, n, x, name + "'s bias")
+    return wp, bp, dtype
+
+
 def _op(x, rows, n, code, branch, gate, post, pre, skip, scale, center, eps):
-    """(the call's description, the parameters' dtype or None)."""
+    """(the call's packed description, the parameters' dtype or None, the gate's
+    rows, whether it is used)."""
     if post is None and pre is None:
         raise ValueError("at least one of post and pre must be given")
-    qw, qb = post if post is not None else (None, None)
-    nw, nb = pre if pre is not None else (None, None)
-    dtype = None
-    for p in (gate, qw, qb, nw, nb):
-        if p is None:
-            continue
-        if dtype is None:
-            dtype = p.dtype
-        elif p.dtype is not dtype:
-            raise TypeError(f"weights, biases and gate have different dtypes ({dtype}, {p.dtype})")
-    gates = 1 if gate is None else _gates(gate, x)
-    ptrs = (_param(qw, n, x, "post's weight"), _param(qb, n, x, "post's bias"),
-            _param(nw, n, x, "pre's weight"), _param(nb, n, x, "pre's bias"))
-    # (A gate of no rows, [0, n], beside no rows of x.)
-    return _lib.ResidualNormOp(rows, n, gates or 1, _ptr(gate) if gates else None, *ptrs, skip,
-                               scale, eps, post is not None, pre is not None, bool(center), code,
-                               branch, _DTYPES[dtype] if dtype is not None else _lib.F32), dtype
+    dtype, gates, gp = None, 1, 0
+    if gate is not None:
+        dtype, gates = gate.dtype, _gates(gate, x)
+        if gates:
+            gp = gate.data_ptr()
+        else:  # a gate of no rows, [0, n], beside no rows of x
+            gates = 1
+    qw = qb = nw = nb = 0
+    if post is not None:
+        qw, qb, dtype = _norm_ptrs(post, dtype, n, x, "post")
+    if pre is not None:
+        nw, nb, dtype = _norm_ptrs(pre, dtype, n, x, "pre")
+    return (_lib.RESIDUAL_NORM_OP.pack(rows, n, gates, gp, qw, qb, nw, nb, skip, scale, eps,
+                                       post is not None, pre is not None, bool(center), code,
+                                       branch, 0 if dtype is None else _DTYPES[dtype]),
+            dtype, gates, gp != 0)
+
+
+def _new_like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t) if t.is_contiguous() else \
+        torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def residual_norm_fwd(x: torch.Tensor, z: torch.Tensor, gate: torch.Tensor | None = None,
@@ -132,18 +155,40 @@ def residual_norm_fwd(x: torch.Tensor, z: torch.Tensor, gate: torch.Tensor | Non
     x, rows, n, ldx = as_rows(x, "x")
     branch = _branch(z, x, "z")
     z, _, _, ldz = as_rows(z, "z")
-    op, _ = _op(x, rows, n, code, branch, gate, post, pre, scale=scale, skip=skip, center=center,
-                eps=eps)
+    op = _op(x, rows, n, code, branch, gate, post, pre, skip, scale, center, eps)[0]
     device, lead = x.device, x.shape[:-1]
-    y = torch.empty(x.shape, dtype=x.dtype, device=device)
-    o = None if pre is None else torch.empty(x.shape, dtype=z.dtype, device=device)
-    used = (post is not None and center, post is not None, pre is not None and center,
-            pre is not None)
-    planes = iter(torch.empty((sum(used), *lead), dtype=torch.float32, device=device).unbind(0))
-    stats = RowStats(*(next(planes) if u else None for u in used))
-    launch("residual_norm_fwd", "residual_norm_fwd", device, ctypes.byref(op), x.data_ptr(), ldx,
-           z.data_ptr(), ldz, y.data_ptr(), n, _ptr(o), n, *map(_ptr, stats))
-    return y, o, stats
+    y = _new_like(x)
+    o = op_ = qm = qr = nm = nr = None
+    k = 2 if center else 1
+    both = post is not None and pre is not None
+    planes = torch.empty((2 * k if both else k, *lead), dtype=torch.float32, device=device).unbind(0)
+    if pre is not None:
+        o = _new_like(z)
+        op_, nr = o.data_ptr(), planes[-1]
+        nm = planes[-2] if center else None
+    if post is not None:
+        qr, qm = planes[k - 1], planes[0] if center else None
+    launch("residual_norm_fwd", "residual_norm_fwd", device, op, x.data_ptr(), ldx, z.data_ptr(),
+           ldz, y.data_ptr(), n, op_, n, _ptr(qm), _ptr(qr), _ptr(nm), _ptr(nr))
+    return y, o, RowStats(qm, qr, nm, nr)
+
+
+def _upstream(t: torch.Tensor, like: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
+    if not t.is_cuda:
+        _require_device(t, name)
+    if t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on "
+                         f"{like.device}")
+    t, _, _, ld = as_rows(t, name)
+    return t, ld
+
+
+def _stat(t: torch.Tensor | None, lead, y: torch.Tensor, name: str) -> int:
+    if t is None or t.dtype is not torch.float32 or t.shape != lead or not t.is_contiguous() \
+            or t.get_device() != y.get_device():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(lead)} on "
+                         f"{y.device}")
+    return t.data_ptr()
 
 
 def residual_norm_bwd(y: torch.Tensor, z: torch.Tensor, dy: torch.Tensor | None,
@@ -152,58 +197,52 @@ def residual_norm_bwd(y: torch.Tensor, z: torch.Tensor, dy: torch.Tensor | None,
                       skip: float = 1.0, center: bool = True, need_params: bool = True,
                       shared: SharedBuffer | None = None) -> ResidualNormGrads:
     """The gradients from y, z, the statistics the forward returned, dy = dL/dy
-    (None: zeros) and do = dL/do (with ``pre``).  Those of the parameters and of
-    the gate have the parameters' type; with ``need_params`` False they are None.
-    ``shared`` lends the workspace."""
+    (None, with ``pre``: zeros) and do = dL/do (with ``pre``).  Those of the
+    parameters and of the gate have the parameters' type; with ``need_params``
+    False they are None.  ``shared`` lends the workspace."""
     code = _dtype_code(y)
     y, rows, n, ldy = as_rows(y, "y")
     branch = _branch(z, y, "z")
     z, _, _, ldz = as_rows(z, "z")
-    op, pdtype = _op(y, rows, n, code, branch, gate, post, pre, scale=scale, skip=skip,
-                     center=center, eps=0.0)
+    op, pdtype, gates, gated = _op(y, rows, n, code, branch, gate, post, pre, skip, scale, center,
+                                   0.0)
     device, lead = y.device, y.shape[:-1]
+    dyp = dop = qm = qr = nm = nr = None
     lddy = lddo = 0
     if dy is not None:
-        if not dy.is_cuda:
-            _require_device(dy, "dy")
-        if dy.shape != y.shape or dy.dtype is not y.dtype or dy.device != device:
-            raise ValueError(f"dy must be a {y.dtype} tensor of shape {tuple(y.shape)} on {device}")
-        dy, _, _, lddy = as_rows(dy, "dy")
+        dy, lddy = _upstream(dy, y, "dy")
+        dyp = dy.data_ptr()
+    elif pre is None:
+        raise ValueError("dy must be given without pre")
     if (do is None) != (pre is None):
         raise ValueError("do must be given with pre, and only with it")
-    if do is not None:
-        if not do.is_cuda:
-            _require_device(do, "do")
-        if do.shape != y.shape or do.dtype is not z.dtype or do.device != device:
-            raise ValueError(f"do must be a {z.dtype} tensor of shape {tuple(y.shape)} on {device}")
-        do, _, _, lddo = as_rows(do, "do")
-    used = (post is not None and center, post is not None, pre is not None and center,
-            pre is not None)
-    for name, t, u in zip(RowStats._fields, stats, used):
-        if u and (t is None or t.dtype is not torch.float32 or t.shape != lead
-                  or t.device != device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(lead)} "
-                             f"on {device}")
-    given = [(post or (None, None))[0], (post or (None, None))[1], (pre or (None, None))[0],
-             (pre or (None, None))[1]]
-    dgate, dparams, ws, nbytes = None, [None] * 4, None, 0
+    if pre is not None:
+        do, lddo = _upstream(do, z, "do")
+        dop = do.data_ptr()
+        nm = _stat(stats[2], lead, y, "pre_mean") if center else None
+        nr = _stat(stats[3], lead, y, "pre_rstd")
+    if post is not None:
+        qm = _stat(stats[0], lead, y, "post_mean") if center else None
+        qr = _stat(stats[1], lead, y, "post_rstd")
+    given = (*(post or (None, None)), *(pre or (None, None)))
+    dgate, grads, ptrs = None, [None] * 4, [None] * 4
     if need_params:
         if gate is not None:
-            dgate = torch.empty(gate.shape, dtype=pdtype, device=device)
+            dgate = torch.empty_like(gate)
         count = sum(p is not None for p in given)
         if count:
             vectors = iter(torch.empty((count, n), dtype=pdtype, device=device).unbind(0))
-            dparams = [None if p is None else next(vectors) for p in given]
-    dx = torch.empty(y.shape, dtype=y.dtype, device=device)
-    dz = torch.empty(y.shape, dtype=z.dtype, device=device)
-    nbytes = library().residual_norm_workspace_bytes(rows, n, op.gates if op.gate else 1)
-    if nbytes:
-        ws = (shared or SharedBuffer()).workspace(nbytes, device)
-    launch("residual_norm_bwd", "residual_norm_bwd", device, ctypes.byref(op), y.data_ptr(), ldy,
-           z.data_ptr(), ldz, _ptr(dy), lddy, _ptr(do), lddo,
-           *(_ptr(t) if u else None for t, u in zip(stats, used)), dx.data_ptr(), n, dz.data_ptr(),
-           n, _ptr(dgate) if op.gate else None, *map(_ptr, dparams), _ptr(ws), nbytes)
-    return ResidualNormGrads(dx, dz, dgate, *dparams)
+            for i, p in enumerate(given):
+                if p is not None:
+                    grads[i] = g = next(vectors)
+                    ptrs[i] = g.data_ptr()
+    dx, dz = _new_like(y), _new_like(z)
+    nbytes = library().residual_norm_workspace_bytes(rows, n, gates)
+    ws = (shared or SharedBuffer()).workspace(nbytes, device)
+    launch("residual_norm_bwd", "residual_norm_bwd", device, op, y.data_ptr(), ldy, z.data_ptr(),
+           ldz, dyp, lddy, dop, lddo, qm, qr, nm, nr, dx.data_ptr(), n, dz.data_ptr(), n,
+           dgate.data_ptr() if gated and dgate is not None else None, *ptrs, ws.data_ptr(), nbytes)
+    return ResidualNormGrads(dx, dz, dgate, *grads)
 
 
 class ResidualNormFn(torch.autograd.Function):

@@ -153,7 +153,9 @@ def op(**k):
              pre_bias=NB, skip=1.0, scale=1.0, eps=1e-5, post=1, pre=1, center=1, stream_dtype=1,
              branch_dtype=1, param_dtype=0)
     d.update(k)
-    return ctypes.byref(_lib.ResidualNormOp(**d))
+    packed = _lib.RESIDUAL_NORM_OP.pack(*d.values())
+    assert packed == bytes(_lib.ResidualNormOp(**d))
+    return packed
 
 
 def rn_fwd(lib, x=X, ldx=64, z=Z, ldz=64, y=Y, ldy=64, o=O, ldo=64, s1=S1, s2=S2, s3=S3, s4=S4,
