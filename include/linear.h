@@ -78,8 +78,9 @@ int linear_fwd(int act, float param, const void *x, size_t ldx, const void *w, s
 
 /* dx [tokens, dim], dw [units, dim] and dbias [units] (overwritten, not added
  * to) from x, w, bias (NULL where the forward had none) and dy [tokens, units].
- * Any of the three may be NULL: what is NULL is not computed.  workspace:
- * 16-byte aligned, at least linear_workspace_bytes(..., 1, aligned) bytes. */
+ * Any of the three may be NULL: what is NULL is not computed.  x may be NULL
+ * where nothing reads it (no activation, and dw NULL).  workspace: 16-byte
+ * aligned, at least linear_workspace_bytes(..., 1, aligned) bytes. */
 int linear_bwd(int act, float param, const void *x, size_t ldx, const void *w, size_t ldw,
                const void *bias, const void *dy, size_t lddy, size_t tokens, size_t dim,
                size_t units, void *dx, size_t lddx, void *dw, size_t lddw, void *dbias,

@@ -17,6 +17,12 @@ declared in the headers under include/).  This package is a thin binding over it
 * ``ffn`` -- the gated feed-forward unit f(x Wg^T) * (x Wu^T), recomputed from
   its input in the backward, and the pre-normalized block of both
   (include/gated_ffn.h);
+* ``linear`` -- a matrix product with bias, activation and residual in its
+  epilogue, recomputed in the backward (include/linear.h);
+* ``residual`` -- the border between blocks: norms before and after, gate, scales
+  and the residual sum in one pass (include/residual_norm.h);
+* ``block`` -- feed-forward blocks, without a gate and as a stack with borders,
+  made of these;
 * ``naive.Swish`` -- the plain module, for comparisons;
 * ``inputs`` -- seeded synthetic workloads; ``accounting`` -- byte counts.
 
@@ -28,7 +34,7 @@ from .functional import (act_bwd, act_fwd, copy_bytes, swish_bwd, swish_bwd_grou
                          swish_fwd_grouped)
 from .module import ActFn, MemoryEfficientActivation, MemoryEfficientSwish, SwishFn, swish
 from ._lib import MeswishError
-from . import dense, ffn, norm
+from . import block, dense, ffn, linear, norm, residual
 
 __all__ = [
     "swish_fwd", "swish_bwd", "swish_fwd_grouped", "swish_bwd_grouped", "copy_bytes",

@@ -740,19 +740,20 @@ extern "C" int linear_bwd(int act, float param, const void* x, size_t ldx, const
     if (!dtype_ok(dtype) || !call_ok(act, param) || !sizes_ok(tokens, dim, units))
         return MESWISH_EINVAL;
     const size_t es = elem_size(dtype);
-    if (!matrix_ok(x, tokens, dim, ldx, es) || !matrix_ok(w, units, dim, ldw, es) ||
+    const bool reads_x = act != LINEAR_IDENTITY || dw;
+    if (((reads_x || x) && !matrix_ok(x, tokens, dim, ldx, es)) || !matrix_ok(w, units, dim, ldw, es) ||
         !aligned(bias, es) || !matrix_ok(dy, tokens, units, lddy, es) ||
         (dx && !matrix_ok(dx, tokens, dim, lddx, es)) ||
         (dw && !matrix_ok(dw, units, dim, lddw, es)) || !aligned(dbias, es))
         return MESWISH_EINVAL;
-    const int align = (rows_aligned(x, ldx, dim, es) && rows_aligned(w, ldw, dim, es)
+    const int align = ((!x || rows_aligned(x, ldx, dim, es)) && rows_aligned(w, ldw, dim, es)
                            ? LINEAR_ALIGNED_XW : 0) |
                       (rows_aligned(dy, lddy, units, es) ? LINEAR_ALIGNED_DY : 0);
     const Space sp = space(tokens, dim, units, act != LINEAR_IDENTITY, es, true, align);
     const size_t need = sp.bytes();
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return MESWISH_EINVAL;
-    const Span in[] = {span(x, tokens, dim, ldx, es), span(w, units, dim, ldw, es),
+    const Span in[] = {span(x, x ? tokens : 0, dim, ldx, es), span(w, units, dim, ldw, es),
                        span(bias, bias ? 1 : 0, units, units, es), span(dy, tokens, units, lddy, es)};
     const Span out[] = {span(dx, dx ? tokens : 0, dim, lddx, es), span(dw, dw ? units : 0, dim, lddw, es),
                         span(dbias, dbias ? 1 : 0, units, units, es),

@@ -53,10 +53,12 @@ def _like(t: torch.Tensor, shape, x: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _weight(w: torch.Tensor, x: torch.Tensor) -> tuple[torch.Tensor, int]:
+def _weight(w: torch.Tensor, x: torch.Tensor, dim: int | None) -> tuple[torch.Tensor, int]:
+    """The weight's rows; dim: their length, None: any."""
     if w.dim() != 2:
-        raise ValueError(f"weight must be [units, {x.shape[-1]}], got {tuple(w.shape)}")
-    _like(w, (w.shape[0], x.shape[-1]), x, "weight")
+        raise ValueError(f"weight must be [units, {'dim' if dim is None else dim}], got "
+                         f"{tuple(w.shape)}")
+    _like(w, w.shape if dim is None else (w.shape[0], dim), x, "weight")
     return _rows(w, "weight")
 
 
@@ -89,7 +91,7 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     workspace."""
     act, code = _code(kind), _dtype_code(x)
     x, ldx = _rows(x, "x")
-    w, ldw = _weight(weight, x)
+    w, ldw = _weight(weight, x, x.shape[-1])
     tokens, (units, dim) = _tokens(x), w.shape
     shape, device = (*x.shape[:-1], units), x.device
     b = _bias(bias, units, x)
@@ -113,30 +115,38 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     return y
 
 
-def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
+def linear_bwd(x: torch.Tensor | None, weight: torch.Tensor, dy: torch.Tensor,
                bias: torch.Tensor | None = None, kind: str | None = None,
                param: float | None = None, need_x: bool = True, need_weight: bool = True,
                need_bias: bool | None = None, shared: SharedBuffer | None = None
                ) -> tuple[torch.Tensor | None, torch.Tensor | None, torch.Tensor | None]:
     """(dx, dweight, dbias) from the input, the weight, the bias and dy = dL/dy.
     What is not needed is None; ``need_bias`` defaults to whether there is a
-    bias.  (The residual's gradient is dy.)  ``shared`` lends its workspace."""
-    act, code = _code(kind), _dtype_code(x)
-    x, ldx = _rows(x, "x")
-    w, ldw = _weight(weight, x)
-    tokens, (units, dim) = _tokens(x), w.shape
-    b, device = _bias(bias, units, x), x.device
-    _like(dy, (*x.shape[:-1], units), x, "dy")
+    bias.  (The residual's gradient is dy.)  x may be None where nothing reads it:
+    no activation, and ``need_weight`` False.  ``shared`` lends its workspace."""
+    if x is None and (kind is not None or need_weight):
+        raise ValueError("x must be given with an activation or need_weight")
+    like = dy if x is None else x
+    act, code, lead = _code(kind), _dtype_code(like), like.shape[:-1]
+    if x is not None:
+        x, ldx = _rows(x, "x")
+    w, ldw = _weight(weight, like, None if x is None else x.shape[-1])
+    units, dim = w.shape
+    if x is None:
+        ldx = dim
+    b, device = _bias(bias, units, like), like.device
+    _like(dy, (*lead, units), like, "dy")
     dy, lddy = _rows(dy, "dy")
+    tokens = _tokens(dy)
     if need_bias is None:
         need_bias = b is not None
-    dx = torch.empty(x.shape, dtype=x.dtype, device=device) if need_x else None
-    dw = torch.empty((units, dim), dtype=x.dtype, device=device) if need_weight else None
-    db = torch.empty((units,), dtype=x.dtype, device=device) if need_bias else None
-    aligned = (_lib.LINEAR_ALIGNED_XW * (_aligned(x, ldx) and _aligned(w, ldw))
+    dx = torch.empty((*lead, dim), dtype=like.dtype, device=device) if need_x else None
+    dw = torch.empty((units, dim), dtype=like.dtype, device=device) if need_weight else None
+    db = torch.empty((units,), dtype=like.dtype, device=device) if need_bias else None
+    aligned = (_lib.LINEAR_ALIGNED_XW * ((x is None or _aligned(x, ldx)) and _aligned(w, ldw))
                + _lib.LINEAR_ALIGNED_DY * _aligned(dy, lddy))
     ws, nbytes = _workspace(tokens, dim, units, act, code, 1, aligned, device, shared)
-    launch("linear_bwd", "linear_bwd", device, act, _param_value(kind, param), x.data_ptr(), ldx,
+    launch("linear_bwd", "linear_bwd", device, act, _param_value(kind, param), _ptr(x), ldx,
            w.data_ptr(), ldw, _ptr(b), dy.data_ptr(), lddy, tokens, dim, units, _ptr(dx), dim,
            _ptr(dw), dim, _ptr(db), _ptr(ws), nbytes, code)
     return dx, dw, db
