@@ -37,6 +37,9 @@ struct LinArgs : Product<T> {  // out: y, or dz (columns padded, zeros past p.ro
     int64_t ldr;
     int act;
     Coef coef;
+    // Backward, or NULL (no db): the waves' column sums of dz, a row of out_cols for
+    // each 16 MT tokens (tiles that are no parts); dz in binary32, rows of out_cols.
+    float *db, *wide;
 };
 
 struct IdentityOp {
@@ -83,16 +86,16 @@ __device__ __forceinline__ void with_act(int act, const F& f)
 // ---------------------------------------------------------------------------
 
 // One element of y or dz, written where it belongs: exactly (with the rare
-// branches).  c is below a.out_cols.
+// branches).  c is below a.out_cols.  Its value before the rounding.
 template <typename T, bool BWD>
-__device__ __forceinline__ void lin_one(const LinArgs<T>& a, int64_t m, int c, float z)
+__device__ __forceinline__ float lin_one(const LinArgs<T>& a, int64_t m, int c, float z)
 {
     constexpr bool P = sizeof(T) == 4;
     T* out = a.out[0] + m * a.ldo[0] + c;
     if (c >= a.p.rows) {
         if constexpr (BWD)  // the workspace's rows are padded: zeros past the last unit
             *out = Elem<T>::put(0.0f);
-        return;
+        return 0.0f;
     }
     if (a.bias)
         z += Elem<T>::get(a.bias[c]);
@@ -101,7 +104,33 @@ __device__ __forceinline__ void lin_one(const LinArgs<T>& a, int64_t m, int c, f
         using Op = decltype(op);
         z = BWD ? act_slope<Op, P>(z, r, a.coef) : act_value<Op, P>(z, a.coef);
     });
-    *out = Elem<T>::put(BWD ? z : z + r);
+    if (!BWD)
+        z += r;
+    *out = Elem<T>::put(z);
+    return z;
+}
+
+// lin_one, and dz in binary32 where db's sums read it.
+template <typename T, bool BWD>
+__device__ __forceinline__ void lin_alone(const LinArgs<T>& a, int64_t m, int c, float z)
+{
+    z = lin_one<T, BWD>(a, m, c, z);
+    if (BWD && a.wide)
+        a.wide[m * a.out_cols + c] = z;
+}
+
+// Sum over the 16 lanes of a row, in every one of them.
+__device__ __forceinline__ float sum16(float v)
+{
+#define LIN_ROR(N)                                                                          \
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(                             \
+                                       0, __builtin_bit_cast(int, v), 0x120 + N, 0xf, 0xf, true))
+    LIN_ROR(8);
+    LIN_ROR(4);
+    LIN_ROR(2);
+    LIN_ROR(1);
+#undef LIN_ROR
+    return v;
 }
 
 // Eight values of the bias, zeros past its end and where there is none.
@@ -166,7 +195,8 @@ __device__ __forceinline__ uint32_t lin_results(const LinArgs<T>& a, int64_t m0,
         T* out = a.out[0] + row * a.ldo[0] + c;
         float bias[8];
         load_bias(a.bias, c, a.p.rows, bias);
-each([&](auto part) {
+        float sum[8] = {};
+        each([&](auto part) {
             constexpr int i0 = decltype(part)::value * MH;
             Beside<T, MH, 1> d;
             if (BWD || a.r)
@@ -186,7 +216,8 @@ each([&](auto part) {
                     o[e] = acc[i0 + t][2 * b + e / 4][e % 4] + bias[e];
                 bool met = false;
                 with_act(a.act, [&](auto op) { met = act8<decltype(op), BWD, P>(o, up, a.coef); });
-                rare |= __any(met) ? 1u << ((i0 + t) * (NT / 2) + b) : 0u;
+                const bool again = __any(met);
+                rare |= again ? 1u << ((i0 + t) * (NT / 2) + b) : 0u;
                 if constexpr (!BWD)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -199,6 +230,10 @@ each([&](auto part) {
                             for (int e = 0; e < 8; ++e)
                                 o[e] = e < left ? o[e] : 0.0f;
                         Eight<T>::store(out, o);
+                        if (!again)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                sum[e] += o[e];
                     } else {
                         store_some8(out, o, left);
                     }
@@ -208,6 +243,13 @@ each([&](auto part) {
                 __builtin_amdgcn_sched_barrier(0);  // few results at a time
             }
         }, std::make_integer_sequence<int, MT / MH>());
+        if (BWD && a.db) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum[e] = sum16(sum[e]);
+            if (l % 16 == 0 && c < a.out_cols)
+                Eight<float>::store(a.db + m0 / (16 * MT) * a.out_cols + c, sum);
+        }
     }, std::make_integer_sequence<int, NT / 2>());
     return rare;
 }
@@ -230,12 +272,18 @@ __device__ __forceinline__ void lin_rare(const LinArgs<T>& a, int64_t m0, int n0
                 z = acc[k / NT][k % NT];
         const int64_t m = m0 + l % 16 + 16 * i;
         const int n = n0 + 32 * (j / 2) + 8 * (l / 16) + 4 * (j % 2);
-        if (m >= a.q.rows)
-            continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (n + e < a.out_cols)
-                lin_one<T, BWD>(a, m, n + e, z[e]);
+            z[e] = m < a.q.rows && n + e < a.out_cols ? lin_one<T, BWD>(a, m, n + e, z[e]) : 0.0f;
+        if (BWD && a.db) {
+            // The row's own thread wrote the sum that these belong to.
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v = sum16(z[e]);
+                if (l % 16 == 0 && n + e < a.out_cols)
+                    a.db[m0 / (16 * MT) * a.out_cols + n + e] += v;
+            }
+        }
     }
 }
 
@@ -274,7 +322,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void lin_few_kernel(const LinArgs<T
 {
     few_tokens<T, 1, 1, QT, kFewWaves, 2>(a, [&](int m, int n, const float (&r)[1]) {
         if (n < a.out_cols)
-            lin_one<T, BWD>(a, m, n, r[0]);
+            lin_alone<T, BWD>(a, m, n, r[0]);
     });
 }
 
@@ -295,7 +343,7 @@ __global__ __launch_bounds__(256) void lin_parts_kernel(const LinArgs<T> a)
             p += (int64_t)a.q.rows * a.part_ld;
         }
     }
-    lin_one<T, BWD>(a, m, c, z);
+    lin_alone<T, BWD>(a, m, c, z);
 }
 
 // The parts of a split sum: dx, dW.
@@ -312,7 +360,8 @@ __global__ __launch_bounds__(256) void lin_pack_kernel(const PackArgs<T> a)
 }
 
 // ---------------------------------------------------------------------------
-// db: column sums of dz.  A block takes 64 vectors of columns and a share of the
+// db: column sums of dz before its rounding.  Where the epilogue of tiles does not
+// leave them (or dz is dy) a block takes 64 vectors of columns and a share of the
 // rows, one row a wave; its waves' sums meet in LDS.  A second kernel adds the
 // shares in order.
 // ---------------------------------------------------------------------------
@@ -321,9 +370,13 @@ struct ColArgs {
     const T* d;
     int64_t ld, rows;
     int cols;
-    float* part;  // [shares][cols]
-    int shares;
-    T* out;
+    float* part;  // [shares] rows, part_ld apart
+    int part_ld, shares;
+};
+
+struct ColSums {
+    const float* part;
+    int part_ld, shares, cols;
 };
 
 constexpr int kColUnroll = 8;  // rows of a wave in flight
@@ -368,13 +421,13 @@ __global__ __launch_bounds__(256) void lin_cols_kernel(const ColArgs<T> a)
     for (int c = threadIdx.x; c < 64 * E; c += 256) {
         const int col = blockIdx.x * (64 * E) + c;
         if (col < a.cols)
-            a.part[(int64_t)blockIdx.y * a.cols + col] =
+            a.part[(int64_t)blockIdx.y * a.part_ld + col] =
                 (lds[0][c] + lds[1][c]) + (lds[2][c] + lds[3][c]);
     }
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void lin_col_sum_kernel(const ColArgs<T> a)
+__global__ __launch_bounds__(256) void lin_col_sum_kernel(const ColSums a, T* out)
 {
     __shared__ float lds[8][32];
     const int c = threadIdx.x % 32, k = threadIdx.x / 32;
@@ -382,7 +435,7 @@ __global__ __launch_bounds__(256) void lin_col_sum_kernel(const ColArgs<T> a)
     float s = 0.0f;
     if (col < a.cols)
         for (int p = k; p < a.shares; p += 8)
-            s += a.part[(int64_t)p * a.cols + col];
+            s += a.part[(int64_t)p * a.part_ld + col];
     lds[k][c] = s;
     __syncthreads();
     if (k == 0 && col < a.cols) {
@@ -390,7 +443,7 @@ __global__ __launch_bounds__(256) void lin_col_sum_kernel(const ColArgs<T> a)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             t += lds[i][c];
-        a.out[col] = Elem<T>::put(t);
+        out[col] = Elem<T>::put(t);
     }
 }
 
@@ -501,12 +554,19 @@ int lin_product(LinArgs<T>& a, bool few, int64_t cols, int64_t k, float* part, h
                         : lin_tiles<T, MODE, BWD, 2, 2, 4, 4, false>(a, stream);
 }
 
-// The workspace: dz in padded rows (backward with an activation), the packed
-// operands, the parts of one split sum at a time (or of db's).  Each is whole
-// 128-byte lines long.
+// Rows of the column sums that a wave of tiles leaves, one for its tokens.
+size_t wave_rows(size_t tokens, bool big)
+{
+    const size_t side = big ? 256 : 128;
+    return 2 * ((tokens + side - 1) / side);
+}
+
+// The workspace: dz in padded rows (backward with an activation; in bfloat16 calls
+// of few tokens or a split sum also in binary32, for db), the packed operands, the
+// parts of one split sum at a time (or of db's).  Each is whole 128-byte lines long.
 struct Space {
-    size_t dz, xw, dy, part;
-    size_t bytes() const { return dz + xw + dy + part; }
+    size_t dz, wide, xw, dy, part;
+    size_t bytes() const { return dz + wide + xw + dy + part; }
 };
 
 Space space(size_t tokens, size_t dim, size_t units, bool act, size_t es, bool backward, int align)
@@ -519,12 +579,19 @@ Space space(size_t tokens, size_t dim, size_t units, bool act, size_t es, bool b
     if ((!backward || act) && !few)
         s.part = part_bytes(kLin, m, f, d, es);
     if (backward) {
+        const Plan plan = make_plan(m, f, d, 1, 1, es);
+        const bool alone = act && (few || plan.splits > 1);
+        size_t db = wave_rows(tokens, plan.big) * padded(units);
+        if (!act || alone)
+            db = (size_t)col_shares(m, f, alone ? sizeof(float) : es) * units;
         if (act)
             s.dz = lines(tokens * padded(units) * es);
         else if (!(align & LINEAR_ALIGNED_DY))
             s.dy = tokens * packed_ld(units, es) * es;
+        if (alone && es < sizeof(float))
+            s.wide = tokens * padded(units) * sizeof(float);
         const size_t more[] = {part_bytes(kLinDx, m, d, f, es), part_bytes(kLinDw, f, d, m, es),
-                               (size_t)col_shares(m, f, es) * units * sizeof(float)};
+                               db * sizeof(float)};
         for (size_t v : more)
             s.part = s.part > v ? s.part : v;
     }
@@ -569,21 +636,30 @@ int pack(Rows<T>& a, size_t arows, Rows<T>* b, size_t brows, T* to, hipStream_t 
 }
 
 template <typename T>
-int col_sums(const Rows<T>& d, size_t rows, size_t cols, float* part, T* out, hipStream_t stream)
+int add_shares(const ColSums& a, T* out, hipStream_t stream)
 {
+    if (a.cols == 0)
+        return MESWISH_OK;
+    ColSums sums = a;
+    void* args[] = {&sums, &out};
+    return launch(reinterpret_cast<const void*>(&lin_col_sum_kernel<T>),
+                  dim3((unsigned)((a.cols + 31) / 32)), 256, args, stream);
+}
+
+// The sums of d's columns, in shares.
+template <typename T>
+int col_sums(const Rows<T>& d, size_t rows, size_t cols, float* part, ColSums& sums,
+             hipStream_t stream)
+{
+    const int shares = col_shares((int64_t)rows, (int64_t)cols, sizeof(T));
+    sums = ColSums{part, (int)cols, shares, (int)cols};
     if (cols == 0)
         return MESWISH_OK;
-    ColArgs<T> a{d.p, d.ld, (int64_t)rows, (int)cols, part,
-                 col_shares((int64_t)rows, (int64_t)cols, sizeof(T)), out};
+    ColArgs<T> a{d.p, d.ld, (int64_t)rows, (int)cols, part, (int)cols, shares};
     void* args[] = {&a};
     constexpr int kCols = 64 * Elem<T>::kPerVec;
-    int rc = launch(reinterpret_cast<const void*>(&lin_cols_kernel<T>),
-                    dim3((unsigned)((cols + kCols - 1) / kCols), (unsigned)a.shares), 256, args,
-                    stream);
-    if (rc != MESWISH_OK)
-        return rc;
-    return launch(reinterpret_cast<const void*>(&lin_col_sum_kernel<T>),
-                  dim3((unsigned)((cols + 31) / 32)), 256, args, stream);
+    return launch(reinterpret_cast<const void*>(&lin_cols_kernel<T>),
+                  dim3((unsigned)((cols + kCols - 1) / kCols), (unsigned)shares), 256, args, stream);
 }
 
 // What a call was given, checked.
@@ -610,10 +686,12 @@ int run(const Call& c)
     const bool few = c.few, act = c.act != LINEAR_IDENTITY;
     char* at = c.workspace;
     T* dz = reinterpret_cast<T*>(at);
-    T* xw = reinterpret_cast<T*>(at += c.space.dz);
+    float* wide = reinterpret_cast<float*>(at += c.space.dz);
+    T* xw = reinterpret_cast<T*>(at += c.space.wide);
     T* dy = reinterpret_cast<T*>(at += c.space.xw);
     float* part = reinterpret_cast<float*>(at += c.space.dy);
     int rc = MESWISH_OK;
+    bool summed = false;  // db is there
     // In the backward without an activation x serves dW alone and w dx.
     const bool need_x = !BWD || act || c.dw, need_w = !BWD || act || c.dx;
     if (c.space.xw)
@@ -635,9 +713,23 @@ int run(const Call& c)
         a.out[0] = BWD ? dz : static_cast<T*>(c.y);
         a.ldo[0] = BWD ? fp : c.ldy;
         a.out_cols = BWD ? (int)fp : (int)c.units;
-        rc = lin_product<T, kLin, BWD>(a, few, (int64_t)c.units, (int64_t)c.dim, part, c.stream);
-        if (BWD)
+        if constexpr (BWD) {
+            const Plan plan = make_plan((int64_t)c.tokens, (int64_t)c.units, (int64_t)c.dim, 1, 1,
+                                        sizeof(T));
+            const bool alone = few || plan.splits > 1;
+            if (c.dbias && !alone)
+                a.db = part;
+            else if (c.dbias && c.space.wide)
+                a.wide = wide;
+            rc = lin_product<T, kLin, true>(a, few, (int64_t)c.units, (int64_t)c.dim, part, c.stream);
             d = Rows<T>{dz, fp, (int)fp};
+            if (rc == MESWISH_OK && a.db)
+                rc = add_shares(ColSums{part, (int)fp, (int)wave_rows(c.tokens, plan.big),
+                                        (int)c.units}, static_cast<T*>(c.dbias), c.stream);
+            summed = a.db != nullptr;
+        } else {
+            rc = lin_product<T, kLin, false>(a, few, (int64_t)c.units, (int64_t)c.dim, part, c.stream);
+        }
     } else if (rc == MESWISH_OK && c.space.dy && (c.dx || c.dw)) {
         rc = pack<T>(d, c.tokens, nullptr, 0, dy, c.stream);
     }
@@ -663,8 +755,14 @@ int run(const Call& c)
             a.out_cols = (int)c.dim;
             rc = lin_product<T, kLinDw, false>(a, false, (int64_t)c.dim, (int64_t)c.tokens, part, c.stream);
         }
-        if (rc == MESWISH_OK && c.dbias)
-            rc = col_sums<T>(d, c.tokens, c.units, part, static_cast<T*>(c.dbias), c.stream);
+        if (rc == MESWISH_OK && c.dbias && !summed) {
+            ColSums sums;
+            rc = c.space.wide ? col_sums(Rows<float>{wide, (int64_t)padded(c.units), 0}, c.tokens,
+                                         c.units, part, sums, c.stream)
+                              : col_sums(d, c.tokens, c.units, part, sums, c.stream);
+            if (rc == MESWISH_OK)
+                rc = add_shares(sums, static_cast<T*>(c.dbias), c.stream);
+        }
     }
     return rc;
 }
