@@ -278,7 +278,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackArgs<T> a)
 template <typename T, int MODE>
 __global__ __launch_bounds__(256) void sum_parts_kernel(const GemmArgs<T> a)
 {
-    sum_parts<T, MODE>(a);
+    sum_parts<T, MODE>(a, blockIdx.x);
 }
 
 // g and u, and the unit: one element a thread.

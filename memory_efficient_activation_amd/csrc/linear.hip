@@ -288,11 +288,11 @@ __device__ __forceinline__ void lin_rare(const LinArgs<T>& a, int64_t m0, int n0
 }
 
 template <typename T, int MODE, bool BWD, bool PARTS, int MT, int NT>
-__device__ __forceinline__ void lin_epilogue(const LinArgs<T>& a, int64_t m0, int n0,
+__device__ __forceinline__ void lin_epilogue(const LinArgs<T>& a, int part, int64_t m0, int n0,
                                              const f32x4 (&acc)[MT][NT])
 {
     if constexpr (PARTS) {
-        store_results<MODE == kLin>(a.part + (int64_t)blockIdx.y * a.q.rows * a.part_ld, a.part_ld,
+        store_results<MODE == kLin>(a.part + (int64_t)part * a.q.rows * a.part_ld, a.part_ld,
                                     a.q.rows, a.part_ld, m0, n0, acc);
     } else if constexpr (MODE != kLin) {
         store_results<false>(a.out[0], a.ldo[0], a.q.rows, a.out_cols, m0, n0, acc);
@@ -303,13 +303,46 @@ __device__ __forceinline__ void lin_epilogue(const LinArgs<T>& a, int64_t m0, in
     }
 }
 
+template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, bool PARTS, class Place>
+__device__ __forceinline__ void lin_tiles_of(const LinArgs<T>& a, const Place at)
+{
+    product_tiles<T, MODE, WM, WN, MT, NT, PARTS>(
+        a,
+        [&](int64_t m0, int n0, int, const f32x4 (&acc)[MT][NT]) {
+            lin_epilogue<T, MODE, BWD, PARTS>(a, at.part(), m0, n0, acc);
+        },
+        at);
+}
+
 template <typename T, int MODE, bool BWD, int WM, int WN, int MT, int NT, bool PARTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void lin_tiles_kernel(const LinArgs<T> a)
 {
-    product_tiles<T, MODE, WM, WN, MT, NT, PARTS>(
-        a, [&](int64_t m0, int n0, int, const f32x4 (&acc)[MT][NT]) {
-            lin_epilogue<T, MODE, BWD, PARTS>(a, m0, n0, acc);
-        });
+    lin_tiles_of<T, MODE, BWD, WM, WN, MT, NT, PARTS>(a, OwnPlace());
+}
+
+// dx and dW by one launch, where both are made of 128 x 128 tiles: the blocks of
+// dx, part after part, then those of dW.  (Backward, bf16, against a launch each:
+// 100 x 1000 -> 1000, GELU 25.6 us and 28.2, 500 x 2000 -> 1000 20.1 and 30.0, 2000 x
+// 2048 -> 2048, GELU 85 and 100, 6000 x 1000 -> 1000, GELU 87 and 91.)
+template <typename T>
+struct PairArgs {
+    LinArgs<T> dx, dw;
+    int dx_blocks;
+};
+
+template <typename T, bool DX_PARTS, bool DW_PARTS>
+__global__ __launch_bounds__(256, 2) void lin_pair_kernel(const PairArgs<T> a)
+{
+    const int block = blockIdx.x;
+    if (block < a.dx_blocks) {
+        const int tiles = a.dx.tiles_m * a.dx.tiles_n;
+        lin_tiles_of<T, kLinDx, false, 2, 2, 4, 4, DX_PARTS>(
+            a.dx, GivenPlace{block % tiles, tiles, block / tiles});
+    } else {
+        const int tiles = a.dw.tiles_m * a.dw.tiles_n, b = block - a.dx_blocks;
+        lin_tiles_of<T, kLinDw, false, 2, 2, 4, 4, DW_PARTS>(
+            a.dw, GivenPlace{b % tiles, tiles, b / tiles});
+    }
 }
 
 // 16 units a block, 16 waves with a share of the sum each.  (bf16 1 x 16384 -> 4096,
@@ -338,19 +371,13 @@ __global__ __launch_bounds__(256) void lin_parts_kernel(const LinArgs<T> a)
     float z = 0.0f;
     if (c < a.p.rows) {
         const float* p = a.part + m * a.part_ld + c;
+#pragma unroll 4  // four loads in flight
         for (int s = 0; s < a.splits; ++s) {
             z += *p;
             p += (int64_t)a.q.rows * a.part_ld;
         }
     }
     lin_alone<T, BWD>(a, m, c, z);
-}
-
-// The parts of a split sum: dx, dW.
-template <typename T, int MODE>
-__global__ __launch_bounds__(256) void lin_sum_kernel(const LinArgs<T> a)
-{
-    sum_parts<T, MODE>(a);
 }
 
 template <typename T>
@@ -360,60 +387,66 @@ __global__ __launch_bounds__(256) void lin_pack_kernel(const PackArgs<T> a)
 }
 
 // ---------------------------------------------------------------------------
-// db: column sums of dz before its rounding.  Where the epilogue of tiles does not
-// leave them (or dz is dy) a block takes 64 vectors of columns and a share of the
-// rows, one row a wave; its waves' sums meet in LDS.  A second kernel adds the
-// shares in order.
+// db: column sums of dz before its rounding, and what ends the backward.
+//
+// The epilogue of tiles leaves a row of sums for each wave's tokens; elsewhere (a
+// split sum, few tokens, dy itself) dz's rows are read again, and where they are many
+// first added up to shares: a block takes 64 vectors of columns and a share of the
+// rows, one row a wave, and its waves' sums meet in LDS.  The last launch adds what
+// there is to be added: the parts of dx and dW, and db's rows or shares, 64
+// columns a block.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct ColArgs {
     const T* d;
     int64_t ld, rows;
     int cols;
-    float* part;  // [shares] rows, part_ld apart
-    int part_ld, shares;
+    float* part;  // [shares][cols]
+    int shares;
 };
 
-struct ColSums {
-    const float* part;
-    int part_ld, shares, cols;
-};
+constexpr int kColUnroll = 8;  // rows of a thread in flight
 
-constexpr int kColUnroll = 8;  // rows of a wave in flight
-
+// s += the rows from `row` on, `step` apart, of the vector of columns at e0.
 template <typename T>
-__global__ __launch_bounds__(256) void lin_cols_kernel(const ColArgs<T> a)
+__device__ __forceinline__ void add_rows(const T* d, int64_t ld, int64_t row, int64_t end, int step,
+                                         int e0, int cols, float* s)
 {
     constexpr int E = Elem<T>::kPerVec, U = kColUnroll;
-    __shared__ float lds[4][64 * E];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int e0 = (blockIdx.x * 64 + lane) * E;
-    const int64_t first = a.rows * blockIdx.y / a.shares, end = a.rows * (blockIdx.y + 1) / a.shares;
-    float s[E] = {};
-    if (e0 < a.cols) {
-        int64_t row = first + wave;
-        for (; row + 4 * (U - 1) < end; row += 4 * U) {
-            u32x4 v[U];
+    for (; row + (U - 1) * step < end; row += U * step) {
+        u32x4 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                v[u] = load_chunk(a.d + (row + 4 * u) * a.ld, e0, a.cols);
+        for (int u = 0; u < U; ++u)
+            v[u] = load_chunk(d + (row + u * step) * ld, e0, cols);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float f[E];
-                Elem<T>::unpack(v[u], f);
-#pragma unroll
-                for (int j = 0; j < E; ++j)
-                    s[j] += f[j];
-            }
-        }
-        for (; row < end; row += 4) {
+        for (int u = 0; u < U; ++u) {
             float f[E];
-            Elem<T>::unpack(load_chunk(a.d + row * a.ld, e0, a.cols), f);
+            Elem<T>::unpack(v[u], f);
 #pragma unroll
             for (int j = 0; j < E; ++j)
                 s[j] += f[j];
         }
     }
+    for (; row < end; row += step) {
+        float f[E];
+        Elem<T>::unpack(load_chunk(d + row * ld, e0, cols), f);
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            s[j] += f[j];
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void lin_cols_kernel(const ColArgs<T> a)
+{
+    constexpr int E = Elem<T>::kPerVec;
+    __shared__ float lds[4][64 * E];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int e0 = (blockIdx.x * 64 + lane) * E;
+    const int64_t first = a.rows * blockIdx.y / a.shares, end = a.rows * (blockIdx.y + 1) / a.shares;
+    float s[E] = {};
+    if (e0 < a.cols)
+        add_rows(a.d, a.ld, first + wave, end, 4, e0, a.cols, s);
 #pragma unroll
     for (int j = 0; j < E; ++j)
         lds[wave][lane * E + j] = s[j];
@@ -421,29 +454,53 @@ __global__ __launch_bounds__(256) void lin_cols_kernel(const ColArgs<T> a)
     for (int c = threadIdx.x; c < 64 * E; c += 256) {
         const int col = blockIdx.x * (64 * E) + c;
         if (col < a.cols)
-            a.part[(int64_t)blockIdx.y * a.part_ld + col] =
+            a.part[(int64_t)blockIdx.y * a.cols + col] =
                 (lds[0][c] + lds[1][c]) + (lds[2][c] + lds[3][c]);
     }
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void lin_col_sum_kernel(const ColSums a, T* out)
+struct TailArgs {
+    LinArgs<T> dx, dw;
+    int dx_blocks, dw_blocks;  // 0: nothing to add
+    const void* rows;          // of db's sums
+    int64_t ld, count;
+    int cols;
+    T* db;
+};
+
+// R: the type of db's rows.
+template <typename T, typename R>
+__global__ __launch_bounds__(256) void lin_tail_kernel(const TailArgs<T> a)
 {
-    __shared__ float lds[8][32];
-    const int c = threadIdx.x % 32, k = threadIdx.x / 32;
-    const int col = blockIdx.x * 32 + c;
-    float s = 0.0f;
-    if (col < a.cols)
-        for (int p = k; p < a.shares; p += 8)
-            s += a.part[(int64_t)p * a.part_ld + col];
-    lds[k][c] = s;
-    __syncthreads();
-    if (k == 0 && col < a.cols) {
-        float t = 0.0f;
+    constexpr int E = Elem<R>::kPerVec, kLanes = 64 / E, kGroups = 256 / kLanes;
+    __shared__ float lds[kGroups][64];
+    int block = blockIdx.x;
+    if (block < a.dx_blocks) {
+        sum_parts<T, kLinDx>(a.dx, block);
+        return;
+    }
+    block -= a.dx_blocks;
+    if (block < a.dw_blocks) {
+        sum_parts<T, kLinDw>(a.dw, block);
+        return;
+    }
+    block -= a.dw_blocks;
+    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const int e0 = block * 64 + lane * E;
+    float s[E] = {};
+    if (e0 < a.cols)
+        add_rows(static_cast<const R*>(a.rows), a.ld, group, a.count, kGroups, e0, a.cols, s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            t += lds[i][c];
-        out[col] = Elem<T>::put(t);
+    for (int j = 0; j < E; ++j)
+        lds[group][lane * E + j] = s[j];
+    __syncthreads();
+    const int col = block * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && col < a.cols) {
+        float t = 0.0f;
+        for (int g = 0; g < kGroups; ++g)
+            t += lds[g][threadIdx.x];
+        a.db[col] = Elem<T>::put(t);
     }
 }
 
@@ -523,35 +580,74 @@ int lin_tiles(LinArgs<T>& a, hipStream_t stream)
         return rc;
     void* args[] = {&a};
     if constexpr (MODE == kLin)
-        return launch_over(reinterpret_cast<const void*>(&lin_parts_kernel<T, BWD>),
-                           (int64_t)a.q.rows * a.out_cols, args, stream);
-    else
-        return launch_over(reinterpret_cast<const void*>(&lin_sum_kernel<T, MODE>),
-                           (int64_t)a.q.rows * (a.part_ld / 4), args, stream);
+        rc = launch_over(reinterpret_cast<const void*>(&lin_parts_kernel<T, BWD>),
+                         (int64_t)a.q.rows * a.out_cols, args, stream);
+    return rc;
 }
 
-// few: by the kernel that reads the weight once.  part: memory for the parts of a
-// split sum; k, cols: the length and the columns that the plan (and the size of
-// that memory) goes by.
-template <typename T, int MODE, bool BWD>
-int lin_product(LinArgs<T>& a, bool few, int64_t cols, int64_t k, float* part, hipStream_t stream)
+// How a product is computed, and where the parts of its sum go.
+template <typename T>
+Plan set_plan(LinArgs<T>& a, int mode, int64_t cols, int64_t k, float* part)
 {
-    a.splits = 1;
+    const Plan p = make_plan(a.q.rows, cols, k, 1, 1, sizeof(T));
+    a.splits = p.splits;
+    a.part = part;
+    a.part_ld = (int)part_ld(mode, cols);
+    return p;
+}
+
+template <typename T, bool DX_PARTS, bool DW_PARTS>
+int lin_pair(PairArgs<T>& a, int64_t blocks, hipStream_t stream)
+{
+    void* args[] = {&a};
+    return launch(reinterpret_cast<const void*>(&lin_pair_kernel<T, DX_PARTS, DW_PARTS>),
+                  dim3((unsigned)blocks), 256, args, stream);
+}
+
+// few: by the kernel that reads the weight once.  (The parts of dx and dW are
+// added by the backward's last launch.)
+template <typename T, int MODE, bool BWD>
+int lin_product(LinArgs<T>& a, bool few, const Plan& p, hipStream_t stream)
+{
     if (a.q.rows == 0 || a.out_cols == 0)
         return MESWISH_OK;
     if constexpr (MODE == kLin) {
         if (few)
             return a.q.rows <= 16 ? lin_few<T, BWD, 1>(a, stream) : lin_few<T, BWD, 2>(a, stream);
     }
-    const Plan p = make_plan(a.q.rows, cols, k, 1, 1, sizeof(T));
-    a.splits = p.splits;
-    a.part = part;
-    a.part_ld = (int)part_ld(MODE, cols);
     if (p.big)
         return p.splits > 1 ? lin_tiles<T, MODE, BWD, 2, 4, 8, 4, true>(a, stream)
                             : lin_tiles<T, MODE, BWD, 2, 4, 8, 4, false>(a, stream);
     return p.splits > 1 ? lin_tiles<T, MODE, BWD, 2, 2, 4, 4, true>(a, stream)
                         : lin_tiles<T, MODE, BWD, 2, 2, 4, 4, false>(a, stream);
+}
+
+// dx and dW, either of which may be absent (no out[0]).
+template <typename T>
+int lin_grads(LinArgs<T>& dx, LinArgs<T>& dw, const Plan& px, const Plan& pw, hipStream_t stream)
+{
+    auto tiles = [](LinArgs<T>& a) {
+        a.tiles_m = (a.q.rows + 127) / 128;
+        a.tiles_n = (a.out_cols + 127) / 128;
+        return (int64_t)a.tiles_m * a.tiles_n * a.splits;
+    };
+    if (dx.out[0] && dw.out[0] && !px.big && !pw.big) {
+        const int64_t bx = tiles(dx), bw = tiles(dw);
+        if (bx > 0 && bw > 0 && bx + bw < ((int64_t)1 << 23)) {
+            PairArgs<T> a{dx, dw, (int)bx};
+            if (dx.splits > 1)
+                return dw.splits > 1 ? lin_pair<T, true, true>(a, bx + bw, stream)
+                                     : lin_pair<T, true, false>(a, bx + bw, stream);
+            return dw.splits > 1 ? lin_pair<T, false, true>(a, bx + bw, stream)
+                                 : lin_pair<T, false, false>(a, bx + bw, stream);
+        }
+    }
+    int rc = MESWISH_OK;
+    if (dx.out[0])
+        rc = lin_product<T, kLinDx, false>(dx, false, px, stream);
+    if (rc == MESWISH_OK && dw.out[0])
+        rc = lin_product<T, kLinDw, false>(dw, false, pw, stream);
+    return rc;
 }
 
 // Rows of the column sums that a wave of tiles leaves, one for its tokens.
@@ -561,12 +657,20 @@ size_t wave_rows(size_t tokens, bool big)
     return 2 * ((tokens + side - 1) / side);
 }
 
+// Most rows that db's last launch adds without shares: a block adds 64 columns of
+// them, 16 rows (bfloat16: 32) at a time.  (Backward, bf16, without shares against
+// with them: 300 x 1024 -> 1024, GELU 28.8 us and 31.0, 500 x 2000 -> 1000 20.1 and
+// 22.4, 1000 x 500 -> 1000 25.2 and 25.5, 2000 x 500 -> 500 59.6 and 29.0.)
+constexpr size_t kTailRows = 512;
+
 // The workspace: dz in padded rows (backward with an activation; in bfloat16 calls
 // of few tokens or a split sum also in binary32, for db), the packed operands, the
-// parts of one split sum at a time (or of db's).  Each is whole 128-byte lines long.
+// parts of z's sum or of dx's and dW's, db's sums of waves or its shares.  Each is whole
+// 128-byte lines long.
 struct Space {
-    size_t dz, wide, xw, dy, part;
-    size_t bytes() const { return dz + wide + xw + dy + part; }
+    size_t dz, wide, xw, dy, part, db;
+    size_t dw_part;  // where dW's parts are in `part`
+    size_t bytes() const { return dz + wide + xw + dy + part + db; }
 };
 
 Space space(size_t tokens, size_t dim, size_t units, bool act, size_t es, bool backward, int align)
@@ -577,25 +681,25 @@ Space space(size_t tokens, size_t dim, size_t units, bool act, size_t es, bool b
     if (!(align & LINEAR_ALIGNED_XW) && (backward || !few))
         s.xw = (tokens + units) * packed_ld(dim, es) * es;
     if ((!backward || act) && !few)
-        s.part = part_bytes(kLin, m, f, d, es);
+        s.part = lines(part_bytes(kLin, m, f, d, es));
     if (backward) {
         const Plan plan = make_plan(m, f, d, 1, 1, es);
         const bool alone = act && (few || plan.splits > 1);
-        size_t db = wave_rows(tokens, plan.big) * padded(units);
-        if (!act || alone)
-            db = (size_t)col_shares(m, f, alone ? sizeof(float) : es) * units;
+        if (act && !alone)
+            s.db = wave_rows(tokens, plan.big) * padded(units) * sizeof(float);
+        else
+            s.db = (size_t)col_shares(m, f, alone ? sizeof(float) : es) * units * sizeof(float);
+        s.db = lines(s.db);
         if (act)
             s.dz = lines(tokens * padded(units) * es);
         else if (!(align & LINEAR_ALIGNED_DY))
             s.dy = tokens * packed_ld(units, es) * es;
         if (alone && es < sizeof(float))
             s.wide = tokens * padded(units) * sizeof(float);
-        const size_t more[] = {part_bytes(kLinDx, m, d, f, es), part_bytes(kLinDw, f, d, m, es),
-                               db * sizeof(float)};
-        for (size_t v : more)
-            s.part = s.part > v ? s.part : v;
+        s.dw_part = lines(part_bytes(kLinDx, m, d, f, es));
+        const size_t grads = s.dw_part + lines(part_bytes(kLinDw, f, d, m, es));
+        s.part = s.part > grads ? s.part : grads;
     }
-    s.part = lines(s.part);
     return s;
 }
 
@@ -635,31 +739,43 @@ int pack(Rows<T>& a, size_t arows, Rows<T>* b, size_t brows, T* to, hipStream_t 
                   dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), 256, p, stream);
 }
 
-template <typename T>
-int add_shares(const ColSums& a, T* out, hipStream_t stream)
+// The rows of db's sums: type R, ld elements apart.
+template <typename R>
+struct ColRows {
+    const R* p;
+    int64_t ld, count;
+};
+
+// Shares of the sums of d's columns.
+template <typename R>
+int add_up(const ColRows<R>& d, size_t cols, float* part, ColRows<float>& out, hipStream_t stream)
 {
-    if (a.cols == 0)
-        return MESWISH_OK;
-    ColSums sums = a;
-    void* args[] = {&sums, &out};
-    return launch(reinterpret_cast<const void*>(&lin_col_sum_kernel<T>),
-                  dim3((unsigned)((a.cols + 31) / 32)), 256, args, stream);
+    const int shares = col_shares(d.count, (int64_t)cols, sizeof(R));
+    out = ColRows<float>{part, (int64_t)cols, shares};
+    ColArgs<R> a{d.p, d.ld, d.count, (int)cols, part, shares};
+    void* args[] = {&a};
+    constexpr int kCols = 64 * Elem<R>::kPerVec;
+    return launch(reinterpret_cast<const void*>(&lin_cols_kernel<R>),
+                  dim3((unsigned)((cols + kCols - 1) / kCols), (unsigned)shares), 256, args, stream);
 }
 
-// The sums of d's columns, in shares.
-template <typename T>
-int col_sums(const Rows<T>& d, size_t rows, size_t cols, float* part, ColSums& sums,
+// The backward's last launch, if there is anything left to add.
+template <typename T, typename R>
+int lin_tail(const LinArgs<T>& dx, const LinArgs<T>& dw, const ColRows<R>& rows, size_t cols, T* db,
              hipStream_t stream)
 {
-    const int shares = col_shares((int64_t)rows, (int64_t)cols, sizeof(T));
-    sums = ColSums{part, (int)cols, shares, (int)cols};
-    if (cols == 0)
+    auto blocks = [](const LinArgs<T>& a) {
+        return a.out[0] && a.splits > 1 ? ((int64_t)a.q.rows * (a.part_ld / 4) + 255) / 256 : 0;
+    };
+    const int64_t bx = blocks(dx), bw = blocks(dw), bd = db ? (int64_t)(cols + 63) / 64 : 0;
+    if (bx + bw + bd == 0)
         return MESWISH_OK;
-    ColArgs<T> a{d.p, d.ld, (int64_t)rows, (int)cols, part, (int)cols, shares};
+    if (bx + bw + bd >= ((int64_t)1 << 24))
+        return MESWISH_EINVAL;
+    TailArgs<T> a{dx, dw, (int)bx, (int)bw, rows.p, rows.ld, rows.count, (int)cols, db};
     void* args[] = {&a};
-    constexpr int kCols = 64 * Elem<T>::kPerVec;
-    return launch(reinterpret_cast<const void*>(&lin_cols_kernel<T>),
-                  dim3((unsigned)((cols + kCols - 1) / kCols), (unsigned)shares), 256, args, stream);
+    return launch(reinterpret_cast<const void*>(&lin_tail_kernel<T, R>),
+                  dim3((unsigned)(bx + bw + bd)), 256, args, stream);
 }
 
 // What a call was given, checked.
@@ -684,19 +800,24 @@ int run(const Call& c)
     Rows<T> w{static_cast<const T*>(c.w), c.ldw, (int)c.dim};
     const Rows<T> x_given = x, w_given = w;
     const bool few = c.few, act = c.act != LINEAR_IDENTITY;
+    const int64_t dim = (int64_t)c.dim, units = (int64_t)c.units;
     char* at = c.workspace;
     T* dz = reinterpret_cast<T*>(at);
     float* wide = reinterpret_cast<float*>(at += c.space.dz);
     T* xw = reinterpret_cast<T*>(at += c.space.wide);
     T* dy = reinterpret_cast<T*>(at += c.space.xw);
     float* part = reinterpret_cast<float*>(at += c.space.dy);
+    float* sums = reinterpret_cast<float*>(at += c.space.part);
     int rc = MESWISH_OK;
-    bool summed = false;  // db is there
     // In the backward without an activation x serves dW alone and w dx.
     const bool need_x = !BWD || act || c.dw, need_w = !BWD || act || c.dx;
     if (c.space.xw)
         rc = pack(x, need_x ? c.tokens : 0, &w, need_w ? c.units : 0, xw, c.stream);
     Rows<T> d{static_cast<const T*>(c.r), c.ldr, (int)c.units};
+    // db's rows: dy, dz in binary32 calls, or what the product leaves of dz in binary32.
+    ColRows<T> rows{d.p, d.ld, (int64_t)c.tokens};
+    ColRows<float> wide_rows{};
+    bool of_waves = false;
     if (rc == MESWISH_OK && (!BWD || act)) {
         LinArgs<T> a{};
         const Rows<T>&p = few ? w_given : w, &q = few ? x_given : x;
@@ -713,56 +834,58 @@ int run(const Call& c)
         a.out[0] = BWD ? dz : static_cast<T*>(c.y);
         a.ldo[0] = BWD ? fp : c.ldy;
         a.out_cols = BWD ? (int)fp : (int)c.units;
-        if constexpr (BWD) {
-            const Plan plan = make_plan((int64_t)c.tokens, (int64_t)c.units, (int64_t)c.dim, 1, 1,
-                                        sizeof(T));
-            const bool alone = few || plan.splits > 1;
-            if (c.dbias && !alone)
-                a.db = part;
-            else if (c.dbias && c.space.wide)
+        const Plan plan = set_plan(a, kLin, units, dim, part);
+        if (BWD && c.dbias) {
+            if (!few && plan.splits == 1) {
+                a.db = sums;
+                of_waves = true;
+                wide_rows = ColRows<float>{sums, fp, (int64_t)wave_rows(c.tokens, plan.big)};
+            } else if (c.space.wide) {
                 a.wide = wide;
-            rc = lin_product<T, kLin, true>(a, few, (int64_t)c.units, (int64_t)c.dim, part, c.stream);
+                wide_rows = ColRows<float>{wide, fp, (int64_t)c.tokens};
+            }
+        }
+        rc = lin_product<T, kLin, BWD>(a, few, plan, c.stream);
+        if (BWD) {
             d = Rows<T>{dz, fp, (int)fp};
-            if (rc == MESWISH_OK && a.db)
-                rc = add_shares(ColSums{part, (int)fp, (int)wave_rows(c.tokens, plan.big),
-                                        (int)c.units}, static_cast<T*>(c.dbias), c.stream);
-            summed = a.db != nullptr;
-        } else {
-            rc = lin_product<T, kLin, false>(a, few, (int64_t)c.units, (int64_t)c.dim, part, c.stream);
+            rows = ColRows<T>{dz, fp, (int64_t)c.tokens};
         }
     } else if (rc == MESWISH_OK && c.space.dy && (c.dx || c.dw)) {
         rc = pack<T>(d, c.tokens, nullptr, 0, dy, c.stream);
     }
     if constexpr (BWD) {
-        if (rc == MESWISH_OK && c.dx) {
-            LinArgs<T> a{};
-            a.p = operand<T>(w.p, w.ld, w.p, w.ld, (size_t)w.cols);
-            a.q = operand<T>(d.p, d.ld, d.p, d.ld, c.tokens);
-            a.k = (int)c.units;
-            a.out[0] = static_cast<T*>(c.dx);
-            a.ldo[0] = c.lddx;
-            a.out_cols = (int)c.dim;
-            rc = lin_product<T, kLinDx, false>(a, false, (int64_t)c.dim, (int64_t)c.units, part, c.stream);
+        LinArgs<T> dx{}, dw{};
+        Plan px{}, pw{};
+        if (c.dx) {
+            dx.p = operand<T>(w.p, w.ld, w.p, w.ld, (size_t)w.cols);
+            dx.q = operand<T>(d.p, d.ld, d.p, d.ld, c.tokens);
+            dx.k = (int)c.units;
+            dx.out[0] = static_cast<T*>(c.dx);
+            dx.ldo[0] = c.lddx;
+            dx.out_cols = (int)c.dim;
+            px = set_plan(dx, kLinDx, dim, units, part);
         }
-        if (rc == MESWISH_OK && c.dw) {
-            LinArgs<T> a{};
-            a.p = operand<T>(x.p, x.ld, x.p, x.ld, (size_t)x.cols);
-            a.q = operand<T>(d.p, d.ld, d.p, d.ld, c.units);
-            a.k = (int)c.tokens;
-            a.q_cols = d.cols;
-            a.out[0] = static_cast<T*>(c.dw);
-            a.ldo[0] = c.lddw;
-            a.out_cols = (int)c.dim;
-            rc = lin_product<T, kLinDw, false>(a, false, (int64_t)c.dim, (int64_t)c.tokens, part, c.stream);
+        if (c.dw) {
+            dw.p = operand<T>(x.p, x.ld, x.p, x.ld, (size_t)x.cols);
+            dw.q = operand<T>(d.p, d.ld, d.p, d.ld, c.units);
+            dw.k = (int)c.tokens;
+            dw.q_cols = d.cols;
+            dw.out[0] = static_cast<T*>(c.dw);
+            dw.ldo[0] = c.lddw;
+            dw.out_cols = (int)c.dim;
+            pw = set_plan(dw, kLinDw, dim, (int64_t)c.tokens, part + c.space.dw_part / sizeof(float));
         }
-        if (rc == MESWISH_OK && c.dbias && !summed) {
-            ColSums sums;
-            rc = c.space.wide ? col_sums(Rows<float>{wide, (int64_t)padded(c.units), 0}, c.tokens,
-                                         c.units, part, sums, c.stream)
-                              : col_sums(d, c.tokens, c.units, part, sums, c.stream);
-            if (rc == MESWISH_OK)
-                rc = add_shares(sums, static_cast<T*>(c.dbias), c.stream);
+        if (rc == MESWISH_OK)
+            rc = lin_grads(dx, dw, px, pw, c.stream);
+        T* db = units ? static_cast<T*>(c.dbias) : nullptr;
+        if (rc == MESWISH_OK && db && !of_waves && c.tokens > kTailRows) {
+            const ColRows<float> given = wide_rows;
+            rc = given.p ? add_up(given, c.units, sums, wide_rows, c.stream)
+                         : add_up(rows, c.units, sums, wide_rows, c.stream);
         }
+        if (rc == MESWISH_OK)
+            rc = wide_rows.p ? lin_tail(dx, dw, wide_rows, c.units, db, c.stream)
+                             : lin_tail(dx, dw, rows, c.units, db, c.stream);
     }
     return rc;
 }

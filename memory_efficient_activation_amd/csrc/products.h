@@ -307,11 +307,35 @@ __device__ __forceinline__ void tile_of_block(int id, int tiles_m, int tiles_n, 
 }
 
 // Steps [first, total) of a sum of `total` steps: block row y's share.
-__device__ __forceinline__ void part_of_sum(int splits, int& first, int& total)
+__device__ __forceinline__ void part_of_sum(int splits, int part, int& first, int& total)
 {
-    const int whole = total, y = blockIdx.y;
-    first = (int)((int64_t)whole * y / splits);
-    total = (int)((int64_t)whole * (y + 1) / splits);
+    const int whole = total;
+    first = (int)((int64_t)whole * part / splits);
+    total = (int)((int64_t)whole * (part + 1) / splits);
+}
+
+// A block's place among those of its product: the first of its tiles, how far it
+// steps to the next one, its part of the sums.  In a launch of one product they are
+// read where they are used, which holds no registers; of several, given.
+struct OwnPlace {
+    __device__ static int block() { return blockIdx.x; }
+    __device__ static int blocks() { return gridDim.x; }
+    __device__ static int part() { return blockIdx.y; }
+};
+
+struct GivenPlace {
+    int block_, blocks_, part_;
+    __device__ int block() const { return block_; }
+    __device__ int blocks() const { return blocks_; }
+    __device__ int part() const { return part_; }
+};
+
+// The LDS that tiles are loaded to: the same memory for every product of a kernel.
+template <int BYTES>
+__device__ __forceinline__ char* tile_memory()
+{
+    __shared__ __attribute__((aligned(1024))) char lds[BYTES];
+    return lds;
 }
 
 // ---------------------------------------------------------------------------
@@ -453,8 +477,10 @@ struct FastTile {
 
 // The product of args a (a Product).  finish(m0, n0, plane, acc) ends a wave's
 // tile: its results from row m0 and column n0 (of P's rows, kUp) on.
-template <typename T, int MODE, int WM, int WN, int MT, int NT, bool PARTS, class Args, class Finish>
-__device__ __forceinline__ void product_tiles(const Args& a, const Finish& finish)
+template <typename T, int MODE, int WM, int WN, int MT, int NT, bool PARTS, class Args, class Finish,
+          class Place = OwnPlace>
+__device__ __forceinline__ void product_tiles(const Args& a, const Finish& finish,
+                                              const Place at = Place())
 {
     using F = Form<MODE>;
     constexpr bool PK = F::kPK, QK = F::kQK;
@@ -463,7 +489,7 @@ __device__ __forceinline__ void product_tiles(const Args& a, const Finish& finis
     using QT = FastTile<T, QK, false, BM, WAVES>;
     constexpr int kK = PT::kK, E = Elem<T>::kPerVec, STEPS = KB / 64;
     constexpr int kStage = PT::kBytes + QT::kBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+    char* lds = tile_memory<2 * kStage>();
     const uint32_t lds0 = (uint32_t)(uintptr_t)(MEBLOCK_LDS char*)lds;
 
     const int tiles = a.tiles_m * a.tiles_n * F::kPlanes;
@@ -472,7 +498,7 @@ __device__ __forceinline__ void product_tiles(const Args& a, const Finish& finis
     int first = 0, total = steps == 0 ? 1 : F::kSums * steps;
     const int whole = total;
     if constexpr (PARTS)
-        part_of_sum(a.splits, first, total);
+        part_of_sum(a.splits, at.part(), first, total);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wm = wave / WN * (MT * 16), wn = wave % WN * (NT * 16);
 
@@ -555,11 +581,11 @@ __device__ __forceinline__ void product_tiles(const Args& a, const Finish& finis
         }
     };
     i32x4 rp, rq;
-    int ahead = first, tile_ahead = blockIdx.x;  // the step whose loads come next
+    int ahead = first, tile_ahead = at.block();  // the step whose loads come next
     auto next_step = [&]() {
         if (ahead == total) {
             ahead = first;
-            tile_ahead += gridDim.x;
+            tile_ahead += at.blocks();
         }
         // Past the last tile nothing is read (zeros are written).
         const bool any = tile_ahead < tiles;
@@ -655,7 +681,7 @@ __device__ __forceinline__ void product_tiles(const Args& a, const Finish& finis
     constexpr int BG = 1;
     uint32_t place = 0;
 #pragma unroll 1
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (int tile = at.block(); tile < tiles; tile += at.blocks()) {
         int om, on, op = 0;  // this tile's place in the output
         if constexpr (F::kPlanes == 2) {
             tile_of_block(tile, 2 * a.tiles_m, a.tiles_n, om, on);
@@ -877,17 +903,18 @@ __device__ __forceinline__ void pack_rows(const PackArgs<T>& a)
 // The parts of a split sum, added in order: four columns a thread.
 // ---------------------------------------------------------------------------
 template <typename T, int MODE>
-__device__ __forceinline__ void sum_parts(const Product<T>& a)
+__device__ __forceinline__ void sum_parts(const Product<T>& a, int block)
 {
     constexpr int kPlanes = Form<MODE>::kPlanes;
     const int64_t per_row = a.part_ld / 4, rows = (int64_t)a.q.rows * kPlanes;
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t at = (int64_t)block * 256 + threadIdx.x;
     if (at >= rows * per_row)
         return;
     const int64_t row = at / per_row;
     const int n = (int)(at % per_row) * 4;
     const float* p = a.part + row * a.part_ld + n;
     f32x4 v = f32x4{};
+#pragma unroll 4  // four loads in flight
     for (int s = 0; s < a.splits; ++s)
         v += *reinterpret_cast<const f32x4*>(p + s * rows * a.part_ld);
     const int plane = row >= a.q.rows;
