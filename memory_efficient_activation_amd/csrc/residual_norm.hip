@@ -32,6 +32,7 @@ namespace meblock {
 namespace {
 
 constexpr int C = 8;  // columns of a thread and chunk
+constexpr int kColThreads = 256;  // of the sums over rows by themselves
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
@@ -1107,97 +1108,135 @@ __global__ __launch_bounds__(1024) void rn_bwd_long_kernel(const RnArgs a)
     }
 }
 
-// Wide rows (n > 8192): the sums over rows, 256 threads of eight columns by an
-// item's rows.
-template <typename TS, typename TB, bool POST, bool PRE>
-__global__ __launch_bounds__(256) void rn_cols_kernel(const RnArgs a)
+// Rows whose sums do not fit the registers beside them (n > 8192, or shorter than
+// a chunk: CUT): the sums over rows by themselves, a block 2048 columns of an item's
+// rows, the next row's loads under this one's work.  As in rn_bwd_kernel T0 and T1
+// give three of them.  Bound by HBM: it reads what the rows' kernel read once more
+// (4096 x 16384, bf16: 537 MB).
+template <typename TS, typename TB, bool POST, bool PRE, bool Z, bool CUT>
+__global__ __launch_bounds__(kColThreads, 2) void rn_cols_kernel(const RnArgs a)
 {
     const int n = a.n;
-    const int64_t first = ((int64_t)blockIdx.x * 256 + threadIdx.x) * C;
-    if (first >= n)
+    const int64_t begin = (int64_t)blockIdx.x * (kColThreads * C), own = begin + threadIdx.x * C;
+    if (own >= n)
         return;
-    const int e0 = (int)first;
-    float qw[C], qb[C], gate[C], nw[C];
-    float ag[C], acc[4][C];
-    load_params(a.post_weight, a.wide, e0, n, 1.0f, qw);
-    load_params(a.post_bias, a.wide, e0, n, 0.0f, qb);
-    load_params(a.pre_weight, a.wide, e0, n, 1.0f, nw);
+    const Place at((int)own, CUT ? C : n);
+    // A chunk moved back may begin before the block's columns.
+    const int64_t base = begin > 0 ? begin - C : 0;
+    const int off = CUT ? 0 : (int)(at.col - base);
+    float nw[C], anw[C], anb[C], aqw[C], aqb[C];
+    load_params(a.pre_weight, a.wide, at.col, n, 1.0f, nw);
 #pragma unroll
     for (int j = 0; j < C; ++j)
-        ag[j] = acc[0][j] = acc[1][j] = acc[2][j] = acc[3][j] = 0.0f;
+        anw[j] = anb[j] = aqw[j] = aqb[j] = 0.0f;
+    auto put = [&](void* to, int wide, int64_t index, const float* f) {
+        if constexpr (CUT) {
+            for (int j = 0; j < n; ++j)
+                put_param(to, wide, index + j, f[j]);
+        } else if (!at.none()) {
+            put_params(to, wide, index + at.col, f);
+        }
+    };
     const int64_t items = a.gates * a.shares;
-    const bool use_z = POST || a.dgate;
     for (int64_t index = blockIdx.y; index < items; index += gridDim.y) {
         const Item it = item_of(a, index);
-        load_params(a.gate ? gate_of(a, it.gate) : nullptr, a.wide, e0, n, 1.0f, gate);
-        for (int64_t row = it.first; row < it.end; ++row) {
-            Chunk<TS> ry, rdy;
-            Chunk<TB> rz, rdo;
-            if constexpr (PRE) {
-                ry.load_cut(static_cast<const TS*>(a.x) + row * a.ldx, e0, n);
-                rdo.load_cut(static_cast<const TB*>(a.dout) + row * a.lddout, e0, n);
-            }
-            if (use_z) {
-                if (a.dy_mask)
-                    rdy.load_cut(static_cast<const TS*>(a.dy) + row * a.lddy, e0, n);
-                rz.load_cut(static_cast<const TB*>(a.z) + row * a.ldz, e0, n);
-            }
-            float e[C], h[C];
+        float t0[C], t1[C];
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                e[j] = 0.0f;
-            if (use_z && a.dy_mask)
-                rdy.values(e);
+        for (int j = 0; j < C; ++j)
+            t0[j] = t1[j] = 0.0f;
+        Chunk<TS> ry, rdy;
+        Chunk<TB> rz, rdo;
+        float ym = 0.0f, yr = 0.0f, zm = 0.0f, zr = 0.0f, m1 = 0.0f, m2 = 0.0f;
+        auto one = [&](auto& chunk, const auto* row) {
+            if constexpr (CUT)
+                chunk.load_cut(row, 0, n);
+            else
+                chunk.load(row + base, off);
+        };
+        auto load = [&](int64_t row) {
             if constexpr (PRE) {
-                float c[C];
-                const float yr = a.pre_rstd[row], m1 = a.means[2 * row], m2 = a.means[2 * row + 1];
-                ry.values(h);
-                normalize(h, a.center ? a.pre_mean[row] : 0.0f, yr, e0, n);
-                rdo.values(c);
-#pragma unroll
-                for (int j = 0; j < C; ++j) {
-                    acc[2][j] = fmaf(c[j], h[j], acc[2][j]);
-                    acc[3][j] += c[j];
-                    e[j] = fmaf(yr, (c[j] * nw[j] - m1) - h[j] * m2, e[j]);
+                one(ry, static_cast<const TS*>(a.x) + row * a.ldx);
+                one(rdo, static_cast<const TB*>(a.dout) + row * a.lddout);
+                ym = a.pre_mean[row];
+                yr = a.pre_rstd[row];
+            }
+            if constexpr (Z) {
+                one(rdy, static_cast<const TS*>(a.dy) + row * a.lddy);
+                one(rz, static_cast<const TB*>(a.z) + row * a.ldz);
+                if constexpr (PRE) {
+                    m1 = a.means[2 * row];
+                    m2 = a.means[2 * row + 1];
+                }
+                if constexpr (POST) {
+                    zm = a.post_mean[row];
+                    zr = a.post_rstd[row];
                 }
             }
-            if (!use_z)
-                continue;
-            rz.values(h);
-            if constexpr (POST)
-                normalize(h, a.center ? a.post_mean[row] : 0.0f, a.post_rstd[row], e0, n);
+        };
+        if (it.first < it.end)
+            load(it.first);
+        for (int64_t row = it.first; row < it.end; ++row) {
+            float e[C], h[C], c[C], z[C];
+            if constexpr (Z) {
+                rdy.keep(a.dy_mask);
+                rdy.values(e);
+                rz.values(z);
+            }
+            if constexpr (PRE) {
+                ry.values(h);
+                rdo.values(c);
+            }
+            // (Without center the means' places hold something else.)
+            const float ymean = a.center ? ym : 0.0f, yrstd = yr, zmean = a.center ? zm : 0.0f,
+                        zrstd = zr, mean1 = m1, mean2 = m2;
+            load(row + 1 < it.end ? row + 1 : row);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (PRE)
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                const float t = a.scale * e[j];
-                ag[j] = fmaf(t, POST ? fmaf(h[j], qw[j], qb[j]) : h[j], ag[j]);
-                if constexpr (POST) {
-                    acc[0][j] = fmaf(t * gate[j], h[j], acc[0][j]);
-                    acc[1][j] = fmaf(t, gate[j], acc[1][j]);
+                for (int j = 0; j < C; ++j) {
+                    h[j] = (h[j] - ymean) * yrstd;
+                    anw[j] = fmaf(c[j], h[j], anw[j]);
+                    anb[j] += c[j];
+                    if constexpr (Z)
+                        e[j] = fmaf(yrstd, (c[j] * nw[j] - mean1) - h[j] * mean2, e[j]);
+                }
+            if constexpr (Z)
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    if constexpr (POST)
+                        z[j] = (z[j] - zmean) * zrstd;
+                    t0[j] += e[j];
+                    t1[j] = fmaf(e[j], z[j], t1[j]);
+                }
+        }
+        if constexpr (Z) {
+            float f[C], g[C];
+            if (a.dgate) {
+                load_params(POST ? a.post_weight : nullptr, a.wide, at.col, n, 1.0f, f);
+                load_params(POST ? a.post_bias : nullptr, a.wide, at.col, n, 0.0f, g);
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    f[j] = a.scale * (POST ? fmaf(f[j], t1[j], g[j] * t0[j]) : t1[j]);
+                put(a.gate_part ? static_cast<void*>(a.gate_part) : a.dgate,
+                    a.gate_part ? 1 : a.wide, (a.gate_part ? index : it.gate) * n, f);
+            }
+            if constexpr (POST) {
+                load_params(a.gate ? gate_of(a, it.gate) : nullptr, a.wide, at.col, n, 1.0f, g);
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    aqw[j] = fmaf(a.scale * g[j], t1[j], aqw[j]);
+                    aqb[j] = fmaf(a.scale * g[j], t0[j], aqb[j]);
                 }
             }
         }
-        if (a.dgate)
-#pragma unroll
-            for (int j = 0; j < C; ++j) {
-                if (e0 + j < n) {
-                    if (a.gate_part)
-                        a.gate_part[index * n + e0 + j] = ag[j];
-                    else
-                        put_param(a.dgate, a.wide, it.gate * n + e0 + j, ag[j]);
-                }
-                ag[j] = 0.0f;
-            }
     }
     if (!a.part)
         return;
-    float* part = a.part + (int64_t)blockIdx.y * 4 * n + e0;
+    const float* acc[4] = {aqw, aqb, anw, anb};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (a.dparam[k])
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-                if (e0 + j < n)
-                    part[(int64_t)k * n + j] = acc[k][j];
+            put(a.part, 1, ((int64_t)blockIdx.y * 4 + k) * n, acc[k]);
 }
 
 // The gradients of the parameters (vectors 0 to 3) and of the gate's rows (from
@@ -1264,6 +1303,11 @@ constexpr int kFwdBlocks = 512;
 // Most blocks of the kernels of 1024 threads that loop over what is left: a
 // launch has fewer than 2^32 threads.
 constexpr int64_t kMaxGrid = 1 << 21;
+// Blocks of the sums over rows by themselves, for all columns: two on a CU.  More
+// leave more partial sums to add (backward, both norms, bf16 / binary32: 4096 x 16384
+// 264 / 525 us, of 1024 blocks 287 / 554, of 256 297 / 514; 1000 x 9001 64 / 93, 74 / 104
+// and 65 / 90).
+constexpr int kColBlocks = 512;
 constexpr int kSumsWidth = 8192;   // widest rows whose sums stay in registers
 constexpr int kRowWidth = 16384;   // widest rows that do
 
@@ -1334,7 +1378,7 @@ bool wants_params(const RnArgs& a)
 // most of either that the workspace is for): a share of a gate row's rows to a
 // block; whole gate rows where there are more of them than blocks; and to a group
 // where a block's groups would be idle for the few rows of a gate row.
-void plan_items(RnArgs& a, int64_t groups, int64_t& blocks)
+void plan_items(RnArgs& a, int64_t groups, int64_t& blocks, int64_t parts = kMaxParts)
 {
     a.by_group = groups > 1 && a.gates > 1 && a.gate_rows < 2 * groups;
     if (a.by_group) {
@@ -1342,12 +1386,12 @@ void plan_items(RnArgs& a, int64_t groups, int64_t& blocks)
         blocks = (a.gates + groups - 1) / groups;
     } else {
         const int64_t most = (a.gate_rows + groups - 1) / groups;  // shares with work
-        a.shares = kMaxParts / a.gates;
+        a.shares = parts / a.gates;
         a.shares = a.shares > most ? most : a.shares;
         a.shares = a.shares < 1 ? 1 : a.shares;
         blocks = a.gates * a.shares;
     }
-    blocks = blocks < kMaxParts ? blocks : kMaxParts;
+    blocks = blocks < parts ? blocks : parts;
     if (a.shares == 1 && a.gates > 1)
         a.gate_part = nullptr;  // an item is a whole gate row: its sum is the gradient
     a.parts = (int)blocks;
@@ -1368,29 +1412,30 @@ int bwd_launch(RnArgs& a, hipStream_t stream)
 }
 
 // The sums over rows by themselves.
-template <typename TS, typename TB, bool POST, bool PRE>
+template <typename TS, typename TB, bool POST, bool PRE, bool Z, bool CUT>
 int cols_launch(RnArgs& a, hipStream_t stream)
 {
     if (!a.dgate && !wants_params(a))
         return MESWISH_OK;
-    int64_t blocks;
-    plan_items(a, 1, blocks);
+    const int64_t cols = ((int64_t)a.n + kColThreads * C - 1) / (kColThreads * C);
+    int64_t blocks, parts = kColBlocks / cols;
+    parts = parts < 1 ? 1 : parts < kMaxParts ? parts : kMaxParts;
+    plan_items(a, 1, blocks, parts);
     void* args[] = {&a};
-    const int64_t cols = ((int64_t)a.n + 256 * C - 1) / (256 * C);
-    const int rc = launch(reinterpret_cast<const void*>(&rn_cols_kernel<TS, TB, POST, PRE>),
-                          dim3((unsigned)cols, (unsigned)blocks), 256, args, stream);
+    const int rc = launch(reinterpret_cast<const void*>(&rn_cols_kernel<TS, TB, POST, PRE, Z, CUT>),
+                          dim3((unsigned)cols, (unsigned)blocks), kColThreads, args, stream);
     if (rc != MESWISH_OK || !(wants_params(a) || (a.dgate && a.gate_part)))
         return rc;
     return sums_launch(a, stream);
 }
 
-template <typename TS, typename TB, bool POST, bool PRE>
+template <typename TS, typename TB, bool POST, bool PRE, bool Z, bool CUT>
 int bwd_long(RnArgs& a, hipStream_t stream)
 {
     void* args[] = {&a};
     const int rc = launch(reinterpret_cast<const void*>(&rn_bwd_long_kernel<TS, TB, POST, PRE>),
                           dim3((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)), 1024, args, stream);
-    return rc == MESWISH_OK ? cols_launch<TS, TB, POST, PRE>(a, stream) : rc;
+    return rc == MESWISH_OK ? cols_launch<TS, TB, POST, PRE, Z, CUT>(a, stream) : rc;
 }
 
 template <typename TS, typename TB, bool POST, bool PRE, bool Z>
@@ -1398,7 +1443,7 @@ int bwd_run(RnArgs& a, hipStream_t stream)
 {
     const int n = a.n;
     if (n < C)
-        return bwd_long<TS, TB, POST, PRE>(a, stream);
+        return bwd_long<TS, TB, POST, PRE, Z, true>(a, stream);
     if (n <= 64)
         return bwd_launch<TS, TB, POST, PRE, Z, 8, 1, true>(a, stream);
     if (n <= 256)
@@ -1414,9 +1459,9 @@ int bwd_run(RnArgs& a, hipStream_t stream)
     if (n <= kSumsWidth)
         return bwd_launch<TS, TB, POST, PRE, Z, 1024, 1, true>(a, stream);
     if (n > kRowWidth)
-        return bwd_long<TS, TB, POST, PRE>(a, stream);
+        return bwd_long<TS, TB, POST, PRE, Z, false>(a, stream);
     const int rc = bwd_launch<TS, TB, POST, PRE, Z, 1024, 2, false>(a, stream);
-    return rc == MESWISH_OK ? cols_launch<TS, TB, POST, PRE>(a, stream) : rc;
+    return rc == MESWISH_OK ? cols_launch<TS, TB, POST, PRE, Z, false>(a, stream) : rc;
 }
 
 template <typename TS, typename TB, bool BWD>
