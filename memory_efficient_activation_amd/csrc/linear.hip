@@ -11,8 +11,23 @@
 //   kLinDw  dW:  P = x (n contiguous), Q = dz (m contiguous), k = tokens.
 //
 // dz is written in the tensors' type, also where that is bfloat16: it is the
-// next products' operand, which the matrix cores take in that type.  Without an
-// activation dz is dy, read where it is.
+// next products' operand, which the matrix cores take in that type (half a step,
+// 2^-8 of an element at the most; dx and dW are off by 0.0023 of the norm where one
+// rounding of the result alone gives 0.0017).  db sums it before that rounding.
+// Without an activation dz is dy, read where it is.
+//
+// What bounds it, bf16: 16384 tokens the matrix cores at the clock the power limit
+// leaves (16384 x 16384 -> 4096 with a residual 1.67 to 1.71 ms, 1.29 to 1.32 PFLOP/s,
+// cores 70 % busy; 4096 -> 16384 with GELU 1.77 ms; backward 5.45 ms, 1.21 PFLOP/s of
+// its three products: recomputation 2.07 ms, 52 % busy, as its epilogue reads dy,
+// evaluates f' and writes dz; dx 1.65, dW 1.70); one token HBM (16384 -> 4096, 134 MB:
+// 26.5 us); some hundred tokens the launches one after another, of which the backward
+// has three to five.  Binary32: its matrix instructions, and tiles that leave CUs
+// idle (1500 x 1000 -> 2730: 264 tiles of 128 on 256 CUs, 114 us where a whole number of
+// rounds would take some 60).
+//
+// Two launches are joined where nothing orders them: dx with dW, and whatever is left
+// to be added up at the end.
 
 #include <hip/hip_runtime.h>
 
@@ -585,11 +600,18 @@ int lin_tiles(LinArgs<T>& a, hipStream_t stream)
     return rc;
 }
 
+// Products that share the GPU with dx or dW, for their plans: in binary32 the other
+// of the two counts.  (Backward with both counted and each by itself, binary32: 1500 x
+// 1000 -> 2730, GELU 278 us and 306, 300 x 1024 -> 1024 30 and 35; bf16: 300 x 1024 ->
+// 1024, GELU 32.5 and 28.7, 6000 x 1000 -> 1000, GELU 97.5 and 85, 500 x 2000 -> 1000
+// 19.9 and 20.1.)
+int products_beside(size_t es, bool both) { return both && es == 4 ? 2 : 1; }
+
 // How a product is computed, and where the parts of its sum go.
 template <typename T>
-Plan set_plan(LinArgs<T>& a, int mode, int64_t cols, int64_t k, float* part)
+Plan set_plan(LinArgs<T>& a, int mode, int64_t cols, int64_t k, float* part, int beside = 1)
 {
-    const Plan p = make_plan(a.q.rows, cols, k, 1, 1, sizeof(T));
+    const Plan p = make_plan(a.q.rows, cols, k, beside, 1, sizeof(T));
     a.splits = p.splits;
     a.part = part;
     a.part_ld = (int)part_ld(mode, cols);
@@ -696,8 +718,17 @@ Space space(size_t tokens, size_t dim, size_t units, bool act, size_t es, bool b
             s.dy = tokens * packed_ld(units, es) * es;
         if (alone && es < sizeof(float))
             s.wide = tokens * padded(units) * sizeof(float);
-        s.dw_part = lines(part_bytes(kLinDx, m, d, f, es));
-        const size_t grads = s.dw_part + lines(part_bytes(kLinDw, f, d, m, es));
+        // Whether one of them is wanted or both.
+        auto most = [&](int mode, int64_t rows, int64_t k) {
+            size_t parts = 1;
+            for (const bool both : {false, true}) {
+                const Plan p = make_plan(rows, d, k, products_beside(es, both), 1, es);
+                parts = parts > (size_t)p.splits ? parts : (size_t)p.splits;
+            }
+            return parts > 1 ? lines(parts * rows * part_ld(mode, d) * sizeof(float)) : 0;
+        };
+        s.dw_part = most(kLinDx, m, f);
+        const size_t grads = s.dw_part + most(kLinDw, f, m);
         s.part = s.part > grads ? s.part : grads;
     }
     return s;
@@ -863,7 +894,7 @@ int run(const Call& c)
             dx.out[0] = static_cast<T*>(c.dx);
             dx.ldo[0] = c.lddx;
             dx.out_cols = (int)c.dim;
-            px = set_plan(dx, kLinDx, dim, units, part);
+            px = set_plan(dx, kLinDx, dim, units, part, products_beside(sizeof(T), c.dw));
         }
         if (c.dw) {
             dw.p = operand<T>(x.p, x.ld, x.p, x.ld, (size_t)x.cols);
@@ -873,7 +904,8 @@ int run(const Call& c)
             dw.out[0] = static_cast<T*>(c.dw);
             dw.ldo[0] = c.lddw;
             dw.out_cols = (int)c.dim;
-            pw = set_plan(dw, kLinDw, dim, (int64_t)c.tokens, part + c.space.dw_part / sizeof(float));
+            pw = set_plan(dw, kLinDw, dim, (int64_t)c.tokens, part + c.space.dw_part / sizeof(float),
+                          products_beside(sizeof(T), c.dx));
         }
         if (rc == MESWISH_OK)
             rc = lin_grads(dx, dw, px, pw, c.stream);

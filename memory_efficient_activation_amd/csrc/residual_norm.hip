@@ -16,6 +16,11 @@
 //   * Where the sums over rows do not fit the registers beside the rows
 //     (n > 8192), a kernel of its own takes them, from each row's two means.
 //   * Rows past 16384 values are read again for each pass, one block per row.
+//   * The last chunk of a row is moved back to end with it, so that loads and values
+//     need no mask; a thread's next row is loaded under the work on this one.
+// Measured, both norms, bf16 with binary32 parameters: 16384 x 4096 forward 100 us
+// (5.4 TB/s), backward 182 us (4.4 TB/s, 10 us of it the second launch, which adds
+// 33 MB of partial sums); 1 x 4096 17 us, of which the host's call takes 12.
 
 #include <hip/hip_runtime.h>
 
@@ -355,7 +360,8 @@ __device__ __forceinline__ void row_stats(const RnArgs& a, float (&f)[R][V][C], 
 }
 
 // TS, TB: the stream's type and the branches'.  R rows of a group at a time: their
-// loads in flight together, their sums in one exchange.
+// loads in flight together, their sums in one exchange.  (bf16, both norms, two rows
+// and one: 16384 x 4096 99.7 us and 100.8, 200000 x 128 56.6 and 60.7.)
 template <typename TS, typename TB, bool POST, bool PRE, int G, int V, int R>
 __global__ __launch_bounds__(Block<G>::kThreads, 4) void rn_fwd_kernel(const RnArgs a)
 {
@@ -880,9 +886,8 @@ __global__ __launch_bounds__(Block<G>::kThreads, 4) void rn_bwd_kernel(const RnA
         }
         if constexpr (!(SUMS && Z))
             continue;
-        // What the item's two sums give.  The item's last row may have been the
-        // last row of other groups, not of this one: no barrier is needed, the
-        // sums are the thread's own.
+        // What the item's two sums give: the thread's own, so that no barrier is
+        // needed before them.
         float f[V][C], b[C];
         if (a.dgate) {
 #pragma unroll
@@ -1298,7 +1303,9 @@ __global__ __launch_bounds__(512) void rn_sums_kernel(const RnArgs a)
 // Most blocks of the backward, each with its own partial sums: two of 512
 // threads on a CU.
 constexpr int kMaxParts = 512;
-// Most blocks of the forward, each keeping its columns of the parameters.
+// Most blocks of the forward, each keeping its columns of the parameters.  (512, 256
+// and 1024, bf16: 16384 x 4096 99.7, 106.4 and 101.4 us; 16384 x 1024 25.5, 29.0, 26.4;
+// 200000 x 128 56.6, 70.1, 54.7.)
 constexpr int kFwdBlocks = 512;
 // Most blocks of the kernels of 1024 threads that loop over what is left: a
 // launch has fewer than 2^32 threads.
