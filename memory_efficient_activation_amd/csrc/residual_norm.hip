@@ -19,8 +19,8 @@
 //   * The last chunk of a row is moved back to end with it, so that loads and values
 //     need no mask; a thread's next row is loaded under the work on this one.
 // Measured, both norms, bf16 with binary32 parameters: 16384 x 4096 forward 100 us
-// (5.4 TB/s), backward 182 us (4.4 TB/s, 10 us of it the second launch, which adds
-// 33 MB of partial sums); 1 x 4096 17 us, of which the host's call takes 12.
+// (5.4 TB/s), backward 175 us (4.6 TB/s, with the second launch, which adds 17 MB
+// of partial sums); 1 x 4096 17 us, of which the host's call takes 12.
 
 #include <hip/hip_runtime.h>
 
@@ -1301,7 +1301,7 @@ __global__ __launch_bounds__(512) void rn_sums_kernel(const RnArgs a)
 // ---------------------------------------------------------------------------
 
 // Most blocks of the backward, each with its own partial sums: two of 512
-// threads on a CU.
+// threads on a CU.  (1024, bf16: 16384 x 4096 205 us, 3000 x 2048 39.7 and not 28.4.)
 constexpr int kMaxParts = 512;
 // Most blocks of the forward, each keeping its columns of the parameters.  (512, 256
 // and 1024, bf16: 16384 x 4096 99.7, 106.4 and 101.4 us; 16384 x 1024 25.5, 29.0, 26.4;
@@ -1409,7 +1409,13 @@ int bwd_launch(RnArgs& a, hipStream_t stream)
 {
     int64_t blocks;
     RnArgs b = a;
-    plan_items(b, Block<G>::kGroups, blocks);
+    // Where a block's one row is 32 KB or more (y, z, dy and do), a block a CU has
+    // enough loads in flight and leaves half the partial sums.  (512 and 256 blocks,
+    // both norms: 16384 x 4096 bf16 181 us and 175, 8192 x 8192 197 and 176, 600 x 4096
+    // binary32 38 and 26; 24 KB, 10000 x 3000 bf16, 93 and 108; 36 KB, a binary32
+    // stream, 131 and 135; four rows of 8 KB, 16384 x 1024 bf16, 45 and 49.)
+    const bool wide = Block<G>::kGroups == 1 && a.n * 2 * (sizeof(TS) + sizeof(TB)) >= 32768;
+    plan_items(b, Block<G>::kGroups, blocks, wide ? kMaxParts / 2 : kMaxParts);
     void* args[] = {&b};
     int rc = launch(reinterpret_cast<const void*>(&rn_bwd_kernel<TS, TB, POST, PRE, Z, G, V, SUMS>),
                     dim3((unsigned)blocks), Block<G>::kThreads, args, stream);
