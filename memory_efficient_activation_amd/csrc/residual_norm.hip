@@ -1409,12 +1409,15 @@ int bwd_launch(RnArgs& a, hipStream_t stream)
 {
     int64_t blocks;
     RnArgs b = a;
-    // Where a block's one row is 32 KB or more (y, z, dy and do), a block a CU has
-    // enough loads in flight and leaves half the partial sums.  (512 and 256 blocks,
-    // both norms: 16384 x 4096 bf16 181 us and 175, 8192 x 8192 197 and 176, 600 x 4096
-    // binary32 38 and 26; 24 KB, 10000 x 3000 bf16, 93 and 108; 36 KB, a binary32
-    // stream, 131 and 135; four rows of 8 KB, 16384 x 1024 bf16, 45 and 49.)
-    const bool wide = Block<G>::kGroups == 1 && a.n * 2 * (sizeof(TS) + sizeof(TB)) >= 32768;
+    // Where a block's one row is 32 KB or more of what is read (y and do, z, dy if it
+    // is given), a block a CU has enough loads in flight and leaves half the partial
+    // sums.  (512 and 256 blocks, both norms: 16384 x 4096 bf16 181 us and 175, 8192 x
+    // 8192 197 and 176, 600 x 4096 binary32 38 and 26; 24 KB, 16384 x 4096 bf16 without
+    // dy, 159 and 177, 10000 x 3000 bf16 93 and 108; 36 KB, a binary32 stream, 131 and
+    // 135; four rows of 8 KB, 16384 x 1024 bf16, 45 and 49.)
+    const size_t read = a.n * ((PRE ? sizeof(TS) + sizeof(TB) : 0) + (a.dy_mask ? sizeof(TS) : 0) +
+                               (Z ? sizeof(TB) : 0));
+    const bool wide = Block<G>::kGroups == 1 && read >= 32768;
     plan_items(b, Block<G>::kGroups, blocks, wide ? kMaxParts / 2 : kMaxParts);
     void* args[] = {&b};
     int rc = launch(reinterpret_cast<const void*>(&rn_bwd_kernel<TS, TB, POST, PRE, Z, G, V, SUMS>),
