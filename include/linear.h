@@ -26,9 +26,9 @@
  *     bias and the residual.  f and f' are evaluated on it to 1e-5 in binary32
  *     calls, and to 2^-14 in bfloat16 calls (the activations' shorter paths;
  *     the rounding of the result is 2^-9 to 2^-8 of it).  bfloat16 calls round
- *     dz to bfloat16 for the products and the sum that use it (the matrix cores'
- *     operand type; without an activation dz is dy itself).  Every output is
- *     rounded once, to nearest even.
+ *     dz to bfloat16 for the two products that use it (the matrix cores' operand
+ *     type; without an activation dz is dy itself); db sums it before.  Every
+ *     output is rounded once, to nearest even.
  *   - ld*: elements between the starts of consecutive rows, at least the
  *     row's length and at most LINEAR_MAX_LD; rows are contiguous.  Element
  *     alignment is required.  Rows that do not start on 16-byte boundaries
@@ -36,7 +36,8 @@
  *     to padded ones in the workspace where a product over tiles reads them:
  *     x and w together, and in the backward without an activation dy.
  *   - act, param: as meswish_act_fwd, or LINEAR_IDENTITY for none.
- *   - Results are deterministic: sums have a fixed order, no atomics.
+ *   - Results are deterministic: sums have a fixed order, no atomics.  (In binary32
+ *     the order of dx's and dw's may depend on whether the other is asked for.)
  *   - Limits: tokens < 2^30; dim, units <= LINEAR_MAX_LD.
  *   - An output may not overlap an input, another output or the workspace
  *     (MESWISH_EALIAS; y may not be r either); column ranges of one matrix do

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from memory_efficient_activation_amd import linear, residual
+from oracle import ffn_oracle, finish_oracle as fo
 
 from gpu_util import say
 
@@ -94,3 +95,39 @@ def test_border_of_rows_far_apart():
                                    got[2], gate, (gate, None), (None, None))
     for a, b in zip(g, s):
         assert a is b is None or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", [None, "relu"])
+def test_weight_gradients_over_many_rows(kind):
+    """Sums over 2^21 rows of positive values (past 2^31 elements): a row too many
+    or too few of each thousand would show."""
+    tokens, dim, units = (1 << 21) + 77, 1032, 1032
+    x, dy = rows(tokens, dim, 1).abs_(), rows(tokens, units, 2).abs_()
+    w = torch.rand(units, dim, device=DEV).to(BF16)  # z > 0: relu's slope is 1
+    dw, db = linear.linear_bwd(x, w, dy, None, kind, need_x=False, need_bias=True)[1:]
+    times = torch.tensor([(tokens + 999 - i) // 1000 for i in range(1000)], dtype=torch.float64, device=DEV)
+    few = dy[:1000].double() * times[:, None]
+    want_w, want_b = few.t() @ x[:1000].double(), few.sum(0)
+    # A sum of 2^21 positive terms in any order, then a rounding to bfloat16 (half a
+    # step, 2^-8): at the worst each addition is off by 2^-24 of the sum.
+    for got, want in ((dw, want_w), (db, want_b)):
+        off = float(((got.double() - want) / want).abs().max())
+        say(f"[large] {kind}: {off:.2e}")
+        assert off <= tokens * 2.0 ** -24 + 2.0 ** -8
+
+
+@pytest.mark.parametrize("n", [1024, 16000])
+def test_border_parameters_over_many_rows(n):
+    count = ((1 << 31) // n // 1000 + 1) * 1000
+    x, z = rows(count, n, 1), rows(count, n, 2)
+    gate, pw, pb, nw, nb = (torch.randn(n, device=DEV) for _ in range(5))
+    args = gate, (pw, pb), (nw, nb)
+    y, o, stats = residual.residual_norm_fwd(x, z, *args)
+    g = residual.residual_norm_bwd(y, z, x, o, stats, *args)
+    some = residual.RowStats(*(s[:1000] for s in stats))
+    want, bound = fo.border_backward(y[:1000], z[:1000], x[:1000], o[:1000], some, *args, 1.0, 1.0, True)
+    # Every thousand rows are the same: `times` the sum.  Errors grow with it, and with
+    # the number of additions on the way, rows / 256 + 300 at the most.
+    times, depth = count // 1000, (count // 256 + 300) / (1000 // 256 + 300)
+    for got, v, e in zip(g[2:], want[2:], bound[2:]):
+        assert ffn_oracle.worst(got, v * times, e * times * depth) <= 1

@@ -58,3 +58,29 @@ def test_repeats_and_lent_memory(dtype):
             got = linear.linear_bwd(x, w, dy, b, "gelu", shared=shared)
             assert all(torch.equal(p, q) for p, q in zip(got, want))
             shared.workspace(1, torch.device(DEV)).fill_(255)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", [None, "gelu"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_each_gradient_alone(shape, kind, dtype):
+    """Asked for alone or in pairs, a gradient is what it is among all three: bit for
+    bit in bfloat16, to the order of its sum in binary32."""
+    tokens, dim, units = shape
+    torch.manual_seed(tokens)
+    x, w = torch.randn(tokens, dim, device=DEV).to(dtype), torch.randn(units, dim, device=DEV).to(dtype)
+    b, dy = torch.randn(units, device=DEV).to(dtype), torch.randn(tokens, units, device=DEV).to(dtype)
+    want = linear.linear_bwd(x, w, dy, b, kind)
+    sizes = (units, tokens, tokens)  # of the sums
+    for need in range(8):
+        asked = [bool(need >> i & 1) for i in range(3)]
+        got = linear.linear_bwd(x, w, dy, b, kind, None, *asked)
+        for p, q, on, k in zip(got, want, asked, sizes):
+            assert (p is None) == (not on)
+            if on and dtype is BF16:
+                assert torch.equal(p, q)
+            elif on:
+                # Two orders of a sum of k terms: the norm of the difference is at most
+                # k 2^-24 of the terms', which are not larger than sqrt(k) times the sum's
+                # here (random signs), twice.
+                assert float((p - q).norm()) <= 2 * (k + 2) ** 1.5 * 2.0 ** -24 * float(q.norm())
