@@ -928,7 +928,10 @@ __global__ __launch_bounds__(Block<G>::kThreads, 4) void rn_bwd_kernel(const RnA
                         for (int j = 0; j < C; ++j)
                             post_sums[k][own_slot<G, V>(v) + j] += f[v][j];
                     } else if (a.dparam[k] && !at[v].none()) {
-                        // The thread's own columns of the block's partial sums.
+                        // The thread's own columns of the block's partial sums.  Those
+                        // that a chunk moved back shares are the chunk before's, which
+                        // may be another wave's: each column is added to and written
+                        // by one thread alone.
                         float* p = part + (int64_t)k * n;
                         if (begun) {
                             load_params(p, 1, at[v].col, n, 0.0f, b);
@@ -936,7 +939,14 @@ __global__ __launch_bounds__(Block<G>::kThreads, 4) void rn_bwd_kernel(const RnA
                             for (int j = 0; j < C; ++j)
                                 f[v][j] += b[j];
                         }
-                        store8(p, at[v].col, f[v]);
+                        if (at[v].shared == 0) {
+                            store8(p, at[v].col, f[v]);
+                        } else {
+#pragma unroll
+                            for (int j = 1; j < C; ++j)
+                                if (j >= at[v].shared)
+                                    p[at[v].col + j] = f[v][j];
+                        }
                     }
                 }
             }
