@@ -945,7 +945,13 @@ extern "C" size_t linear_workspace_bytes(size_t tokens, size_t dim, size_t units
         align &= ~LINEAR_ALIGNED_XW;
     if (units * es % 16)
         align &= ~LINEAR_ALIGNED_DY;
-    return space(tokens, dim, units, act != LINEAR_IDENTITY, es, backward != 0, align).bytes();
+    const bool f = act != LINEAR_IDENTITY, bwd = backward != 0;
+    const size_t need = space(tokens, dim, units, f, es, bwd, align).bytes();
+    if (align & LINEAR_ALIGNED_XW || dim * es % 16)
+        return need;
+    // The call's rows may turn out aligned, and few tokens then take a split sum.
+    const size_t other = space(tokens, dim, units, f, es, bwd, align | LINEAR_ALIGNED_XW).bytes();
+    return need > other ? need : other;
 }
 
 extern "C" int linear_fwd(int act, float param, const void* x, size_t ldx, const void* w, size_t ldw,
