@@ -11,7 +11,8 @@ A norm is layer normalization, or with ``center`` False the same without the
 mean (v / sqrt(mean(v^2) + eps)).  The gate is a vector over the last dimension,
 one for all rows or one for each index of x's leading dimensions.  In the manner
 of the memory-efficient activations the backward keeps the stream y (which the
-next block reads anyway), z, and two values a row and norm.
+next block reads anyway; with ``pre``), z (with ``post`` or a learned gate), and two
+values a row and norm.
 
 * ``residual_norm_fwd(x, z, gate, post, pre)`` -> (y, o, RowStats);
 * ``residual_norm_bwd(y, z, dy, do, stats, gate, post, pre)`` -> ResidualNormGrads;
@@ -194,12 +195,16 @@ def _stat(t: torch.Tensor | None, lead, y: torch.Tensor, name: str) -> int:
 def residual_norm_bwd(y: torch.Tensor, z: torch.Tensor, dy: torch.Tensor | None,
                       do: torch.Tensor | None, stats: RowStats, gate: torch.Tensor | None = None,
                       post: Affine | None = None, pre: Affine | None = None, scale: float = 1.0,
-                      skip: float = 1.0, center: bool = True, need_params: bool = True,
+                      skip: float = 1.0, center: bool = True,
+                      need_params: bool | tuple[bool, ...] = True,
                       shared: SharedBuffer | None = None) -> ResidualNormGrads:
     """The gradients from y, z, the statistics the forward returned, dy = dL/dy
     (None, with ``pre``: zeros) and do = dL/do (with ``pre``).  Those of the
-    parameters and of the gate have the parameters' type; with ``need_params``
-    False they are None.  ``shared`` lends the workspace."""
+    parameters and of the gate have the parameters' type.  ``need_params``: whether
+    they are computed, or for each of (gate, post's weight, its bias, pre's weight,
+    its bias); what is not needed is None.  y is read only with ``pre``, z only with
+    ``post`` or for the gate's gradient; elsewhere any tensors like them will do.
+    ``shared`` lends the workspace."""
     code = _dtype_code(y)
     y, rows, n, ldy = as_rows(y, "y")
     branch = _branch(z, y, "z")
@@ -227,15 +232,15 @@ def residual_norm_bwd(y: torch.Tensor, z: torch.Tensor, dy: torch.Tensor | None,
     given = (*(post or (None, None)), *(pre or (None, None)))
     dgate, grads, ptrs = None, [None] * 4, [None] * 4
     if need_params:
-        if gate is not None:
+        need = need_params if isinstance(need_params, tuple) else (True,) * 5
+        if gate is not None and need[0]:
             dgate = torch.empty_like(gate)
-        count = sum(p is not None for p in given)
-        if count:
-            vectors = iter(torch.empty((count, n), dtype=pdtype, device=device).unbind(0))
-            for i, p in enumerate(given):
-                if p is not None:
-                    grads[i] = g = next(vectors)
-                    ptrs[i] = g.data_ptr()
+        wanted = [i for i, p in enumerate(given) if p is not None and need[i + 1]]
+        if wanted:
+            vectors = torch.empty((len(wanted), n), dtype=pdtype, device=device).unbind(0)
+            for i, g in zip(wanted, vectors):
+                grads[i] = g
+                ptrs[i] = g.data_ptr()
     dx, dz = _new_like(y), _new_like(z)
     nbytes = library().residual_norm_workspace_bytes(rows, n, gates)
     ws = (shared or SharedBuffer()).workspace(nbytes, device)
@@ -246,8 +251,10 @@ def residual_norm_bwd(y: torch.Tensor, z: torch.Tensor, dy: torch.Tensor | None,
 
 
 class ResidualNormFn(torch.autograd.Function):
-    """(y, o) keeping y, z and the rows' statistics; y alone without ``pre``.
-    post, pre: whether there is such a norm (its weight and bias may be None)."""
+    """(y, o) keeping what the backward reads: y under the norm behind it, z under the
+    norm before it or for the gate's gradient, and the rows' statistics; y alone
+    without ``pre``.  post, pre: whether there is such a norm (its weight and bias may
+    be None)."""
 
     @staticmethod
     def forward(ctx, x, z, gate, post_weight, post_bias, pre_weight, pre_bias, post, pre, scale,
@@ -256,21 +263,28 @@ class ResidualNormFn(torch.autograd.Function):
         y, o, stats = residual_norm_fwd(
             x, z, gate, (post_weight, post_bias) if post else None,
             (pre_weight, pre_bias) if pre else None, scale, skip, center, eps)
-        ctx.save_for_backward(y, z, gate, post_weight, post_bias, pre_weight, pre_bias, *stats)
-        ctx.args = post, pre, scale, skip, center, shared
+        of_gate = gate is not None and ctx.needs_input_grad[2]
+        ctx.save_for_backward(y if pre else None, z if post or of_gate else None, gate, post_weight,
+                              post_bias, pre_weight, pre_bias, *stats)
+        ctx.args = post, pre, scale, skip, center, shared, z.dtype
         return (y, o) if pre else y
 
     @staticmethod
     @first_order
     def backward(ctx, dy, do=None):
         y, z, gate, qw, qb, nw, nb, *stats = ctx.saved_tensors
-        post, pre, scale, skip, center, shared = ctx.args
+        post, pre, scale, skip, center, shared, branch = ctx.args
         need = ctx.needs_input_grad
         if pre and do is None:
-            do = torch.zeros_like(z)
+            do = torch.zeros(y.shape, dtype=branch, device=y.device)
+        # What was not kept is not read: its gradient is a tensor like it.
+        if y is None:
+            y = dy = dy.contiguous()
+        if z is None:
+            z = do = do.contiguous()
         g = residual_norm_bwd(y, z, dy, do, RowStats(*stats), gate, (qw, qb) if post else None,
-                              (nw, nb) if pre else None, scale, skip, center, any(need[2:7]),
-                              shared)
+                              (nw, nb) if pre else None, scale, skip, center,
+                              any(need[2:7]) and need[2:7], shared)
         return (*(v if n else None for v, n in zip(g, need)), *[None] * 7)
 
 
