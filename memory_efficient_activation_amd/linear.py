@@ -3,7 +3,8 @@
 y = residual + f(x W^T + bias), f any activation of the family or none, bias and
 residual optional.  One kernel computes the product and what follows it; in the
 manner of the memory-efficient activations the backward keeps x alone and
-computes the product under f' again (without an activation it needs none).
+computes the product under f' again (without an activation it needs none, nor x
+unless the weight has a gradient).
 
 * ``linear_fwd(x, weight, bias, residual, kind, param)`` -> y;
 * ``linear_bwd(x, weight, dy, bias, kind, param)`` -> (dx, dweight, dbias);
@@ -153,11 +154,13 @@ def linear_bwd(x: torch.Tensor | None, weight: torch.Tensor, dy: torch.Tensor,
 
 
 class LinearFn(torch.autograd.Function):
-    """residual + f(x W^T + bias) keeping x (and references to the parameters)."""
+    """residual + f(x W^T + bias) keeping x, where an activation or the weight's
+    gradient reads it (and references to the parameters)."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, residual, kind, param, shared):
-        ctx.save_for_backward(x, weight, bias)
+        reads_x = kind is not None or ctx.needs_input_grad[1]
+        ctx.save_for_backward(x if reads_x else None, weight, bias)
         ctx.kind, ctx.param, ctx.shared = kind, param, shared
         return linear_fwd(x, weight, bias, residual, kind, param, shared=shared)
 
