@@ -266,17 +266,19 @@ class ResidualNormFn(torch.autograd.Function):
         of_gate = gate is not None and ctx.needs_input_grad[2]
         ctx.save_for_backward(y if pre else None, z if post or of_gate else None, gate, post_weight,
                               post_bias, pre_weight, pre_bias, *stats)
-        ctx.args = post, pre, scale, skip, center, shared, z.dtype
+        ctx.args = post, pre, scale, skip, center, shared, x.dtype, z.dtype
         return (y, o) if pre else y
 
     @staticmethod
     @first_order
     def backward(ctx, dy, do=None):
         y, z, gate, qw, qb, nw, nb, *stats = ctx.saved_tensors
-        post, pre, scale, skip, center, shared, branch = ctx.args
+        post, pre, scale, skip, center, shared, stream, branch = ctx.args
         need = ctx.needs_input_grad
         if pre and do is None:
             do = torch.zeros(y.shape, dtype=branch, device=y.device)
+        if not pre and dy is None:
+            dy = torch.zeros(z.shape, dtype=stream, device=z.device)
         # What was not kept is not read: its gradient is a tensor like it.
         if y is None:
             y = dy = dy.contiguous()
