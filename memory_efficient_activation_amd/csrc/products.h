@@ -1015,7 +1015,7 @@ inline int launch_tiles(Args& a, const void* fn, int bm, int bn, int planes, int
     if (tiles == 0)
         return MESWISH_OK;
     const int64_t grid = resident && tiles > resident ? resident : tiles;
-    if (tiles > ((int64_t)1 << 30) || grid >= ((int64_t)1 << 23))
+    if (tiles > ((int64_t)1 << 30) || grid * block >= (int64_t)1 << 32)
         return MESWISH_EINVAL;
     void* args[] = {&a};
     return launch(fn, dim3((unsigned)grid, a.splits), block, args, stream);
