@@ -22,6 +22,7 @@ from __future__ import annotations
 import torch
 import torch.nn as nn
 
+from . import residual
 from ._autograd import first_order
 from .dense import EPS, SharedBuffer
 from .ffn import gated_ffn_bwd, gated_ffn_fwd
@@ -60,10 +61,17 @@ class PreNormFeedForwardFn(torch.autograd.Function):
         if need_first:
             dn, dw1, db1 = linear_bwd(n, w1, da, b1, ctx.kind, ctx.param, need_norm, need[3],
                                       need[4], shared=shared)
-        if need_norm:
-            dx, dw, db = layer_norm_bwd(x, dn, mean, rstd, weight, need[1] or need[2],
-                                        shared=shared)
-            dx = dx.add_(dy) if need[0] else None
+            del da
+        if need[0]:
+            # The border behind y = x: dy and the norm's share are added in binary32 and
+            # rounded once.
+            g = residual.residual_norm_bwd(x, dn, dy, dn, residual.RowStats(None, None, mean, rstd),
+                                           pre=(weight, bias),
+                                           need_params=(False, False, False, need[1], need[2]),
+                                           shared=shared)
+            dx, dw, db = g.dx, g.dpre_weight, g.dpre_bias
+        elif need_norm:  # reads no dy, and writes a map less
+            dw, db = layer_norm_bwd(x, dn, mean, rstd, weight, shared=shared)[1:]
         grads = (dx, dw, db, dw1, db1, dw2, db2)
         return (*(g if wanted else None for g, wanted in zip(grads, need)), None, None, None, None)
 
