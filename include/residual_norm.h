@@ -24,7 +24,8 @@
  *     dw_pre = sum do yhat, db_pre = sum do, dw_post = sum q zhat, db_post = sum q
  *
  * In the manner of the memory-efficient activations the backward keeps the
- * stream y, which the next block reads anyway, z, and two values a row and norm.
+ * stream y, which the next block reads anyway (with pre), z (with post or for
+ * dgate), and two values a row and norm.
  *
  * Conventions (as in meswish.h): device pointers owned by the caller, no
  * allocation or synchronisation, asynchronous on `stream` (a hipStream_t,

@@ -22,9 +22,10 @@
 // its three products: recomputation 2.07 ms, 52 % busy, as its epilogue reads dy,
 // evaluates f' and writes dz; dx 1.65, dW 1.70); one token HBM (16384 -> 4096, 134 MB:
 // 26.5 us); some hundred tokens the launches one after another, of which the backward
-// has three to five.  Binary32: its matrix instructions, and tiles that leave CUs
-// idle (1500 x 1000 -> 2730: 264 tiles of 128 on 256 CUs, 114 us where a whole number of
-// rounds would take some 60).
+// has three to five.  Binary32: its matrix instructions, and counts of tiles just past
+// the CUs' (1500 x 1000 -> 2730, 264 tiles of 128 on 256 CUs: in two parts, 528 blocks of
+// half the sum and a second launch that reads 33 MB of parts, 115 us; whole, 135; 1536 x
+// 1000 -> 2688, 252 tiles, 80).
 //
 // Two launches are joined where nothing orders them: dx with dW, and whatever is left
 // to be added up at the end.
@@ -193,7 +194,11 @@ __device__ __forceinline__ bool act8(float* z, const float* up, const Coef& k)
 // which a lane met a rare argument: lin_rare does those again, to the same places
 // (which is why y may not be the residual).  (bf16 16384 x 4096 -> 16384, GELU
 // forward: z of standard deviation 1, where it is never needed, 1.68 ms; 1.4, where one
-// vector in ten thousand is, 1.72 against 2.12 with whole waves done again.)
+// vector in ten thousand is, 1.72 against 2.12 with whole waves done again; 1.8 1.99,
+// 2.1 2.52, and from 2.5 on, where most vectors are, 2.8 to 3.0; the backward then 7.3 to
+// 7.5 and not 5.4.  Tanh-GELU the same from a standard deviation of 3 and 4 on, Swish not
+// up to 6.  Binary32 4096 x 2048 -> 4096, GELU forward 0.50 to 0.60 ms, backward 2.39 to
+// 2.49.)
 template <typename T, bool BWD, int MT, int NT>
 __device__ __forceinline__ uint32_t lin_results(const LinArgs<T>& a, int64_t m0, int n0,
                                          const f32x4 (&acc)[MT][NT])

@@ -19,8 +19,10 @@
 //   * The last chunk of a row is moved back to end with it, so that loads and values
 //     need no mask; a thread's next row is loaded under the work on this one.
 // Measured, both norms, bf16 with binary32 parameters: 16384 x 4096 forward 100 us
-// (5.4 TB/s), backward 175 us (4.6 TB/s, with the second launch, which adds 17 MB
-// of partial sums); 1 x 4096 17 us, of which the host's call takes 12.
+// (5.4 TB/s), backward 175 us (4.6 TB/s, with the second launch, which adds the partial
+// sums: 17 MB of the norms', with a gate 21); 1 x 4096 17 us, of which the host's call
+// takes 12.  Rows of 65 to 128 values leave half or more of their 32 lanes without
+// columns (200000 x 128 forward 57 us, 3.6 TB/s).
 
 #include <hip/hip_runtime.h>
 
@@ -1423,8 +1425,9 @@ int bwd_launch(RnArgs& a, hipStream_t stream)
     // is given), a block a CU has enough loads in flight and leaves half the partial
     // sums.  (512 and 256 blocks, both norms: 16384 x 4096 bf16 181 us and 175, 8192 x
     // 8192 197 and 176, 600 x 4096 binary32 38 and 26; 24 KB, 16384 x 4096 bf16 without
-    // dy, 159 and 177, 10000 x 3000 bf16 93 and 108; 36 KB, a binary32 stream, 131 and
-    // 135; four rows of 8 KB, 16384 x 1024 bf16, 45 and 49.)
+    // dy, 159 and 177, 10000 x 3000 bf16 93 and 108; four rows of 8 KB, 16384 x 1024 bf16,
+    // 45 and 49.  At 36 KB, 10000 x 3000 beside a binary32 stream, the rule costs 3 %: 131
+    // and 135.)
     const size_t read = a.n * ((PRE ? sizeof(TS) + sizeof(TB) : 0) + (a.dy_mask ? sizeof(TS) : 0) +
                                (Z ? sizeof(TB) : 0));
     const bool wide = Block<G>::kGroups == 1 && read >= 32768;
