@@ -233,6 +233,8 @@ def residual_norm_bwd(y: torch.Tensor, z: torch.Tensor, dy: torch.Tensor | None,
     dgate, grads, ptrs = None, [None] * 4, [None] * 4
     if need_params:
         need = need_params if isinstance(need_params, tuple) else (True,) * 5
+        if len(need) != 5:
+            raise ValueError(f"need_params names five gradients, got {len(need)}")
         if gate is not None and need[0]:
             dgate = torch.empty_like(gate)
         wanted = [i for i, p in enumerate(given) if p is not None and need[i + 1]]

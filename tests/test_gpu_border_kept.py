@@ -50,6 +50,9 @@ def test_some_of_the_parameters():
         some = residual.residual_norm_bwd(y, z, dy, do, stats, need_params=need, **args)
         for g, want, on in zip(some, whole, (True, True, *need)):
             assert torch.equal(g, want) if on else g is None
+    for need in ((True,) * 4, (False,) * 6):
+        with pytest.raises(ValueError, match="five"):
+            residual.residual_norm_bwd(y, z, dy, do, stats, need_params=need, **args)
 
 
 def test_stack_without_a_norm_of_the_branch():
